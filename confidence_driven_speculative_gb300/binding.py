@@ -46,6 +46,21 @@ class DsparkStep(ctypes.Structure):
     ]
 
 
+class DsparkAttn(ctypes.Structure):
+    """Mirror of ``struct dspark_attn`` (same field order and C types)."""
+    _fields_ = (
+        [(n, ctypes.c_int32) for n in (
+            "B", "rows", "q_max", "Hq", "Hkv", "D", "dtype", "page_size", "num_pages",
+            "max_pages", "rot_dim", "interleaved", "window")]
+        + [("scale", ctypes.c_float)]
+        + [(n, ctypes.c_int64) for n in (
+            "q_stride", "k_stride", "v_stride", "page_stride", "slot_stride", "head_stride")]
+        + [(n, _P) for n in (
+            "q", "k", "v", "q_rot", "k_rot", "k_cache", "v_cache", "row_off", "row_req",
+            "packed_pos", "seq_lens", "block_table", "rope_freq", "out", "workspace")]
+        + [("workspace_bytes", ctypes.c_size_t)])
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -80,6 +95,12 @@ def load():
         lib.dspark_verify_cap_accept.restype = ctypes.c_int
         lib.dspark_verify_noalloc.argtypes = [SP, ctypes.c_int32, _P, _P]
         lib.dspark_verify_noalloc.restype = ctypes.c_int
+        for name in ("dspark_rope_append", "dspark_step_attention", "dspark_prompt_attention"):
+            fn = getattr(lib, name)
+            fn.argtypes = [ctypes.POINTER(DsparkAttn), _P]
+            fn.restype = ctypes.c_int
+        lib.dspark_attn_workspace_size.argtypes = [ctypes.c_int32] * 4
+        lib.dspark_attn_workspace_size.restype = ctypes.c_size_t
         lib.dspark_workspace_size.argtypes = [ctypes.c_int32] * 4
         lib.dspark_workspace_size.restype = ctypes.c_size_t
         lib.dspark_workspace_init.argtypes = [_P, ctypes.c_size_t, _P]
@@ -111,7 +132,7 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
-def _call(name: str, step: DsparkStep, stream, check: bool) -> int:
+def _call(name: str, step, stream, check: bool) -> int:
     rc = getattr(load(), name)(ctypes.byref(step), _stream(stream))
     if check and rc != DSPARK_OK:
         raise DsparkError(rc, name)
@@ -182,6 +203,25 @@ def dspark_fit_sts_tau(conf, tau_used, L, accept_len, tau_out, tau_min: float = 
     if check and rc != DSPARK_OK:
         raise DsparkError(rc, "dspark_fit_sts_tau")
     return rc
+
+
+def dspark_rope_append(attn: DsparkAttn, stream=None, check: bool = True) -> int:
+    """Rotates q and k by the rows' positions and appends k and v to the paged cache."""
+    return _call("dspark_rope_append", attn, stream, check)
+
+
+def dspark_step_attention(attn: DsparkAttn, stream=None, check: bool = True) -> int:
+    """The step's packed rows attend over the paged cache."""
+    return _call("dspark_step_attention", attn, stream, check)
+
+
+def dspark_prompt_attention(attn: DsparkAttn, stream=None, check: bool = True) -> int:
+    """Whole prompts, packed one after the other, attend to themselves causally."""
+    return _call("dspark_prompt_attention", attn, stream, check)
+
+
+def dspark_attn_workspace_size(Hq: int, Hkv: int, D: int, q_max: int) -> int:
+    return int(load().dspark_attn_workspace_size(Hq, Hkv, D, q_max))
 
 
 DSPARK_NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -350,3 +390,138 @@ class StepBuffers:
 
     def device_status(self, stream=None) -> int:
         return dspark_read_device_status(self.workspace.data_ptr(), stream)
+
+
+def rope_freq(rot_dim: int, theta: float = 10000.0, inv_freq=None, device="cuda"):
+    """The ``rope_freq`` array of :class:`DsparkAttn`: an int64 tensor of
+    rot_dim / 2 frequencies in 2^-64 of a turn per position, from
+    theta^(-2i/rot_dim) or from ``inv_freq`` (radians per position, in any
+    scaling of the context; a sequence of rot_dim / 2 floats)."""
+    import math
+
+    import torch
+    if inv_freq is None:
+        inv_freq = [theta ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+    inv_freq = [float(f) for f in inv_freq]
+    if len(inv_freq) != rot_dim // 2:
+        raise ValueError(f"inv_freq must have {rot_dim // 2} entries, got {len(inv_freq)}")
+    turns = [int(round(math.ldexp(f / (2.0 * math.pi), 64))) % (1 << 64) for f in inv_freq]
+    signed = [t - (1 << 64) if t >= 1 << 63 else t for t in turns]
+    return torch.tensor(signed, dtype=torch.int64, device=device)
+
+
+class AttnBuffers:
+    """The ``dspark_attn`` struct of one batch shape, with the outputs and the
+    workspace that it points at.  Inputs are attached with :meth:`bind`."""
+
+    def __init__(self, B: int, rows: int, q_max: int, Hq: int, Hkv: int, D: int,
+                 page_size: int = 64, num_pages: int = 0, max_pages: int = 0, rot_dim: int = 0,
+                 interleaved: bool = False, scale: Optional[float] = None, window: int = 0,
+                 k_rot: bool = False, prompt: bool = False, device="cuda", stream=None):
+        """``k_rot``: dspark_rope_append also writes the rotated keys in packed
+        order (what dspark_prompt_attention reads).  ``prompt``: no cache is
+        used, and page_size, num_pages and max_pages stay 0."""
+        import torch
+        self.q_rot = torch.zeros((rows, Hq, D), dtype=torch.bfloat16, device=device)
+        self.k_rot = (torch.zeros((rows, Hkv, D), dtype=torch.bfloat16, device=device)
+                      if k_rot else None)
+        self.out = torch.zeros((rows, Hq, D), dtype=torch.bfloat16, device=device)
+        self.ws_bytes = dspark_attn_workspace_size(Hq, Hkv, D, q_max)
+        if self.ws_bytes == 0:
+            raise ValueError("shape outside the library's limits")
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        dspark_workspace_init(self.workspace.data_ptr(), self.ws_bytes, stream)
+        self.attn = a = DsparkAttn()
+        a.B, a.rows, a.q_max, a.Hq, a.Hkv, a.D = B, rows, q_max, Hq, Hkv, D
+        a.dtype = DSPARK_BF16
+        if not prompt:
+            a.page_size, a.num_pages, a.max_pages = page_size, num_pages, max_pages
+        a.rot_dim, a.interleaved, a.window = rot_dim, int(bool(interleaved)), window
+        a.scale = D ** -0.5 if scale is None else scale
+        a.q_rot, a.k_rot, a.out = _ptr(self.q_rot), _ptr(self.k_rot), _ptr(self.out)
+        a.workspace, a.workspace_bytes = self.workspace.data_ptr(), self.ws_bytes
+        self._keep = {}
+
+    def bind(self, q=None, k=None, v=None, q_rot=None, k_rot=None, k_cache=None, v_cache=None,
+             row_off=None, row_req=None, packed_pos=None, seq_lens=None, block_table=None,
+             rope_freq=None) -> "AttnBuffers":
+        """Point the struct at device tensors.  q, k, v: [rows, heads, D] with
+        contiguous heads (views of one projection's output are fine).  q_rot,
+        k_rot: contiguous, in place of the buffers' own.  k_cache, v_cache:
+        [num_pages, page_size, Hkv, D] views of any strides, both alike.
+        What is left out stays NULL; the library checks what each call needs."""
+        import torch
+        a = self.attn
+        bf16 = torch.bfloat16
+        for name, heads in (("q", a.Hq), ("k", a.Hkv), ("v", a.Hkv)):
+            t = locals()[name]
+            if t is not None:
+                _device_view(t, name, bf16, (a.rows, heads, a.D))
+                if (heads > 1 and t.stride(1) != a.D) or t.stride(2) != 1:
+                    raise ValueError(f"the heads of {name} must be contiguous")
+                row = t.stride(0) if a.rows > 1 else heads * a.D
+                setattr(a, name + "_stride", row)
+            setattr(a, name, _ptr(t))
+        for name, heads in (("q_rot", a.Hq), ("k_rot", a.Hkv)):
+            t = locals()[name]
+            if t is not None:
+                _device_view(t, name, bf16, (a.rows, heads, a.D))
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+                setattr(self, name, t)
+                setattr(a, name, _ptr(t))
+        if k_cache is not None or v_cache is not None:
+            if k_cache is None or v_cache is None:
+                raise ValueError("k_cache and v_cache come together")
+            shape = (a.num_pages, a.page_size, a.Hkv, a.D)
+            _device_view(k_cache, "k_cache", bf16, shape)
+            _device_view(v_cache, "v_cache", bf16, shape)
+            st = _cache_strides(k_cache)
+            if st != _cache_strides(v_cache):
+                raise ValueError("k_cache and v_cache must have the same strides")
+            if st[3] != 1:
+                raise ValueError("the entries of k_cache must be contiguous")
+            a.page_stride, a.slot_stride, a.head_stride = st[:3]
+        a.k_cache, a.v_cache = _ptr(k_cache), _ptr(v_cache)
+        for name, t, n in (("row_off", row_off, a.B + 1), ("row_req", row_req, a.rows),
+                           ("packed_pos", packed_pos, a.rows), ("seq_lens", seq_lens, a.B),
+                           ("block_table", block_table, a.B * a.max_pages)):
+            _device_array(t, name, "int32", n, optional=True)
+            setattr(a, name, _ptr(t))
+        if rope_freq is not None:
+            _device_view(rope_freq, "rope_freq", torch.int64, (a.rot_dim // 2,))
+            if not rope_freq.is_contiguous():
+                raise ValueError("rope_freq must be contiguous")
+        a.rope_freq = _ptr(rope_freq)
+        self._keep = dict(q=q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, row_off=row_off,
+                          row_req=row_req, packed_pos=packed_pos, seq_lens=seq_lens,
+                          block_table=block_table, rope_freq=rope_freq)
+        return self
+
+    def device_status(self, stream=None) -> int:
+        return dspark_read_device_status(self.workspace.data_ptr(), stream)
+
+
+def _device_view(t, name: str, dtype, shape) -> None:
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be CUDA device memory")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _cache_strides(t) -> tuple:
+    """Strides of a [pages, slots, heads, D] view; those of axes of length 1,
+    which torch leaves open, as the packed ones."""
+    st = list(t.stride())
+    if t.shape[2] == 1:
+        st[2] = t.shape[3]
+    if t.shape[1] == 1:
+        st[1] = t.shape[2] * t.shape[3]
+    if t.shape[0] == 1:
+        st[0] = max(t.shape[1] * st[1], t.shape[2] * st[2])
+    return tuple(st)

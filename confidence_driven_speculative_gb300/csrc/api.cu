@@ -10,6 +10,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "attn.cuh"
 #include "dspark_internal.cuh"
 #include "sts_fit.cuh"
 
@@ -613,3 +614,157 @@ extern "C" dspark_status dspark_verify_noalloc(const dspark_step *s, int32_t res
     }
     return DSPARK_OK;
 }
+
+// ---------------------------------------------------------------------------
+// The attention calls (rope_append.cu, step_attention.cu, prompt_attention.cu).
+// ---------------------------------------------------------------------------
+namespace {
+
+dspark_status check_attn(const dspark_attn *a, const char *fn) {
+    if (!a) return fail(DSPARK_EINVAL, "%s: attn is NULL", fn);
+    if (a->B < 0 || a->B > DSPARK_MAX_B)
+        return fail(DSPARK_EINVAL, "%s: B=%d outside [0, %d]", fn, a->B, DSPARK_MAX_B);
+    if (a->rows < 0 || a->rows > DSPARK_MAX_ROWS)
+        return fail(DSPARK_EINVAL, "%s: rows=%d outside [0, %d]", fn, a->rows, DSPARK_MAX_ROWS);
+    if (a->q_max < 1) return fail(DSPARK_EINVAL, "%s: q_max=%d < 1", fn, a->q_max);
+    if (a->Hq < 1 || a->Hq > DSPARK_MAX_HEADS || a->Hkv < 1 || a->Hkv > a->Hq || a->Hq % a->Hkv)
+        return fail(DSPARK_EINVAL, "%s: Hq=%d, Hkv=%d (Hq <= %d, a multiple of Hkv)", fn, a->Hq,
+                    a->Hkv, DSPARK_MAX_HEADS);
+    if (a->D != 64 && a->D != 128) return fail(DSPARK_EINVAL, "%s: D=%d is not 64 or 128", fn, a->D);
+    if (a->dtype != DSPARK_BF16) return fail(DSPARK_EDTYPE, "%s: dtype=%d", fn, a->dtype);
+    if (a->window < 0) return fail(DSPARK_EINVAL, "%s: window=%d < 0", fn, a->window);
+    return DSPARK_OK;
+}
+
+dspark_status check_cache(const dspark_attn *a, const char *fn) {
+    if (a->page_size < 1 || a->page_size > 65536)
+        return fail(DSPARK_EINVAL, "%s: page_size=%d outside [1, 65536]", fn, a->page_size);
+    if (a->num_pages < 1 || a->max_pages < 1)
+        return fail(DSPARK_EINVAL, "%s: num_pages=%d, max_pages=%d: each is >= 1", fn, a->num_pages,
+                    a->max_pages);
+    if ((long long)a->max_pages * a->page_size > INT32_MAX - 65536)
+        return fail(DSPARK_EINVAL, "%s: max_pages=%d pages of %d positions pass 32 bits", fn,
+                    a->max_pages, a->page_size);
+    REQUIRE(a->k_cache);
+    REQUIRE(a->v_cache);
+    REQUIRE(a->block_table);
+    REQUIRE_ALIGNED(a->k_cache, 16);
+    REQUIRE_ALIGNED(a->v_cache, 16);
+    if (a->page_stride <= 0 || a->slot_stride <= 0 || a->head_stride <= 0)
+        return fail(DSPARK_EINVAL, "%s: cache strides must be > 0", fn);
+    if (a->page_stride % 8 || a->slot_stride % 8 || a->head_stride % 8)
+        return fail(DSPARK_EALIGN, "%s: a cache stride is not a multiple of 8 elements", fn);
+    return DSPARK_OK;
+}
+
+dspark_status check_row_stride(int64_t stride, int heads, int D, const char *what, const char *fn) {
+    if (stride < (int64_t)heads * D)
+        return fail(DSPARK_EINVAL, "%s: %s=%lld is less than a row", fn, what, (long long)stride);
+    if (stride % 8) return fail(DSPARK_EALIGN, "%s: %s is not a multiple of 8 elements", fn, what);
+    return DSPARK_OK;
+}
+
+dspark_status check_attn_softmax(const dspark_attn *a, const char *fn) {
+    if (!(a->scale > 0.0f) || std::isinf(a->scale))
+        return fail(DSPARK_EINVAL, "%s: scale must be finite and > 0", fn);
+    REQUIRE(a->q_rot);
+    REQUIRE(a->row_off);
+    REQUIRE(a->out);
+    REQUIRE_ALIGNED(a->q_rot, 16);
+    REQUIRE_ALIGNED(a->out, 16);
+    const size_t need = dspark::attn_workspace_bytes();
+    if (!a->workspace) return fail(DSPARK_EWORKSPACE, "%s: workspace is NULL", fn);
+    if (!aligned(a->workspace, 256))
+        return fail(DSPARK_EWORKSPACE, "%s: workspace is not 256-byte aligned", fn);
+    if (a->workspace_bytes < need)
+        return fail(DSPARK_EWORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn,
+                    a->workspace_bytes, need);
+    return DSPARK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dspark_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t D, int32_t q_max) {
+    if (Hq < 1 || Hq > DSPARK_MAX_HEADS || Hkv < 1 || Hkv > Hq || Hq % Hkv || (D != 64 && D != 128) ||
+        q_max < 1)
+        return 0;
+    return dspark::attn_workspace_bytes();
+}
+
+dspark_status dspark_rope_append(const dspark_attn *a, dspark_stream_t stream) {
+    NvtxRange range("dspark_rope_append");
+    const char *fn = "dspark_rope_append";
+    dspark_status st = check_attn(a, fn);
+    if (st) return st;
+    if (a->rot_dim < 0 || a->rot_dim > a->D || a->rot_dim % 16)
+        return fail(DSPARK_EINVAL, "%s: rot_dim=%d is not a multiple of 16 in [0, %d]", fn,
+                    a->rot_dim, a->D);
+    if (a->B == 0 || a->rows == 0) return DSPARK_OK;
+    if (!a->q && !a->k) return fail(DSPARK_EINVAL, "%s: q and k are both NULL", fn);
+    if (!a->k != !a->v) return fail(DSPARK_EINVAL, "%s: one of k and v is NULL", fn);
+    REQUIRE(a->row_req);
+    REQUIRE(a->packed_pos);
+    if (a->rot_dim > 0) REQUIRE(a->rope_freq);
+    if (a->rot_dim > 0) REQUIRE_ALIGNED(a->rope_freq, 8);
+    if (a->q) {
+        REQUIRE(a->q_rot);
+        REQUIRE_ALIGNED(a->q, 16);
+        REQUIRE_ALIGNED(a->q_rot, 16);
+        if ((st = check_row_stride(a->q_stride, a->Hq, a->D, "q_stride", fn))) return st;
+    }
+    if (a->k) {
+        if ((st = check_cache(a, fn))) return st;
+        REQUIRE_ALIGNED(a->k, 16);
+        REQUIRE_ALIGNED(a->v, 16);
+        REQUIRE_ALIGNED(a->k_rot, 16);
+        if ((st = check_row_stride(a->k_stride, a->Hkv, a->D, "k_stride", fn))) return st;
+        if ((st = check_row_stride(a->v_stride, a->Hkv, a->D, "v_stride", fn))) return st;
+    }
+    DeviceInfo *dev;
+    if ((st = device_info(&dev))) return st;
+    cudaError_t e = dspark::launch_rope_append(*a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rope_append_kernel launch");
+    return DSPARK_OK;
+}
+
+dspark_status dspark_step_attention(const dspark_attn *a, dspark_stream_t stream) {
+    NvtxRange range("dspark_step_attention");
+    const char *fn = "dspark_step_attention";
+    dspark_status st = check_attn(a, fn);
+    if (st) return st;
+    if (a->q_max > DSPARK_MAX_STEP_ROWS)
+        return fail(DSPARK_EINVAL, "%s: q_max=%d outside [1, %d]", fn, a->q_max, DSPARK_MAX_STEP_ROWS);
+    if (a->B == 0 || a->rows == 0) return DSPARK_OK;
+    if ((st = check_attn_softmax(a, fn))) return st;
+    if ((st = check_cache(a, fn))) return st;
+    DeviceInfo *dev;
+    if ((st = device_info(&dev))) return st;
+    cudaError_t e = dspark::launch_step_attention(*a, dev->sms, g_wait_ns.load(),
+                                                  reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "step_attention_kernel launch");
+    return DSPARK_OK;
+}
+
+dspark_status dspark_prompt_attention(const dspark_attn *a, dspark_stream_t stream) {
+    NvtxRange range("dspark_prompt_attention");
+    const char *fn = "dspark_prompt_attention";
+    dspark_status st = check_attn(a, fn);
+    if (st) return st;
+    if (a->B == 0 || a->rows == 0) return DSPARK_OK;
+    if ((st = check_attn_softmax(a, fn))) return st;
+    REQUIRE(a->k_rot);
+    REQUIRE(a->v);
+    REQUIRE_ALIGNED(a->k_rot, 16);
+    REQUIRE_ALIGNED(a->v, 16);
+    if ((st = check_row_stride(a->v_stride, a->Hkv, a->D, "v_stride", fn))) return st;
+    DeviceInfo *dev;
+    if ((st = device_info(&dev))) return st;
+    cudaError_t e = dspark::launch_prompt_attention(*a, dev->sms, g_wait_ns.load(),
+                                                    reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "prompt_attention_kernel launch");
+    return DSPARK_OK;
+}
+
+}  // extern "C"

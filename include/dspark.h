@@ -318,6 +318,130 @@ dspark_status dspark_fit_sts_tau(int32_t N, int32_t gamma, const float *conf,
                                  float *tau_out, float *nll_out, int32_t *n_obs,
                                  dspark_stream_t stream);
 
+/* ===========================================================================
+ * The attention side of the target forward that fills target_logits.
+ *
+ * dspark_compact hands the target a ragged batch: rows [root, d_1..d_{L_b}]
+ * per request, their positions and their owners.  Three calls run the
+ * attention of one layer on such rows:
+ *
+ *   dspark_rope_append      rotates q and k by the rows' positions and
+ *                           appends k and v to a paged cache;
+ *   dspark_step_attention   the step's rows attend over the paged cache
+ *                           (one row per request where L_b = 0);
+ *   dspark_prompt_attention whole prompts attend to themselves, causally,
+ *                           packed one after the other.
+ *
+ * All three take one dspark_attn.  The conventions at the top of this file
+ * hold (ownership, asynchrony, errors, workspace); in addition:
+ *   - Element type: q, k, v, the caches and the outputs are bfloat16
+ *     (dtype = DSPARK_BF16; another code is DSPARK_EDTYPE).  Scores, softmax
+ *     statistics and sums are fp32; each output is rounded once.  Softmax
+ *     weights are rounded to bfloat16 before they multiply v, and their sum
+ *     is taken over the rounded weights.
+ *   - Packed rows: row r belongs to request row_req[r] (-1: padding) and sits
+ *     at position packed_pos[r]; request b owns rows row_off[b] ..
+ *     row_off[b+1], at consecutive positions.  These are the arrays that
+ *     dspark_score_compact and dspark_compact write; prompts are described
+ *     the same way.  Padding rows are neither read nor written.
+ *   - Cache: entry (page, slot, head) of k_cache and of v_cache starts
+ *     page * page_stride + slot * slot_stride + head * head_stride elements
+ *     from the base and holds D elements.  Position p of request b lives in
+ *     page block_table[b][p / page_size], slot p % page_size.  Any page_size
+ *     >= 1.  A page id outside [0, num_pages), and a position past max_pages
+ *     pages, is no memory: nothing is stored there and its keys are masked.
+ *   - Heads: query head h reads cached head h / (Hq / Hkv).
+ *   - Masked keys do not contribute, whatever their k and v hold (infinities
+ *     and NaN among them).  A row that sees no key gives zeros.
+ * =========================================================================== */
+
+/* Limits checked by the three calls. */
+#define DSPARK_MAX_HEADS 256
+#define DSPARK_MAX_ROWS (1 << 24)
+/* Rows of one request that dspark_step_attention takes (1 + gamma). */
+#define DSPARK_MAX_STEP_ROWS (DSPARK_MAX_GAMMA + 1)
+
+typedef struct dspark_attn {
+    /* ---- shapes ---------------------------------------------------------- */
+    int32_t B;          /* requests, 0..DSPARK_MAX_B (0: every call is a no-op) */
+    int32_t rows;       /* packed row slots of q, k, v, q_rot, k_rot, out; >= row_off[B];
+                           0..DSPARK_MAX_ROWS (0: every call is a no-op) */
+    int32_t q_max;      /* bound of one request's rows, >= 1; dspark_step_attention:
+                           1..DSPARK_MAX_STEP_ROWS.  Rows of a request past it are not
+                           computed */
+    int32_t Hq, Hkv;    /* query and cached heads, 1..DSPARK_MAX_HEADS, Hq % Hkv == 0 */
+    int32_t D;          /* head size: 64 or 128 */
+    int32_t dtype;      /* DSPARK_BF16 */
+    int32_t page_size;  /* positions per page, 1..65536 */
+    int32_t num_pages;  /* pages of the caches, >= 1 */
+    int32_t max_pages;  /* columns of block_table, >= 1 */
+    int32_t rot_dim;    /* leading entries of a head that are rotated: a multiple of 16,
+                           0..D; the rest is copied */
+    int32_t interleaved; /* pairs (2i, 2i+1) if nonzero, else (i, i + rot_dim/2) */
+    int32_t window;     /* > 0: a row at position p sees keys p-window+1..p; 0: 0..p */
+    float scale;        /* scores are scale * q.k; finite and > 0 */
+
+    /* ---- strides, in elements --------------------------------------------- */
+    int64_t q_stride, k_stride, v_stride; /* between rows of q, k, v; the heads of a row
+                                             are contiguous.  Multiples of 8 */
+    int64_t page_stride, slot_stride, head_stride; /* both caches; multiples of 8 */
+
+    /* ---- device pointers; those to bfloat16 16-byte aligned ----------------- */
+    const void *q;  /* [rows, Hq, D] unrotated queries (row stride q_stride) */
+    const void *k;  /* [rows, Hkv, D] unrotated keys (row stride k_stride) */
+    const void *v;  /* [rows, Hkv, D] values (row stride v_stride) */
+    void *q_rot;    /* [rows, Hq, D] contiguous; may be q itself where q is contiguous */
+    void *k_rot;    /* [rows, Hkv, D] contiguous; dspark_rope_append: NULL where only the
+                       cache is wanted; may be k itself where k is contiguous */
+    void *k_cache, *v_cache;
+    const int32_t *row_off;     /* [B+1] */
+    const int32_t *row_req;     /* [rows] */
+    const int32_t *packed_pos;  /* [rows] */
+    const int32_t *seq_lens;    /* [B] position of each request's first row, or NULL (0) */
+    const int32_t *block_table; /* [B, max_pages] */
+    const uint64_t *rope_freq;  /* [rot_dim / 2] turns per position, in 2^-64 of a turn */
+    void *out;                  /* [rows, Hq, D] contiguous */
+
+    /* ---- scratch ------------------------------------------------------------ */
+    void *workspace;        /* dspark_step_attention, dspark_prompt_attention; zeroed once
+                               with dspark_workspace_init */
+    size_t workspace_bytes;
+} dspark_attn;
+
+/* Bytes of workspace that the attention calls need for these heads and this
+ * q_max (any B, any length).  Returns 0 outside the limits above. */
+size_t dspark_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t D, int32_t q_max);
+
+/*
+ * Position rotation of q and k, and append of k and v to the paged cache.
+ * Pair i of a head of row r turns by packed_pos[r] * rope_freq[i] (mod 1
+ * turn): (x, y) -> (x cos - y sin, y cos + x sin).  A frequency f (radians
+ * per position) is the integer round(f / (2 pi) * 2^64); the phase is the
+ * low word of an integer product, so it loses nothing however far the
+ * position (packed_pos >= 0).
+ * Reads q, k, v, row_req, packed_pos, block_table, rope_freq (rot_dim > 0).
+ * Writes q_rot, k_rot (when set) and the rows' cache entries.
+ * k and v NULL together: only q is rotated; q NULL: only k and v are handled.
+ */
+dspark_status dspark_rope_append(const dspark_attn *attn, dspark_stream_t stream);
+
+/*
+ * The step's rows attend over the paged cache: row j of request b is at
+ * position seq_lens[b] + j and sees the cached keys up to that position
+ * (inside the window, if there is one); its own key is in the cache already.
+ * Reads q_rot, row_off, seq_lens, block_table, k_cache, v_cache.  Writes out
+ * rows row_off[b] .. row_off[b+1].
+ */
+dspark_status dspark_step_attention(const dspark_attn *attn, dspark_stream_t stream);
+
+/*
+ * Whole prompts: row i of request b sees rows 0..i of its own request (inside
+ * the window, if there is one).  Keys and values come from the packed rows,
+ * k_rot and v (row stride v_stride); the cache is not read.
+ * Reads q_rot, k_rot, v, row_off.  Writes out rows row_off[b] .. row_off[b+1].
+ */
+dspark_status dspark_prompt_attention(const dspark_attn *attn, dspark_stream_t stream);
+
 /*
  * Blocking read of the workspace's device status word (0 = healthy).  A
  * nonzero value means a kernel gave up on a bounded wait: bit 0 (1) an
