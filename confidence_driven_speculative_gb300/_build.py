@@ -19,7 +19,7 @@ OBJ_DIR = os.path.join(PKG, "lib", "obj")
 LIB_PATH = os.path.join(PKG, "lib", "libdspark.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "score_budget.cu", "compact.cu", "verify.cu", "verify_small.cu", "sts_fit.cu",
-           "rope_append.cu", "step_attention.cu", "prompt_attention.cu"]
+           "tensor_map.cu", "rope_append.cu", "step_attention.cu", "prompt_attention.cu"]
 
 
 def nvcc() -> str:

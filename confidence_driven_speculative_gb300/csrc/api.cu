@@ -672,7 +672,7 @@ dspark_status check_attn_softmax(const dspark_attn *a, const char *fn) {
     REQUIRE(a->out);
     REQUIRE_ALIGNED(a->q_rot, 16);
     REQUIRE_ALIGNED(a->out, 16);
-    const size_t need = dspark::attn_workspace_bytes();
+    const size_t need = dspark::attn_workspace_bytes(a->Hq, a->Hkv, a->D, a->q_max);
     if (!a->workspace) return fail(DSPARK_EWORKSPACE, "%s: workspace is NULL", fn);
     if (!aligned(a->workspace, 256))
         return fail(DSPARK_EWORKSPACE, "%s: workspace is not 256-byte aligned", fn);
@@ -690,7 +690,7 @@ size_t dspark_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t D, int32_t q_
     if (Hq < 1 || Hq > DSPARK_MAX_HEADS || Hkv < 1 || Hkv > Hq || Hq % Hkv || (D != 64 && D != 128) ||
         q_max < 1)
         return 0;
-    return dspark::attn_workspace_bytes();
+    return dspark::attn_workspace_bytes(Hq, Hkv, D, q_max);
 }
 
 dspark_status dspark_rope_append(const dspark_attn *a, dspark_stream_t stream) {
@@ -739,6 +739,10 @@ dspark_status dspark_step_attention(const dspark_attn *a, dspark_stream_t stream
     if (a->B == 0 || a->rows == 0) return DSPARK_OK;
     if ((st = check_attn_softmax(a, fn))) return st;
     if ((st = check_cache(a, fn))) return st;
+    if (!dspark::step_strides_ok(*a))
+        return fail(DSPARK_EINVAL,
+                    "%s: page_size=%d is not a multiple of 8, and page_stride or head_stride is not "
+                    "a whole number of slots", fn, a->page_size);
     DeviceInfo *dev;
     if ((st = device_info(&dev))) return st;
     cudaError_t e = dspark::launch_step_attention(*a, dev->sms, g_wait_ns.load(),

@@ -12,7 +12,10 @@ namespace dspark {
 constexpr int kAttnMaxCtas = 160;  // CTAs of an attention launch (152 SMs)
 
 // Workspace of the attention calls: word 0 is the device status.
-size_t attn_workspace_bytes();
+size_t attn_workspace_bytes(int Hq, int Hkv, int D, int q_max);
+
+// Can the cache be copied key by key (pages of no multiple of 8 positions)?
+bool step_strides_ok(const dspark_attn &a);
 
 cudaError_t launch_rope_append(const dspark_attn &a, cudaStream_t s);
 cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_ns, cudaStream_t s);
