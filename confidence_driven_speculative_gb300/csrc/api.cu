@@ -736,6 +736,9 @@ dspark_status dspark_step_attention(const dspark_attn *a, dspark_stream_t stream
     if (st) return st;
     if (a->q_max > DSPARK_MAX_STEP_ROWS)
         return fail(DSPARK_EINVAL, "%s: q_max=%d outside [1, %d]", fn, a->q_max, DSPARK_MAX_STEP_ROWS);
+    if (a->Hq / a->Hkv > DSPARK_MAX_STEP_GROUP)
+        return fail(DSPARK_EINVAL, "%s: %d query heads per cached head, at most %d", fn,
+                    a->Hq / a->Hkv, DSPARK_MAX_STEP_GROUP);
     if (a->B == 0 || a->rows == 0) return DSPARK_OK;
     if ((st = check_attn_softmax(a, fn))) return st;
     if ((st = check_cache(a, fn))) return st;

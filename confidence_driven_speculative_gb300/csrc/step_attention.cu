@@ -38,37 +38,42 @@ namespace dspark {
 namespace {
 
 constexpr int kTile = 128;      // keys of a tile
-constexpr int kMaxCols = 160;   // columns of a unit: 3 x 160 <= 512 TMEM columns
+constexpr int kMaxCols = 160;   // columns of a unit: S, O and L take 3 x 160 of 512 TMEM columns
+constexpr int kTwoS = 128;      // up to so many, S is held twice
+constexpr uint32_t kPGroup = kTile * 32;  // P: 16 columns of 128 keys, rows of 32 bytes
 constexpr int kMaxSlots = 12;   // ring slots (one K or one V tile each)
 constexpr int kWords = 16;      // ring of the tiles' bad-key words
-constexpr int kSoftThreads = 128;
-constexpr int kThreadsStep = 192;  // 4 softmax warps, the producer, the MMA issuer
-constexpr uint32_t kColS = 0, kColO = kMaxCols, kColL = 2 * kMaxCols;
+constexpr int kSoftThreads = 256;  // two groups of 128: each takes every other 16 columns
+constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10;
+constexpr int kThreadsStep = 352;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRefMin = -1e30f;  // reference of a column without a score yet
 constexpr float kRefSlack = 8.0f;  // log2: how far a score may pass the reference
 constexpr int kJoinThreads = 128;
+constexpr size_t kSmemBytes = 232448;  // shared memory of a CTA
 
 // What step_join_kernel needs of the unit that is cut before CTA i.
 struct CutInfo {
     int32_t first, last;      // the CTAs that share it; first < i <= last, or last = -1: no cut
     int32_t slot_first;       // partial slot of the first one (the others': 2 * CTA)
-    int32_t row0, head0;      // packed row of the request, first query head of the group
-    int32_t c0, ncols;
-    int32_t pad;
+    int32_t row0, head0;      // first packed row of the unit, first query head of the group
+    int32_t ncols;
 };
 
 struct StepArgs {
     int B, rows, q_max, Hq, Hkv, G;
     int page_size, num_pages, max_pages, window;
+    uint32_t page_mul, page_shift;  // position / page_size = position * mul >> shift
     int box;                   // keys of a TMA box (divides the page and the tile); 0: gather
     int ncap;                  // columns of a unit at most, a multiple of 16
-    int slots;
+    int rows_cap;              // rows of a unit at most
+    int slots, k_slots;        // ring slots; the first k_slots hold K tiles, the others V tiles
+    int two_s, two_p, two_q;   // S, P, Q held twice
     int page_rows, head_rows;  // gather: rows of the 2-D view per page and head
     int head_x;                // gather: entries of a row per head
     float scale2;              // scale * log2(e)
     int64_t page_stride, slot_stride, head_stride;
-    const uint16_t *q, *v_cache;
+    const uint16_t *v_cache;
     const int32_t *row_off, *seq_lens, *block_table;
     uint16_t *out;
     float *part;               // [2 * CTAs][ncap][D]
@@ -84,8 +89,12 @@ struct Req {
     int pos0;        // position of the first one
     int kbeg, kend;  // keys that some row sees
     int t0, nt;      // tiles
-    int rt, per;     // blocks of columns, columns of one
+    int blocks, per; // blocks of rows, rows of one
 };
+
+__device__ __forceinline__ int page_of(const StepArgs &A, int pos) {
+    return int((uint64_t(uint32_t(pos)) * A.page_mul) >> A.page_shift);
+}
 
 __device__ __forceinline__ Req load_req(const StepArgs &A, int b) {
     Req r;
@@ -95,71 +104,96 @@ __device__ __forceinline__ Req load_req(const StepArgs &A, int b) {
     // far past any table, where nothing is seen, stays in 32 bits
     r.pos0 = A.seq_lens ? min(max(A.seq_lens[b], 0), INT32_MAX - 65536) : 0;
     const int cap = A.max_pages * A.page_size;
-    r.kend = int(min((long long)r.pos0 + r.n, (long long)cap));
+    r.kend = min(r.pos0 + r.n, cap);
     r.kbeg = A.window > 0 ? min(max(r.pos0 - A.window + 1, 0), r.kend) : 0;
     r.t0 = r.kbeg / kTile;
     r.nt = max((r.kend + kTile - 1) / kTile - r.t0, 1);
-    const int cols = r.n * A.G;
-    const int blocks = (cols + A.ncap - 1) / A.ncap;
-    r.per = blocks ? (((cols + blocks - 1) / blocks + 15) & ~15) : 16;
-    r.rt = (cols + r.per - 1) / r.per;
+    r.per = r.n;
+    r.blocks = r.n > 0;
+    if (r.n > A.rows_cap) {
+        r.blocks = (r.n + A.rows_cap - 1) / A.rows_cap;
+        r.per = (r.n + r.blocks - 1) / r.blocks;
+        r.blocks = (r.n + r.per - 1) / r.per;
+    }
     return r;
 }
 
-// Walks the CTA's tiles.
-struct Walk {
+// One (request, cached head, block of rows), and walking to the next.
+struct Unit {
     Req q;
-    int b, h, rt, t;
-    __device__ __forceinline__ void start(const StepArgs &A, int b_, long long off) {
+    int b, h, blk;
+    int j0, ncols;  // first row of the block, its columns
+
+    __device__ __forceinline__ void shape(const StepArgs &A) {
+        j0 = blk * q.per;
+        ncols = min(q.per, q.n - j0) * A.G;
+    }
+    // The unit of tile `off` of request b's list; returns the tile in it.
+    __device__ __forceinline__ int start(const StepArgs &A, int b_, long long off) {
         b = b_;
         q = load_req(A, b);
-        const int per_head = q.rt * q.nt;
+        const int per_head = q.blocks * q.nt;
         h = int(off / per_head);
         const int rem = int(off % per_head);
-        rt = rem / q.nt;
-        t = rem % q.nt;
+        blk = rem / q.nt;
+        shape(A);
+        return rem - blk * q.nt;
     }
-    // To the next tile; the caller stops after the last one.
     __device__ __forceinline__ void next(const StepArgs &A) {
-        if (++t < q.nt) return;
-        t = 0;
-        if (++rt < q.rt) return;
-        rt = 0;
-        if (++h < A.Hkv) return;
-        h = 0;
-        do {
-            if (++b >= A.B) { b = A.B - 1; return; }
-            q = load_req(A, b);
-        } while (q.rt == 0);
+        if (++blk == q.blocks) {
+            blk = 0;
+            if (++h == A.Hkv) {
+                h = 0;
+                do {
+                    if (++b >= A.B) { b = A.B - 1; return; }
+                    q = load_req(A, b);
+                } while (q.blocks == 0);
+            }
+        }
+        shape(A);
     }
-    __device__ __forceinline__ int c0() const { return rt * q.per; }
-    __device__ __forceinline__ int ncols(const StepArgs &A) const { return min(q.per, q.n * A.G - c0()); }
+};
+
+// Slot and phase of a ring walked in order.
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int slots) {
+        if (++slot == slots) { slot = 0; phase ^= 1; }
+    }
 };
 
 struct Ctrl {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
-    uint64_t q_full, s_full, p_full, pv_done, drained;
+    uint64_t q_full[2], q_empty[2], s_full[2];
+    uint64_t p_full[2], pv_done[2], drained;
     uint32_t tmem;
     int gave_up, poison;
     long long warp_total[kThreadsStep / 32];
-    long long total, start_base;
+    long long start_base;
     int start_b;
+    alignas(16) int row[2][2][kTile];     // producers: pages of the boxes, or rows of the keys
     alignas(16) uint32_t bad[kWords][4];  // keys of a tile whose page is no memory
     alignas(16) float ref[kMaxCols];
     alignas(16) float fac[kMaxCols];
     alignas(16) float colmax[4][kMaxCols];
 };
 
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool soft_any(bool x) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 q, %1, 0;\n\t"
-        "barrier.cta.red.or.pred p, 1, 128, q;\n\t"
+        "barrier.cta.red.or.pred p, 1, 256, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r) : "r"(uint32_t(x)) : "memory");
     return r != 0;
+}
+
+// Is phase `parity` of `bar` over?  One answer for the whole warp.
+__device__ __forceinline__ bool warp_test(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -180,38 +214,71 @@ __device__ __forceinline__ uint32_t nonfinite_mask(uint32_t w) {
     return m;
 }
 
-// The columns [lo, hi) of the block that see the key at `kpos`.
-__device__ __forceinline__ void visible_columns(const StepArgs &A, const Walk &w, int c0, int ncols,
-                                                int kpos, bool bad, int &lo, int &hi) {
-    lo = min(max(max(kpos - w.q.pos0, 0) * A.G - c0, 0), ncols);
-    hi = ncols;
+// The columns [lo, hi) of the unit that see the key at `kpos`.
+__device__ __forceinline__ void visible_columns(const StepArgs &A, const Unit &u, int kpos, bool bad,
+                                                int &lo, int &hi) {
+    lo = min(max(kpos - u.q.pos0 - u.j0, 0) * A.G, u.ncols);
+    hi = u.ncols;
     if (A.window > 0) {
-        const long long j = (long long)kpos - w.q.pos0 + A.window;  // rows below see it
-        hi = int(min(max(min(j, (long long)w.q.n) * A.G - c0, 0ll), (long long)ncols));
+        const long long j = (long long)kpos - u.q.pos0 - u.j0 + A.window;  // rows below see it
+        hi = int(min(max(min(j, (long long)u.q.n) * A.G, 0ll), (long long)u.ncols));
     }
-    if (bad || kpos < w.q.kbeg || kpos >= w.q.kend) hi = lo;
+    if (bad || kpos < u.q.kbeg || kpos >= u.q.kend) hi = lo;
+}
+
+// 16 columns of a tile: weights 2^(s * scale2 - ref), rounded, to P; returns
+// the largest exponent.  Columns whose bit of `seen` is clear weigh nothing.
+template <bool kMasked>
+__device__ __forceinline__ float weigh16(const float (&s)[16], const float *ref, float scale2,
+                                         uint32_t seen, uint32_t at, int swz) {
+    float r[16];
+#pragma unroll
+    for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<float4 *>(r + e) = *reinterpret_cast<const float4 *>(ref + e);
+    uint32_t p[8];
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+        float x = fmaf(s[e], scale2, -r[e]), y = fmaf(s[e + 1], scale2, -r[e + 1]);
+        if (kMasked) {
+            if (!((seen >> e) & 1)) x = -INFINITY;
+            if (!((seen >> (e + 1)) & 1)) y = -INFINITY;
+        }
+        top = fmaxf(top, fmaxf(x, y));
+        p[e / 2] = pack_bf16x2(exp2_approx(x), exp2_approx(y));
+    }
+    st_shared16(at + (swz << 4), p[0], p[1], p[2], p[3]);
+    st_shared16(at + ((swz ^ 1) << 4), p[4], p[5], p[6], p[7]);
+    return top;
+}
+
+// Bits of the columns n .. n + 15 that lie in [lo, hi).
+__device__ __forceinline__ uint32_t seen16(int n, int lo, int hi) {
+    const int a = min(max(lo - n, 0), 16), b = min(max(hi - n, 0), 16);
+    return ((1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsStep, 1)
-step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant__ CUtensorMap k_map,
-                      const __grid_constant__ CUtensorMap v_map) {
+step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant__ CUtensorMap q_map,
+                      const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     constexpr int kHalves = D / 64;
     constexpr uint32_t kHalfBytes = kTile * 128;
     constexpr uint32_t kSlotBytes = kHalves * kHalfBytes;
     extern __shared__ uint8_t dyn[];
     __shared__ Ctrl C;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
 
-    // Shared memory: ring, P, Q, ones.
-    const uint32_t base = (smem_addr(dyn) + 1023) & ~1023u;
-    const uint32_t ring = base;
+    // Shared memory: ring, P and Q (once or twice), ones.
+    const uint32_t ring = (smem_addr(dyn) + 1023) & ~1023u;
     const uint32_t p_smem = ring + A.slots * kSlotBytes;
-    const uint32_t p_groups = (A.ncap + 63) / 64;
-    const uint32_t q_smem = p_smem + p_groups * kHalfBytes;
-    const uint32_t q_half = A.ncap * 128;
-    const uint32_t ones = q_smem + kHalves * q_half;
+    const uint32_t p_bytes = A.ncap / 16 * kPGroup;
+    const uint32_t q_smem = p_smem + (1 + A.two_p) * p_bytes;
+    const uint32_t q_half = A.ncap * 128, q_bytes = kHalves * q_half;
+    const uint32_t ones = q_smem + (1 + A.two_q) * q_bytes;
+    // TMEM: S (once or twice), O, L.
+    const uint32_t col_o = A.ncap * (1 + A.two_s), col_l = col_o + A.ncap;
 
     // ---- set-up: barriers, TMEM, the constant operand, the CTA's tiles -----
     if (tid == 0) {
@@ -219,10 +286,13 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
             mbar_init(&C.full[s], 1);
             mbar_init(&C.empty[s], 1);
         }
-        mbar_init(&C.q_full, kSoftThreads);
-        mbar_init(&C.s_full, 2);
-        mbar_init(&C.p_full, 1);
-        mbar_init(&C.pv_done, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&C.q_full[s], 1);
+            mbar_init(&C.q_empty[s], 1);
+            mbar_init(&C.s_full[s], 2);
+            mbar_init(&C.p_full[s], 1);
+            mbar_init(&C.pv_done[s], 1);
+        }
         mbar_init(&C.drained, 1);
         C.gave_up = 0;
         C.poison = 0;
@@ -232,8 +302,9 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
     }
     if (tid < 64) st_shared16(ones + tid * 16, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
     fence_async_shared();
-    if (warp == 5) tmem_alloc(&C.tmem, kTmemCols);
-    if (warp == 4 && lane == 0) {
+    if (warp == kWarpMma) tmem_alloc(&C.tmem, kTmemCols);
+    if (warp == kWarpK && lane == 0) {
+        prefetch_map(&q_map);
         prefetch_map(&k_map);
         prefetch_map(&v_map);
     }
@@ -243,7 +314,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
     long long mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
         const Req r = load_req(A, b);
-        mine += (long long)r.rt * r.nt * A.Hkv;
+        mine += (long long)r.blocks * r.nt * A.Hkv;
     }
     long long incl = mine;
 #pragma unroll
@@ -267,7 +338,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
         long long at = excl;
         for (int b = b_lo; b < b_hi; ++b) {
             const Req r = load_req(A, b);
-            const long long x = (long long)r.rt * r.nt * A.Hkv;
+            const long long x = (long long)r.blocks * r.nt * A.Hkv;
             if (start < at + x) {
                 C.start_b = b;
                 C.start_base = at;
@@ -279,72 +350,81 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int left = int(end - start);
+    const int tiles = int(end - start);
     const uint32_t tmem = C.tmem;
-    Walk w;
-    if (left > 0) w.start(A, C.start_b, start - C.start_base);
+    volatile int *gave_up = &C.gave_up;
+    Unit u;
+    int t = 0;  // tile in the unit
+    if (tiles > 0) t = u.start(A, C.start_b, start - C.start_base);
 
     if (tid == 0) {
         // The unit that is cut before this CTA, for the join.
         CutInfo ci{};
         ci.last = -1;
-        if (left > 0 && w.t > 0) {
-            const long long u0 = start - w.t, u1 = u0 + w.q.nt;
+        if (tiles > 0 && t > 0) {
+            const long long u0 = start - t, u1 = u0 + u.q.nt;
             ci.first = int(((u0 + 1) * ctas - 1) / total);
             ci.last = int((u1 * ctas - 1) / total);
-            const long long s0 = total * ci.first / ctas;
-            ci.slot_first = s0 == u0 ? 2 * ci.first : 2 * ci.first + 1;
-            ci.row0 = w.q.row0;
-            ci.head0 = w.h * A.G;
-            ci.c0 = w.c0();
-            ci.ncols = w.ncols(A);
+            ci.slot_first = total * ci.first / ctas == u0 ? 2 * ci.first : 2 * ci.first + 1;
+            ci.row0 = u.q.row0 + u.j0;
+            ci.head0 = u.h * A.G;
+            ci.ncols = u.ncols;
         }
         A.cut[me] = ci;
     }
 
-    volatile int *gave_up = &C.gave_up;
-    if (left > 0 && warp == 4) {
-        // ---- producer: K and V tiles into the ring ---------------------------
-        // A lane owns one TMA box of the tile (or four keys: gather), and
-        // looks up its pages one tile ahead.
-        struct Ids { int page[4]; };
+    if (tiles > 0 && (warp == kWarpK || warp == kWarpV)) {
+        // ---- producers: one warp copies K tiles and the queries, one V tiles ----
+        // A lane looks up the pages of one TMA box (or of four keys: gather)
+        // one tile ahead; one elected lane issues the copies.
+        const bool is_v = warp == kWarpV;
+        const CUtensorMap *map = is_v ? &v_map : &k_map;
         const int boxes = A.box ? kTile / A.box : 32;
         const int span = A.box ? A.box : 4;
-        auto look_up = [&](const Walk &x, Ids &ids) {
-            const int key0 = (x.q.t0 + x.t) * kTile + lane * span;
+        struct Ids { int page[4]; };
+        auto look_up = [&](const Unit &x, int tile, Ids &ids) {
+            const int key0 = (x.q.t0 + tile) * kTile + lane * span;
+            const int32_t *table = A.block_table + (int64_t)x.b * A.max_pages;
+            const bool wanted = lane < boxes && key0 < x.q.kend && key0 + span > x.q.kbeg;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 ids.page[i] = -1;
-                const int key = key0 + i;
-                if ((i == 0 || !A.box) && lane < boxes) {
-                    const int pi = key / A.page_size;
-                    if (pi < A.max_pages && key0 < x.q.kend && key0 + span > x.q.kbeg)
-                        ids.page[i] = A.block_table[(int64_t)x.b * A.max_pages + pi];
+                if ((i == 0 || !A.box) && wanted) {
+                    const int pi = page_of(A, key0 + i);
+                    if (pi < A.max_pages) ids.page[i] = table[pi];
                 }
             }
         };
         Ids ids;
-        look_up(w, ids);
-        int issued = 0;
-        for (int i = 0; i < left; ++i) {
-            Walk x = w;
-            if (i + 1 < left) x.next(A);
+        look_up(u, t, ids);
+        Ring r, rq;
+        // K and V have rings of their own: each warp meets its own loads only
+        const int my_slots = is_v ? A.slots - A.k_slots : A.k_slots, slot0 = is_v ? A.k_slots : 0;
+        bool first = true, ok = true;
+        int units = 0, issued = 0;  // units, and tiles of this warp
+        for (int i = 0; i < tiles; ++i) {
+            Unit x = u;
+            int tx = t + 1;
+            if (tx == u.q.nt && i + 1 < tiles) {
+                x.next(A);
+                tx = 0;
+            }
             Ids ahead;
-            look_up(x, ahead);
+            if (i + 1 < tiles) look_up(x, tx, ahead);
 
-            const int key0 = (w.q.t0 + w.t) * kTile + lane * span;
-            const bool here = lane < boxes && key0 < w.q.kend && key0 + span > w.q.kbeg;
+            const int tile0 = (u.q.t0 + t) * kTile, key0 = tile0 + lane * span;
+            const bool here = lane < boxes && key0 < u.q.kend && key0 + span > u.q.kbeg;
             uint32_t bad_bits = 0;  // of the lane's keys (gather) or of the whole box
             int row[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                bool ok = ids.page[j] >= 0 && ids.page[j] < A.num_pages;
-                if (!ok) bad_bits |= 1u << j;
-                const int page = ok ? ids.page[j] : 0;  // masked; any memory will do
+                const bool good = ids.page[j] >= 0 && ids.page[j] < A.num_pages;
+                if (!good) bad_bits |= 1u << j;
+                const int page = good ? ids.page[j] : 0;  // masked; any memory will do
                 row[j] = A.box ? page
-                               : page * A.page_rows + w.h * A.head_rows + (key0 + j) % A.page_size;
+                               : page * A.page_rows + u.h * A.head_rows + key0 + j -
+                                     page_of(A, key0 + j) * A.page_size;
             }
-            const int slot_in_page = A.box ? key0 % A.page_size : 0;
             const bool lane_bad = here && (A.box ? (bad_bits & 1) : bad_bits != 0);
             uint32_t words[4] = {0, 0, 0, 0};
             if (__any_sync(0xffffffffu, lane_bad)) {
@@ -362,150 +442,220 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                     words[q] = __reduce_or_sync(0xffffffffu, m);
                 }
             }
-            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, here)) * uint32_t(span) * D * 2;
-            bool ok = true;
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const int s = issued % A.slots;
-                if (issued >= A.slots)
-                    ok = wait_or_give_up(&C.empty[s], (issued / A.slots - 1) & 1, A.wait_ns, gave_up);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) {
-                    if (kv == 0)
-                        for (int q = 0; q < 4; ++q) C.bad[i % kWords][q] = words[q];
-                    mbar_arrive_expect_tx(&C.full[s], bytes);
-                }
-                __syncwarp();
-                if (here) {
-                    const CUtensorMap *map = kv ? &v_map : &k_map;
-                    const uint32_t dst = ring + s * kSlotBytes + lane * span * 128;
-#pragma unroll
-                    for (int hf = 0; hf < kHalves; ++hf) {
-                        if (A.box)
-                            tma_load_4d(dst + hf * kHalfBytes, map, &C.full[s], hf * 64, slot_in_page,
-                                        w.h, row[0]);
-                        else
-                            tma_gather4(dst + hf * kHalfBytes, map, &C.full[s],
-                                        w.h * A.head_x + hf * 64, row[0], row[1], row[2], row[3]);
+            // the boxes to copy: a run of lanes
+            const uint32_t run = __ballot_sync(0xffffffffu, here);
+            const int box_lo = __ffs(run) - 1, box_n = __popc(run);
+            const uint32_t bytes = box_n * uint32_t(span) * D * 2;
+            int *const rows = C.row[is_v][i & 1];
+            if (A.box) rows[lane] = row[0];
+            else *reinterpret_cast<int4 *>(rows + 4 * lane) = make_int4(row[0], row[1], row[2], row[3]);
+            const int slot = slot0 + r.slot;
+            if (i >= my_slots) ok = wait_or_give_up(&C.empty[slot], r.phase ^ 1, A.wait_ns, gave_up);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (!is_v && lane == 0)
+                *reinterpret_cast<uint4 *>(C.bad[i % kWords]) = make_uint4(words[0], words[1], words[2], words[3]);
+            __syncwarp();
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&C.full[slot], bytes);
+                uint32_t dst = ring + slot * kSlotBytes + box_lo * span * 128;
+                if (A.box) {
+                    const int first_key = tile0 + box_lo * span;
+                    int in_page = first_key - page_of(A, first_key) * A.page_size;
+#pragma unroll 4
+                    for (int j = box_lo; j < box_lo + box_n; ++j) {
+                        const int page = rows[j];
+                        tma_load_4d(dst, map, &C.full[slot], 0, in_page, u.h, page);
+                        if (kHalves == 2) tma_load_4d(dst + kHalfBytes, map, &C.full[slot], 64, in_page, u.h, page);
+                        dst += span * 128;
+                        in_page += span;
+                        if (in_page == A.page_size) in_page = 0;
+                    }
+                } else {
+                    const int x0 = u.h * A.head_x;
+#pragma unroll 4
+                    for (int j = box_lo; j < box_lo + box_n; ++j) {
+                        const int4 k = *reinterpret_cast<const int4 *>(rows + 4 * j);
+                        tma_gather4(dst, map, &C.full[slot], x0, k.x, k.y, k.z, k.w);
+                        if (kHalves == 2) tma_gather4(dst + kHalfBytes, map, &C.full[slot], x0 + 64, k.x, k.y, k.z, k.w);
+                        dst += span * 128;
                     }
                 }
-                ++issued;
             }
-            if (!ok) break;
-            w = x;
+            __syncwarp();
+            ++issued;
+            r.next(my_slots);
+            if (first && !is_v) {
+                // The unit's queries: one box per row, its G heads side by side.
+                if (units > A.two_q) ok = wait_or_give_up(&C.q_empty[rq.slot], rq.phase ^ 1, A.wait_ns, gave_up);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&C.q_full[rq.slot], uint32_t(u.ncols) * D * 2);
+                    uint32_t dst = q_smem + rq.slot * q_bytes;
+                    const int row0 = u.q.row0 + u.j0, nrows = u.ncols / A.G;
+                    for (int j = 0; j < nrows; ++j) {
+                        tma_load_3d(dst, &q_map, &C.q_full[rq.slot], 0, u.h * A.G, row0 + j);
+                        if (kHalves == 2) tma_load_3d(dst + q_half, &q_map, &C.q_full[rq.slot], 64, u.h * A.G, row0 + j);
+                        dst += A.G * 128;
+                    }
+                }
+                __syncwarp();
+                rq.next(1 + A.two_q);
+                ++units;
+            }
+            first = tx == 0;
+            u = x;
+            t = tx;
             ids = ahead;
         }
         if (C.gave_up) {
-            // Let the copies in flight land before the CTA ends.
-            for (int k = max(issued - A.slots, 0); k < issued; ++k)
-                mbar_wait_bounded(&C.full[k % A.slots], (k / A.slots) & 1, kDrainTimeoutNs);
+            // Let the copies in flight land before the CTA ends: this warp's
+            // latest copy to each slot, and the queries'.
+            for (int k = max(issued - my_slots, 0); k < issued; ++k)
+                mbar_wait_bounded(&C.full[slot0 + k % my_slots], (k / my_slots) & 1, kDrainTimeoutNs);
+            for (int k = max(units - 1 - A.two_q, 0); k < units; ++k)
+                mbar_wait_bounded(&C.q_full[A.two_q ? k & 1 : 0], (A.two_q ? k >> 1 : k) & 1, kDrainTimeoutNs);
         }
-    } else if (left > 0 && warp == 5) {
-        // ---- MMA issuer -----------------------------------------------------
-        if (lane == 0) {
-            const uint32_t s_tm = tmem + kColS, o_tm = tmem + kColO, l_tm = tmem + kColL;
-            bool first = true, ok = true;
-            int unit = 0;
-            const uint64_t ones_desc = smem_desc(ones, 0, 0);
-            for (int i = 0; i < left; ++i) {
-                const int N = (w.ncols(A) + 15) & ~15;
-                const uint32_t id_s = mma_idesc(128, N, false, false);
-                const uint32_t id_o = mma_idesc(128, N, true, true);
-                const uint32_t id_l = mma_idesc(128, N, false, true);
-                const int ks = (2 * i) % A.slots, vs = (2 * i + 1) % A.slots;
-                if (first) ok = wait_or_give_up(&C.q_full, unit & 1, A.wait_ns, gave_up);
-                ok = ok && wait_or_give_up(&C.full[ks], ((2 * i) / A.slots) & 1, A.wait_ns, gave_up);
-                if (!ok) break;
+    } else if (tiles > 0 && warp == kWarpMma) {
+        // ---- MMA issuer: S of the next tile and O, L of this one, whichever's
+        // operands are there ----------------------------------------------------
+        const uint64_t kd0 = smem_desc(ring, 16, 1024), qd0 = smem_desc(q_smem, 16, 1024);
+        // D = 64: the second group of 64 rows repeats the first
+        const uint64_t vd0 = smem_desc(ring + A.k_slots * kSlotBytes, kHalves == 2 ? kHalfBytes : 0, 1024);
+        const uint64_t pd0 = smem_desc32(p_smem, kPGroup, 256), ones_d = smem_desc(ones, 0, 0);
+        Unit us = u, uo = u;         // units of the next S and of the next O
+        int ts = t, to = t;
+        Ring rk, rv, rq;
+        const int v_slots = A.slots - A.k_slots;
+        bool first_s = true, first_o = true;
+        int si = 0, oi = 0;          // S and O tiles issued
+        uint32_t id_s = 0, id_o = 0, id_l = 0;
+        uint64_t since = 0;
+        uint32_t polls = 0;
+        while (oi < tiles) {
+            if (si < tiles && si <= oi + A.two_s && (!first_s || warp_test(&C.q_full[rq.slot], rq.phase)) &&
+                warp_test(&C.full[rk.slot], rk.phase)) {
+                if (first_s) id_s = mma_idesc(128, (us.ncols + 15) & ~15, false, false);
+                const int buf = A.two_s ? si & 1 : 0;
+                const bool last = ts + 1 == us.q.nt || si + 1 == tiles;
                 tc_fence_after();
-                mbar_arrive(&C.s_full);  // passes the producer's words on
-                const uint32_t kb = ring + ks * kSlotBytes;
+                if (elect_one()) {
+                    mbar_arrive(&C.s_full[buf]);  // passes the producer's words on
+                    const uint64_t kd = kd0 + uint32_t(rk.slot) * (kSlotBytes >> 4);
+                    const uint64_t qd = qd0 + uint32_t(rq.slot) * (q_bytes >> 4);
 #pragma unroll
-                for (int d = 0; d < D / 16; ++d) {
-                    const uint32_t in = (d % 4) * 32;
-                    mma_ss(s_tm, smem_desc(kb + (d / 4) * kHalfBytes + in, 16, 1024),
-                           smem_desc(q_smem + (d / 4) * q_half + in, 16, 1024), id_s, d > 0);
+                    for (int d = 0; d < D / 16; ++d)
+                        mma_ss(tmem + buf * A.ncap, kd + (((d / 4) * kHalfBytes + (d % 4) * 32) >> 4),
+                               qd + (((d / 4) * q_half + (d % 4) * 32) >> 4), id_s, d > 0);
+                    mma_commit(&C.s_full[buf]);
+                    mma_commit(&C.empty[rk.slot]);
+                    if (last) mma_commit(&C.q_empty[rq.slot]);
                 }
-                mma_commit(&C.empty[ks]);
-                mma_commit(&C.s_full);
-                ok = wait_or_give_up(&C.p_full, i & 1, A.wait_ns, gave_up) &&
-                     wait_or_give_up(&C.full[vs], ((2 * i + 1) / A.slots) & 1, A.wait_ns, gave_up);
-                if (!ok) break;
+                __syncwarp();
+                rk.next(A.k_slots);
+                first_s = last;
+                if (last) {
+                    rq.next(1 + A.two_q);
+                    if (si + 1 < tiles) us.next(A);
+                    ts = 0;
+                } else {
+                    ++ts;
+                }
+                ++si;
+                polls = 0;
+                continue;
+            }
+            const int pb = A.two_p ? oi & 1 : 0;
+            if (oi < si && warp_test(&C.p_full[pb], (A.two_p ? oi >> 1 : oi) & 1) && warp_test(&C.full[A.k_slots + rv.slot], rv.phase)) {
+                if (first_o) {
+                    const int N = (uo.ncols + 15) & ~15;
+                    id_o = mma_idesc(128, N, true, true);
+                    id_l = mma_idesc(128, N, false, true);
+                }
                 tc_fence_after();
-                const uint32_t vb = ring + vs * kSlotBytes;
-                // D = 64: the second group of 64 rows repeats the first
-                const uint32_t v_lbo = kHalves == 2 ? kHalfBytes : 0;
+                if (elect_one()) {
+                    const uint64_t vd = vd0 + uint32_t(rv.slot) * (kSlotBytes >> 4);
+                    const uint64_t pd = pd0 + uint32_t(pb) * (p_bytes >> 4);
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k) {
-                    const uint64_t pd = smem_desc(p_smem + k * 2048, kHalfBytes, 1024);
-                    mma_ss(o_tm, smem_desc(vb + k * 2048, v_lbo, 1024), pd, id_o, !(first && k == 0));
-                    mma_ss(l_tm, ones_desc, pd, id_l, !(first && k == 0));
-                }
-                mma_commit(&C.empty[vs]);
-                mma_commit(&C.pv_done);
-                const int t = w.t;
-                if (i + 1 < left) w.next(A);
-                first = w.t != t + 1;
-                if (first) ++unit;
-            }
-            if (C.gave_up) {
-                mma_commit(&C.drained);
-                mbar_wait_bounded(&C.drained, 0, kDrainTimeoutNs);
-            }
-        }
-        __syncwarp();
-    } else if (left > 0) {
-        // ---- softmax: thread = key of the tile ---------------------------------
-        const uint32_t lane_tm = tmem + (uint32_t(warp * 32) << 16);
-        bool first = true;
-        int unit = 0, unit_tile0 = 0;
-        bool ok = true;
-        for (int i = 0; i < left; ++i) {
-            const int c0 = w.c0(), ncols = w.ncols(A), N = (ncols + 15) & ~15;
-            if (first) {
-                unit_tile0 = w.t;
-                // The block's queries, K-major; columns past the last are zeros.
-                constexpr int kChunks = D / 8;
-                for (int e = tid; e < N * kChunks; e += kSoftThreads) {
-                    const int n = e / kChunks, ch = e % kChunks;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (n < ncols) {
-                        const int c = c0 + n, j = c / A.G, g = c - j * A.G;
-                        x = *reinterpret_cast<const uint4 *>(
-                            A.q + ((int64_t)(w.q.row0 + j) * A.Hq + w.h * A.G + g) * D + ch * 8);
+                    for (int k = 0; k < kTile / 16; ++k) {
+                        mma_ss(tmem + col_o, vd + k * (2048 >> 4), pd + k * (512 >> 4), id_o, !(first_o && k == 0));
+                        mma_ss(tmem + col_l, ones_d, pd + k * (512 >> 4), id_l, !(first_o && k == 0));
                     }
-                    st_shared16(q_smem + (ch / 8) * q_half + n * 128 + (((ch % 8) ^ (n & 7)) << 4),
-                                x.x, x.y, x.z, x.w);
+                    mma_commit(&C.pv_done[pb]);
+                    mma_commit(&C.empty[A.k_slots + rv.slot]);
                 }
-                fence_async_shared();
-                mbar_arrive(&C.q_full);
+                __syncwarp();
+                rv.next(v_slots);
+                first_o = ++to == uo.q.nt;
+                if (first_o) {
+                    if (oi + 1 < tiles) uo.next(A);
+                    to = 0;
+                }
+                ++oi;
+                polls = 0;
+                continue;
             }
-            ok = wait_or_give_up(&C.s_full, i & 1, A.wait_ns, gave_up);
-            if (ok && !first) ok = wait_or_give_up(&C.pv_done, (i - 1) & 1, A.wait_ns, gave_up);
-            if (soft_any(!ok)) break;
-            tc_fence_after();
-
-            const int kbase = (w.q.t0 + w.t) * kTile, kpos = kbase + tid;
-            const uint4 bw = *reinterpret_cast<const uint4 *>(C.bad[i % kWords]);
-            const int jmin = c0 / A.G, jmax = (c0 + ncols - 1) / A.G;
-            const bool whole = (bw.x | bw.y | bw.z | bw.w) == 0 && kbase >= w.q.kbeg &&
-                               kbase + kTile <= w.q.kend && kbase + kTile - 1 <= w.q.pos0 + jmin &&
-                               (A.window == 0 || (long long)kbase > (long long)w.q.pos0 + jmax - A.window);
-            int lo = 0, hi = N;
-            if (!whole) {
-                const uint32_t word = warp == 0 ? bw.x : warp == 1 ? bw.y : warp == 2 ? bw.z : bw.w;
-                visible_columns(A, w, c0, ncols, kpos, (word >> lane) & 1, lo, hi);
-                // Masked keys must not reach O through 0 * infinity: a value
-                // row that no column sees is cleared, and one that some
-                // columns see loses its NaN and infinities, which the
-                // epilogue adds to the columns that do see them.
-                const int vs = (2 * i + 1) % A.slots;
-                ok = wait_or_give_up(&C.full[vs], ((2 * i + 1) / A.slots) & 1, A.wait_ns, gave_up);
-                if (soft_any(!ok)) break;
-                if (lo > 0 || hi < ncols) {
-                    const uint32_t vb = ring + vs * kSlotBytes + tid * 128;
-                    for (int ch = 0; ch < 8 * kHalves; ++ch) {
-                        const uint32_t at = vb + (ch / 8) * kHalfBytes + (((ch % 8) ^ (tid & 7)) << 4);
+            if (polls == 0) since = global_timer_ns();
+            if ((++polls & 63u) == 0) {
+                const bool over = *gave_up || global_timer_ns() - since > A.wait_ns;
+                if (__any_sync(0xffffffffu, over)) {
+                    *gave_up = 1;
+                    break;
+                }
+            }
+        }
+        if (C.gave_up) {
+            if (elect_one()) mma_commit(&C.drained);
+            __syncwarp();
+            mbar_wait_bounded(&C.drained, 0, kDrainTimeoutNs);
+        }
+    } else if (tiles > 0) {
+        // ---- softmax: thread = key of the tile -----------------------------------
+        // Once a wait has given up, the others return at once and the loop
+        // runs to its end on whatever there is; the status tells.
+        const int key = tid & 127, grp = tid >> 7;
+        const uint32_t lane_tm = tmem + (uint32_t((warp & 3) * 32) << 16);
+        const int swz = key & 7, p_swz = (key >> 2) & 1;
+        Ring rv;
+        const int v_slots = A.slots - A.k_slots;
+        int i = 0;  // tile of the CTA
+        for (bool first_unit = true; i < tiles; first_unit = false) {
+            const int N = (u.ncols + 15) & ~15, t_first = t;
+            const int here = min(u.q.nt - t, tiles - i);
+            // tiles that every column sees in full: [whole_lo, whole_hi)
+            const int whole_hi = min(u.q.kend, u.q.pos0 + u.j0 + 1) / kTile;
+            const int last_beg = A.window > 0 ? max(u.q.pos0 + u.j0 + u.ncols / A.G - A.window, u.q.kbeg) : u.q.kbeg;
+            const int whole_lo = (last_beg + kTile - 1) / kTile;
+            for (int k = 0; k < here; ++k, ++t, ++i) {
+                const bool first = k == 0;
+                const int buf = A.two_s ? i & 1 : 0;
+                const uint32_t s_tm = lane_tm + buf * A.ncap;
+                wait_or_give_up(&C.s_full[buf], (A.two_s ? i >> 1 : i) & 1, A.wait_ns, gave_up);
+                tc_fence_after();
+                const int tile = u.q.t0 + t;
+                const uint4 bw = *reinterpret_cast<const uint4 *>(C.bad[i % kWords]);
+                const bool whole = (bw.x | bw.y | bw.z | bw.w) == 0 && tile >= whole_lo && tile < whole_hi;
+                int lo = 0, hi = N;
+                if (!whole) {
+                    const int q = warp & 3;
+                    const uint32_t word = q == 0 ? bw.x : q == 1 ? bw.y : q == 2 ? bw.z : bw.w;
+                    visible_columns(A, u, tile * kTile + key, (word >> lane) & 1, lo, hi);
+                }
+                bool move = first;
+                const int pb = A.two_p ? i & 1 : 0;
+                const uint32_t p_row = p_smem + pb * p_bytes + key * 32;
+                if (i > A.two_p)  // P's last reader
+                    wait_or_give_up(&C.pv_done[pb], ((A.two_p ? i >> 1 : i) - 1) & 1, A.wait_ns, gave_up);
+                if (!whole && (lo > 0 || hi < u.ncols)) {
+                    // Masked keys must not reach O through 0 * infinity: a
+                    // value row that no column sees is cleared, and one that
+                    // some see loses its NaN and infinities, which are added
+                    // at the unit's end to the columns that do see them.
+                    wait_or_give_up(&C.full[A.k_slots + rv.slot], rv.phase, A.wait_ns, gave_up);
+                    const uint32_t vb = ring + (A.k_slots + rv.slot) * kSlotBytes + key * 128;
+                    for (int ch = grp; ch < 8 * kHalves; ch += 2) {
+                        const uint32_t at = vb + (ch / 8) * kHalfBytes + (((ch % 8) ^ swz) << 4);
                         if (lo >= hi) {
                             st_shared16(at, 0, 0, 0, 0);
                             continue;
@@ -519,159 +669,171 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                         }
                     }
                 }
-            }
+                rv.next(v_slots);
+                __syncwarp();
 
-            // Weights of the tile against the reference; a unit's first tile
-            // sets the reference before, a tile that passes it moves it.
-            bool move = first;
-            for (;;) {
-                if (move) {
-                    for (int n = 0; n < N; n += 16) {
-                        float s[16];
-                        tmem_ld16(s, lane_tm + kColS + n);
-                        tmem_wait_ld(s);
-                        float keep = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float x = s[e] * A.scale2;
-                            if (n + e < lo || n + e >= hi) x = -INFINITY;
-                            asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(x) : "f"(x));
-                            if (lane == e) keep = x;
-                        }
-                        if (lane < 16) C.colmax[warp][n + lane] = keep;
-                    }
-                    soft_sync();
-                    for (int n = tid; n < N; n += kSoftThreads) {
-                        const float old = first ? kRefMin : C.ref[n];
-                        const float now = fmaxf(fmaxf(fmaxf(C.colmax[0][n], C.colmax[1][n]),
-                                                      fmaxf(C.colmax[2][n], C.colmax[3][n])), old);
-                        C.ref[n] = n < ncols ? now : 0.f;  // the zero columns' scores
-                        C.fac[n] = exp2_approx(old - now);
-                    }
-                    soft_sync();
-                    if (!first) {
-                        for (int n = 0; n < N; n += 16) {
-                            float o[16], l[16];
-                            tmem_ld16(o, lane_tm + kColO + n);
-                            tmem_ld16(l, lane_tm + kColL + n);
-                            tmem_wait_ld(o);
-                            tmem_use16(l);
+                // Weights of the tile against the reference.  A unit's first
+                // tile sets the reference before, a tile that passes it by
+                // too much moves it and starts again (once: then none does).
+                for (int turn = 0; turn < 2; ++turn) {
+                    if (move) {
+                        if (!first && A.two_p)
+                            wait_or_give_up(&C.pv_done[pb ^ 1], ((i - 1) >> 1) & 1, A.wait_ns, gave_up);
+                        tc_fence_after();
+                        for (int n = 16 * grp; n < N; n += 32) {
+                            float s[16];
+                            tmem_ld16(s, s_tm + n);
+                            const uint32_t seen = seen16(n, lo, hi);
+                            tmem_wait_ld(s);
+                            float keep = 0.f;
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                o[e] *= C.fac[n + e];
-                                l[e] *= C.fac[n + e];
+                                float x = ((seen >> e) & 1) ? s[e] * A.scale2 : -INFINITY;
+                                asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(x) : "f"(x));
+                                if (lane == e) keep = x;
                             }
-                            tmem_st16(lane_tm + kColO + n, o);
-                            tmem_st16(lane_tm + kColL + n, l);
+                            if (lane < 16) C.colmax[warp & 3][n + lane] = keep;
                         }
-                        tmem_wait_st();
-                    }
-                }
-                float top = 0.f;
-                for (int n = 0; n < N; n += 16) {
-                    float s[16];
-                    tmem_ld16(s, lane_tm + kColS + n);
-                    float ref[16];
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        *reinterpret_cast<float4 *>(ref + e) = *reinterpret_cast<const float4 *>(C.ref + n + e);
-                    tmem_wait_ld(s);
-                    uint32_t p[8];
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float x = fmaf(s[e], A.scale2, -ref[e]), y = fmaf(s[e + 1], A.scale2, -ref[e + 1]);
-                        if (!whole) {
-                            if (n + e < lo || n + e >= hi) x = -INFINITY;
-                            if (n + e + 1 < lo || n + e + 1 >= hi) y = -INFINITY;
+                        soft_sync();
+                        for (int n = tid; n < N; n += kSoftThreads) {
+                            const float old = first ? kRefMin : C.ref[n];
+                            const float now = fmaxf(fmaxf(fmaxf(C.colmax[0][n], C.colmax[1][n]),
+                                                          fmaxf(C.colmax[2][n], C.colmax[3][n])), old);
+                            // the columns past the last weigh nothing
+                            C.ref[n] = n < u.ncols ? now : INFINITY;
+                            C.fac[n] = exp2_approx(old - now);
                         }
-                        top = fmaxf(top, fmaxf(x, y));
-                        p[e / 2] = pack_bf16x2(exp2_approx(x), exp2_approx(y));
+                        soft_sync();
+                        if (!first) {
+                            for (int n = 16 * grp; n < N; n += 32) {
+                                float o[16], l[16];
+                                tmem_ld16(o, lane_tm + col_o + n);
+                                tmem_ld16(l, lane_tm + col_l + n);
+                                tmem_wait_ld(o);
+                                tmem_use16(l);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    o[e] *= C.fac[n + e];
+                                    l[e] *= C.fac[n + e];
+                                }
+                                tmem_st16(lane_tm + col_o + n, o);
+                                tmem_st16(lane_tm + col_l + n, l);
+                            }
+                            tmem_wait_st();
+                        }
                     }
-                    const uint32_t at = p_smem + (n / 64) * kHalfBytes + tid * 128;
-                    const int ch = (n % 64) / 8;
-                    st_shared16(at + ((ch ^ (tid & 7)) << 4), p[0], p[1], p[2], p[3]);
-                    st_shared16(at + (((ch + 1) ^ (tid & 7)) << 4), p[4], p[5], p[6], p[7]);
+                    // two chunks of 16 columns in turn: one loads while the other is weighed
+                    float top = 0.f;
+                    float s0[16], s1[16];
+                    int n = 16 * grp;
+                    if (n < N) tmem_ld16(s0, s_tm + n);
+                    for (; n < N; n += 64) {
+                        const uint32_t at = p_row + (n / 16) * kPGroup;
+                        const bool more = n + 32 < N;
+                        tmem_wait_ld(s0);
+                        if (more) tmem_ld16(s1, s_tm + n + 32);
+                        top = fmaxf(top, whole ? weigh16<false>(s0, C.ref + n, A.scale2, 0, at, p_swz)
+                                               : weigh16<true>(s0, C.ref + n, A.scale2, seen16(n, lo, hi), at, p_swz));
+                        if (!more) break;
+                        tmem_wait_ld(s1);
+                        if (n + 64 < N) tmem_ld16(s0, s_tm + n + 64);
+                        top = fmaxf(top, whole ? weigh16<false>(s1, C.ref + n + 32, A.scale2, 0, at + 2 * kPGroup, p_swz)
+                                               : weigh16<true>(s1, C.ref + n + 32, A.scale2, seen16(n + 32, lo, hi),
+                                                               at + 2 * kPGroup, p_swz));
+                    }
+                    fence_async_shared();
+                    tc_fence_before();
+                    move = soft_any(top > kRefSlack);
+                    if (!move) break;
                 }
-                fence_async_shared();
-                tc_fence_before();
-                move = soft_any(top > kRefSlack);
-                if (!move) break;
-                first = false;  // O and L hold earlier tiles, or nothing that counts yet
+                if (tid == 0) mbar_arrive(&C.p_full[pb]);
             }
-            if (tid == 0) mbar_arrive(&C.p_full);
 
-            // ---- the unit's end in this CTA ----------------------------------
-            const Walk u = w;
-            if (i + 1 < left) w.next(A);
-            const bool done = i + 1 == left || w.t != u.t + 1;
-            first = done;
-            if (!done) continue;
-            ++unit;
-            ok = wait_or_give_up(&C.pv_done, i & 1, A.wait_ns, gave_up);
-            if (soft_any(!ok)) break;
+            // ---- the unit's end in this CTA --------------------------------------
+            wait_or_give_up(&C.pv_done[A.two_p ? (i - 1) & 1 : 0], (A.two_p ? (i - 1) >> 1 : i - 1) & 1,
+                            A.wait_ns, gave_up);
             tc_fence_after();
-            const bool split = unit_tile0 > 0 || u.t + 1 < u.q.nt;
-            const int d = D == 128 ? tid : tid % 64;
-            const bool writer = tid < D;
+            const bool split = t_first > 0 || t < u.q.nt;
+            const int d = key % D;
+            const bool writer = key < D;
             // the unit at the CTA's start uses the first of its two slots
-            const int slot = 2 * int(me) + (unit == 1 ? 0 : 1);
-            const bool poison = C.poison;
-            int j = u.c0() / A.G, g = u.c0() % A.G;
-            uint16_t *out = A.out + ((int64_t)(u.q.row0 + j) * A.Hq + u.h * A.G + g) * D + d;
-            float *part = A.part + (int64_t)slot * A.ncap * D + d;
-            for (int n = 0; n < N; n += 16) {
+            const int slot = 2 * int(me) + (first_unit ? 0 : 1);
+            uint16_t *const out0 = A.out + ((int64_t)(u.q.row0 + u.j0) * A.Hq + u.h * A.G) * D + d;
+            float *const part0 = A.part + (int64_t)slot * A.ncap * D + d;
+            const int wrap = (A.Hq - A.G) * D;
+            for (int n = 16 * grp; n < N; n += 32) {
                 float o[16], l[16];
-                tmem_ld16(o, lane_tm + kColO + n);
-                tmem_ld16(l, lane_tm + kColL + n);
+                tmem_ld16(o, lane_tm + col_o + n);
+                tmem_ld16(l, lane_tm + col_l + n);
                 tmem_wait_ld(o);
                 tmem_use16(l);
+                const int m = min(16, u.ncols - n);
+                if (split) {
+                    float *part = part0 + (int64_t)n * D;
+                    float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    if (n + e >= ncols) break;
-                    float x = o[e];
-                    if (poison) {
-                        // keys of this CTA's tiles that some columns see and others do not
-                        const int k0 = max((u.q.t0 + unit_tile0) * kTile, u.q.kbeg);
-                        const int k1 = min((u.q.t0 + u.t + 1) * kTile, u.q.kend);
-                        for (int key = k0; key < k1; ++key) {
-                            int vlo, vhi;
-                            visible_columns(A, u, u.c0(), ncols, key, false, vlo, vhi);
-                            if (vlo == 0 && vhi == ncols) continue;
-                            if (n + e < vlo || n + e >= vhi) continue;
-                            const int page = A.block_table[(int64_t)u.b * A.max_pages + key / A.page_size];
-                            if (page < 0 || page >= A.num_pages) continue;
-                            const float v = bf16_lo(A.v_cache[page * A.page_stride + (key % A.page_size) * A.slot_stride +
-                                                              u.h * A.head_stride + d]);
-                            if (!isfinite(v)) x += v;
+                    for (int e = 0; e < 16; ++e) {
+                        if (e < m && writer) part[e * D] = o[e];
+                        if (lane == e) sum = l[e];
+                    }
+                    if (lane < m && (warp & 3) == 0) {
+                        A.stat[((int64_t)slot * 2) * A.ncap + n + lane] = C.ref[n + lane];
+                        A.stat[((int64_t)slot * 2 + 1) * A.ncap + n + lane] = sum;
+                    }
+                } else {
+                    int g = n % A.G;
+                    uint16_t *out = out0 + (int64_t)(n / A.G) * A.Hq * D + g * D;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float y = l[e] == 0.f ? 0.f : __fdividef(o[e], l[e]);
+                        if (e < m && writer) *out = uint16_t(pack_bf16x2(y, 0.f));
+                        out += D;
+                        if (++g == A.G) {
+                            g = 0;
+                            out += wrap;
                         }
                     }
-                    if (split) {
-                        if (writer) part[(int64_t)(n + e) * D] = x;
-                        if (tid == 0) {
-                            A.stat[((int64_t)slot * 2) * A.ncap + n + e] = C.ref[n + e];
-                            A.stat[((int64_t)slot * 2 + 1) * A.ncap + n + e] = l[e];
+                }
+            }
+            if (C.poison) soft_sync();  // the other group's outputs are written
+            if (C.poison && writer && grp == 0) {
+                // What was taken out of V: for the keys of this CTA's
+                // tiles that some columns see and others do not.
+                const int k0 = max((u.q.t0 + t_first) * kTile, u.q.kbeg);
+                const int k1 = min((u.q.t0 + t) * kTile, u.q.kend);
+                for (int k = k0; k < k1; ++k) {
+                    int vlo, vhi;
+                    visible_columns(A, u, k, false, vlo, vhi);
+                    if (vlo >= vhi || (vlo == 0 && vhi == u.ncols)) continue;
+                    const int page = A.block_table[(int64_t)u.b * A.max_pages + k / A.page_size];
+                    if (page < 0 || page >= A.num_pages) continue;
+                    const float v = bf16_lo(A.v_cache[page * A.page_stride + (k % A.page_size) * A.slot_stride +
+                                                      u.h * A.head_stride + d]);
+                    if (isfinite(v)) continue;
+                    for (int n = vlo; n < vhi; ++n) {
+                        if (split) {
+                            part0[(int64_t)n * D] += v;
+                        } else {
+                            uint16_t *y = out0 + (int64_t)(n / A.G) * A.Hq * D + (n % A.G) * D;
+                            *y = uint16_t(pack_bf16x2(bf16_lo(*y) + v, 0.f));
                         }
-                    } else {
-                        const float y = l[e] == 0.f ? 0.f : x / l[e];
-                        if (writer) *out = uint16_t(pack_bf16x2(y, 0.f));
-                    }
-                    out += D;
-                    if (++g == A.G) {
-                        g = 0;
-                        out += (int64_t)(A.Hq - A.G) * D;
                     }
                 }
             }
             tc_fence_before();
             soft_sync();  // ref, poison and O are read before the next unit writes them
             if (tid == 0) C.poison = 0;
+            if (i < tiles) {
+                u.next(A);
+                t = 0;
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && C.gave_up) atomicOr(A.status, kStatusWaitTimeout);
-    if (warp == 5) tmem_free(tmem, kTmemCols);
+    if (warp == kWarpMma) tmem_free(tmem, kTmemCols);
 }
 
 // Adds the partial sums of the units that were cut, in the order of the keys.
@@ -716,7 +878,7 @@ __global__ void __launch_bounds__(kJoinThreads) step_join_kernel(const StepArgs 
                 for (int e = 0; e < E; ++e) acc[e] += f * p[e];
             }
         }
-        const int c = ci.c0 + n, j = c / A.G, g = c - j * A.G;
+        const int j = n / A.G, g = n - j * A.G;
         uint32_t *out = reinterpret_cast<uint32_t *>(A.out + ((int64_t)(ci.row0 + j) * A.Hq + ci.head0 + g) * D + lane * E);
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -724,24 +886,36 @@ __global__ void __launch_bounds__(kJoinThreads) step_join_kernel(const StepArgs 
     }
 }
 
+// Rows of a unit at most: those whose columns fit.
+int step_rows(int Hq, int Hkv, int q_max) { return std::min(q_max, kMaxCols / (Hq / Hkv)); }
 int step_columns(int Hq, int Hkv, int q_max) {
-    const long long cols = (long long)q_max * (Hq / Hkv);
-    return int(std::min<long long>((cols + 15) / 16 * 16, kMaxCols));
+    return (step_rows(Hq, Hkv, q_max) * (Hq / Hkv) + 15) / 16 * 16;
 }
 
 constexpr size_t kHeaderBytes = 256 + (sizeof(CutInfo) * kAttnMaxCtas + 255) / 256 * 256;
 
 template <int D>
-cudaError_t launch(StepArgs A, const CUtensorMap &km, const CUtensorMap &vm, int ctas, cudaStream_t s) {
+cudaError_t launch(StepArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStream_t s) {
+    // S, P and Q are held twice where two slots for K and two for V remain: P
+    // before Q, since a tile's products need P and only a unit's first tile Q.
+    A.two_s = A.ncap <= kTwoS;
     const size_t slot = size_t(D) * 2 * kTile;
-    const size_t fixed = 2048 + size_t((A.ncap + 63) / 64) * kTile * 128 + size_t(A.ncap) * D * 2;
-    const size_t room = 232448 - sizeof(Ctrl) - 256 - fixed;
-    A.slots = int(std::min<size_t>(room / slot, kMaxSlots));
-    const size_t smem = fixed + A.slots * slot;
+    const size_t p = size_t(A.ncap / 16) * kPGroup, q = size_t(A.ncap) * D * 2;
+    const size_t room = kSmemBytes - sizeof(Ctrl) - 256 - 2048;
+    size_t fixed = 0;
+    for (int twice = 2; twice >= 0; --twice) {
+        A.two_p = A.two_s && twice >= 1;
+        A.two_q = twice == 2;
+        fixed = p * (1 + A.two_p) + q * (1 + A.two_q);
+        if (fixed + 4 * slot <= room) break;
+    }
+    A.slots = int(std::min<size_t>((room - fixed) / slot, kMaxSlots));
+    A.k_slots = A.slots / 2;
+    const size_t smem = 2048 + fixed + A.slots * slot;
     cudaError_t e = cudaFuncSetAttribute(step_attention_kernel<D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    step_attention_kernel<D><<<ctas, kThreadsStep, smem, s>>>(A, km, vm);
+    step_attention_kernel<D><<<ctas, kThreadsStep, smem, s>>>(A, maps[0], maps[1], maps[2]);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (ctas == 1) return cudaSuccess;
     cudaLaunchConfig_t cfg{};
@@ -792,10 +966,13 @@ cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_n
     A.B = a.B; A.rows = a.rows; A.q_max = a.q_max; A.Hq = a.Hq; A.Hkv = a.Hkv; A.G = a.Hq / a.Hkv;
     A.page_size = a.page_size; A.num_pages = a.num_pages; A.max_pages = a.max_pages;
     A.window = a.window;
+    A.page_shift = 31;  // exact below 2^31: page_mul = ceil(2^shift / page_size) < 2^32
+    while ((1u << (A.page_shift - 31)) < unsigned(a.page_size)) ++A.page_shift;
+    A.page_mul = uint32_t(((1ull << A.page_shift) + a.page_size - 1) / a.page_size);
     A.ncap = step_columns(a.Hq, a.Hkv, a.q_max);
+    A.rows_cap = step_rows(a.Hq, a.Hkv, a.q_max);
     A.scale2 = float(double(a.scale) * 1.4426950408889634);
     A.page_stride = a.page_stride; A.slot_stride = a.slot_stride; A.head_stride = a.head_stride;
-    A.q = static_cast<const uint16_t *>(a.q_rot);
     A.v_cache = static_cast<const uint16_t *>(a.v_cache);
     A.row_off = a.row_off; A.seq_lens = a.seq_lens; A.block_table = a.block_table;
     A.out = static_cast<uint16_t *>(a.out);
@@ -809,7 +986,14 @@ cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_n
 
     // A page of 8 k positions is copied in boxes of whole pages or parts of
     // them; other pages key by key (four keys a copy).
-    CUtensorMap maps[2];
+    CUtensorMap maps[3];
+    {
+        const uint64_t dims[3] = {uint64_t(a.D), uint64_t(a.Hq), uint64_t(a.rows)};
+        const uint64_t st[2] = {uint64_t(a.D) * 2, uint64_t(a.D) * a.Hq * 2};
+        const uint32_t bx[3] = {64, uint32_t(A.G), 1};
+        const cudaError_t e = encode_map(&maps[0], a.q_rot, 3, dims, st, bx);
+        if (e != cudaSuccess) return e;
+    }
     const int box = gcd(a.page_size, kTile);
     const void *bases[2] = {a.k_cache, a.v_cache};
     if (box >= 8) {
@@ -818,7 +1002,7 @@ cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_n
         const uint64_t st[3] = {uint64_t(a.slot_stride) * 2, uint64_t(a.head_stride) * 2, uint64_t(a.page_stride) * 2};
         const uint32_t bx[4] = {64, uint32_t(box), 1, 1};
         for (int i = 0; i < 2; ++i) {
-            const cudaError_t e = encode_map(&maps[i], bases[i], 4, dims, st, bx);
+            const cudaError_t e = encode_map(&maps[1 + i], bases[i], 4, dims, st, bx);
             if (e != cudaSuccess) return e;
         }
     } else {
@@ -832,12 +1016,12 @@ cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_n
         const uint64_t st[1] = {uint64_t(row) * 2};
         const uint32_t bx[2] = {64, 1};
         for (int i = 0; i < 2; ++i) {
-            const cudaError_t e = encode_map(&maps[i], bases[i], 2, dims, st, bx);
+            const cudaError_t e = encode_map(&maps[1 + i], bases[i], 2, dims, st, bx);
             if (e != cudaSuccess) return e;
         }
     }
     const int ctas = std::min(sms, kAttnMaxCtas);
-    return a.D == 128 ? launch<128>(A, maps[0], maps[1], ctas, s) : launch<64>(A, maps[0], maps[1], ctas, s);
+    return a.D == 128 ? launch<128>(A, maps, ctas, s) : launch<64>(A, maps, ctas, s);
 }
 
 }  // namespace dspark

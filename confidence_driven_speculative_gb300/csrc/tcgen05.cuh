@@ -25,6 +25,26 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
            (uint64_t((sbo >> 4) & 0x3fff) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
+// The same for the 32-byte swizzle, MN-major: a row is one K index holding 16
+// entries (32 bytes), 16-byte chunk c of row r at chunk c ^ (r / 4 % 2).
+__device__ __forceinline__ uint64_t smem_desc32(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return uint64_t((addr >> 4) & 0x3fff) | (uint64_t((lbo >> 4) & 0x3fff) << 16) |
+           (uint64_t((sbo >> 4) & 0x3fff) << 32) | (uint64_t(1) << 46) | (uint64_t(6) << 61);
+}
+
+// One lane of the warp, chosen so that the compiler knows it is one: the
+// operands of tcgen05.mma then stay in uniform registers (23 clocks an MMA
+// issued; 79 behind an ordinary test of the lane).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Instruction descriptor: bfloat16 A and B, fp32 accumulator.
 __host__ __device__ constexpr uint32_t mma_idesc(int M, int N, bool a_mn, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
@@ -152,8 +172,9 @@ __device__ __forceinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity, 
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     for (uint32_t it = 1;; ++it) {
+        if (*gave_up) return false;
         if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0 && (*gave_up || global_timer_ns() - t0 > limit_ns)) {
+        if ((it & 15u) == 0 && global_timer_ns() - t0 > limit_ns) {
             *gave_up = 1;
             return false;
         }

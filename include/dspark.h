@@ -358,8 +358,10 @@ dspark_status dspark_fit_sts_tau(int32_t N, int32_t gamma, const float *conf,
 /* Limits checked by the three calls. */
 #define DSPARK_MAX_HEADS 256
 #define DSPARK_MAX_ROWS (1 << 24)
-/* Rows of one request that dspark_step_attention takes (1 + gamma). */
+/* Rows of one request (1 + gamma) and query heads of one cached head that
+ * dspark_step_attention takes. */
 #define DSPARK_MAX_STEP_ROWS (DSPARK_MAX_GAMMA + 1)
+#define DSPARK_MAX_STEP_GROUP 128
 
 typedef struct dspark_attn {
     /* ---- shapes ---------------------------------------------------------- */
