@@ -746,6 +746,9 @@ dspark_status dspark_step_attention(const dspark_attn *a, dspark_stream_t stream
         return fail(DSPARK_EINVAL,
                     "%s: page_size=%d is not a multiple of 8, and page_stride or head_stride is not "
                     "a whole number of slots", fn, a->page_size);
+    if (!dspark::step_list_fits(*a))
+        return fail(DSPARK_EINVAL, "%s: B=%d Hkv=%d max_pages=%d is too large a batch", fn, a->B, a->Hkv,
+                    a->max_pages);
     DeviceInfo *dev;
     if ((st = device_info(&dev))) return st;
     cudaError_t e = dspark::launch_step_attention(*a, dev->sms, g_wait_ns.load(),

@@ -29,6 +29,7 @@
 // (o, m, l) in the workspace, in fp32, and step_join_kernel adds them in the order of
 // the keys, so the result does not depend on timing.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn.cuh"
 #include "dspark_internal.cuh"
@@ -43,22 +44,15 @@ constexpr int kTwoS = 128;      // up to so many, S is held twice
 constexpr uint32_t kPGroup = kTile * 32;  // P: 16 columns of 128 keys, rows of 32 bytes
 constexpr int kMaxSlots = 12;   // ring slots (one K or one V tile each)
 constexpr int kWords = 16;      // ring of the tiles' bad-key words
-constexpr int kSoftThreads = 256;  // two groups of 128: each takes every other 16 columns
-constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10;
-constexpr int kThreadsStep = 352;
+constexpr int kGroups = 4;          // softmax groups of 128 threads: each takes every fourth 16 columns
+constexpr int kSoftThreads = kGroups * kTile;
+constexpr int kWarpK = 16, kWarpV = 17, kWarpBoth = 18, kWarpMma = 19;
+constexpr int kThreadsStep = 640;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRefMin = -1e30f;  // reference of a column without a score yet
-constexpr float kRefSlack = 8.0f;  // log2: how far a score may pass the reference
-constexpr int kJoinThreads = 128;
+constexpr float kRefSlack = 32.0f; // log2: how far a score may pass the reference
+constexpr int kUnitCost = 2;           // what a unit costs beside its tiles, in tiles
 constexpr size_t kSmemBytes = 232448;  // shared memory of a CTA
-
-// What step_join_kernel needs of the unit that is cut before CTA i.
-struct CutInfo {
-    int32_t first, last;      // the CTAs that share it; first < i <= last, or last = -1: no cut
-    int32_t slot_first;       // partial slot of the first one (the others': 2 * CTA)
-    int32_t row0, head0;      // first packed row of the unit, first query head of the group
-    int32_t ncols;
-};
 
 struct StepArgs {
     int B, rows, q_max, Hq, Hkv, G;
@@ -67,6 +61,7 @@ struct StepArgs {
     int box;                   // keys of a TMA box (divides the page and the tile); 0: gather
     int ncap;                  // columns of a unit at most, a multiple of 16
     int rows_cap;              // rows of a unit at most
+    int unit_cost;             // what a unit costs beside its tiles, in tiles
     int slots, k_slots;        // ring slots; the first k_slots hold K tiles, the others V tiles
     int two_s, two_p, two_q;   // S, P, Q held twice
     int page_rows, head_rows;  // gather: rows of the 2-D view per page and head
@@ -78,7 +73,7 @@ struct StepArgs {
     uint16_t *out;
     float *part;               // [2 * CTAs][ncap][D]
     float *stat;               // [2 * CTAs][2][ncap]: reference, sum
-    CutInfo *cut;              // [CTAs]
+    int32_t *arrived;          // [CTAs] parts written of the unit that CTA i is the first of
     int32_t *status;
     uint64_t wait_ns;
 };
@@ -128,16 +123,13 @@ struct Unit {
         j0 = blk * q.per;
         ncols = min(q.per, q.n - j0) * A.G;
     }
-    // The unit of tile `off` of request b's list; returns the tile in it.
-    __device__ __forceinline__ int start(const StepArgs &A, int b_, long long off) {
+    // Unit `i` of request b's list.
+    __device__ __forceinline__ void start(const StepArgs &A, int b_, int i) {
         b = b_;
         q = load_req(A, b);
-        const int per_head = q.blocks * q.nt;
-        h = int(off / per_head);
-        const int rem = int(off % per_head);
-        blk = rem / q.nt;
+        h = i / q.blocks;
+        blk = i - h * q.blocks;
         shape(A);
-        return rem - blk * q.nt;
     }
     __device__ __forceinline__ void next(const StepArgs &A) {
         if (++blk == q.blocks) {
@@ -154,6 +146,26 @@ struct Unit {
     }
 };
 
+// A list of `total` places cut into parts of equal length, one place more to
+// the first ones: CTA i has start(i) .. start(i + 1).  No part is empty before
+// the last one that is not.
+struct Cuts {
+    int parts, each, more;
+    __device__ __forceinline__ Cuts(int total, int ctas) {
+        parts = min(ctas, max(total, 1));
+        each = total / parts;
+        more = total - each * parts;
+    }
+    __device__ __forceinline__ int start(int i) const {
+        i = min(i, parts);
+        return each * i + min(i, more);
+    }
+    __device__ __forceinline__ int of(int place) const {
+        const int longer = (each + 1) * more;
+        return place < longer ? place / (each + 1) : more + (place - longer) / each;
+    }
+};
+
 // Slot and phase of a ring walked in order.
 struct Ring {
     int slot = 0;
@@ -163,29 +175,35 @@ struct Ring {
     }
 };
 
+// A unit that was cut and whose last part this CTA wrote: it joins the parts.
+struct Join {
+    int row0, head0, ncols;             // its first packed row, first query head, columns
+    int slot0, first_cta, members;      // the first part's slot, the CTAs that share it
+};
+
 struct Ctrl {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t q_full[2], q_empty[2], s_full[2];
     uint64_t p_full[2], pv_done[2], drained;
     uint32_t tmem;
-    int gave_up, poison;
-    long long warp_total[kThreadsStep / 32];
-    long long start_base;
-    int start_b;
-    alignas(16) int row[2][2][kTile];     // producers: pages of the boxes, or rows of the keys
-    alignas(16) uint32_t bad[kWords][4];  // keys of a tile whose page is no memory
+    int gave_up, poison, joins;
+    Join join[2];
+    int warp_cost[kThreadsStep / 32], warp_units[kThreadsStep / 32];
+    int tiles_before[2];  // tiles of the list before this CTA's and up to its last
+    int start_b, start_unit, start_tile;
+    alignas(16) int row[2][kTile];        // producers (the third shares K's): pages of the boxes, or rows of the keys
+    alignas(16) uint32_t bad[2][kWords][4];  // (by K warp) keys of a tile whose page is no memory
     alignas(16) float ref[kMaxCols];
     alignas(16) float fac[kMaxCols];
-    alignas(16) float colmax[4][kMaxCols];
 };
 
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
 __device__ __forceinline__ bool soft_any(bool x) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 q, %1, 0;\n\t"
-        "barrier.cta.red.or.pred p, 1, 256, q;\n\t"
+        "barrier.cta.red.or.pred p, 1, 512, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r) : "r"(uint32_t(x)) : "memory");
     return r != 0;
@@ -226,15 +244,16 @@ __device__ __forceinline__ void visible_columns(const StepArgs &A, const Unit &u
     if (bad || kpos < u.q.kbeg || kpos >= u.q.kend) hi = lo;
 }
 
-// 16 columns of a tile: weights 2^(s * scale2 - ref), rounded, to P; returns
+// 16 columns of a tile, on their way from TMEM: weights 2^(s * scale2 - ref), rounded, to P; returns
 // the largest exponent.  Columns whose bit of `seen` is clear weigh nothing.
 template <bool kMasked>
-__device__ __forceinline__ float weigh16(const float (&s)[16], const float *ref, float scale2,
+__device__ __forceinline__ float weigh16(float (&s)[16], const float *ref, float scale2,
                                          uint32_t seen, uint32_t at, int swz) {
     float r[16];
 #pragma unroll
     for (int e = 0; e < 16; e += 4)
         *reinterpret_cast<float4 *>(r + e) = *reinterpret_cast<const float4 *>(ref + e);
+    tmem_wait_ld(s);
     uint32_t p[8];
     float top = 0.f;
 #pragma unroll
@@ -258,6 +277,78 @@ __device__ __forceinline__ uint32_t seen16(int n, int lo, int hi) {
     return ((1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
+// Adds the parts of a unit that was cut, in the order of the keys, on all warps of
+// the CTA that wrote its part last.  A warp takes kCols
+// columns at a time and asks for 4 / kCols parts of each before it knows
+// their weights.  kCols > 1: all parts are there at once (members <= 4 / kCols).
+template <int D, int kCols>
+__device__ __forceinline__ void join_columns(const StepArgs &A, const Join &J, int warp, int lane) {
+    constexpr int E = D / 32, kParts = 4 / kCols;
+    using Vec = typename std::conditional<E == 4, float4, float2>::type;
+    const int ncols = J.ncols, members = J.members;
+    uint16_t *const out0 = A.out + ((int64_t)J.row0 * A.Hq + J.head0) * D;
+    auto slot_of = [&](int k) { return k == 0 ? J.slot0 : 2 * (J.first_cta + k); };
+    const int my_k = lane % kParts, my_c = lane / kParts;  // lanes 0..3: one part of one column
+    for (int n0 = warp * kCols; n0 < ncols; n0 += kThreadsStep / 32 * kCols) {
+        float m = kRefMin, acc[kCols][E], l[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+            l[c] = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[c][e] = 0.f;
+        }
+        for (int k0 = 0; k0 < members; k0 += kParts) {
+            Vec x[kCols][kParts];
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+#pragma unroll
+                for (int k = 0; k < kParts; ++k)
+                    if (k0 + k < members && n0 + c < ncols)
+                        x[c][k] = __ldcg(reinterpret_cast<const Vec *>(
+                            A.part + ((int64_t)slot_of(k0 + k) * A.ncap + n0 + c) * D + lane * E));
+            float ref = kRefMin, sum = 0.f;
+            if (my_c < kCols && k0 + my_k < members && n0 + my_c < ncols) {
+                const float *st = A.stat + (int64_t)slot_of(k0 + my_k) * 2 * A.ncap + n0 + my_c;
+                ref = __ldcg(st);
+                sum = __ldcg(st + A.ncap);
+            }
+            float top = ref;
+#pragma unroll
+            for (int o = kParts / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float m_new = fmaxf(m, top);  // the lane's column's
+            const float w = exp2_approx(ref - m_new), f_old = exp2_approx(m - m_new);
+            m = m_new;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                const float f = __shfl_sync(0xffffffffu, f_old, c * kParts);
+                l[c] *= f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[c][e] *= f;
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) {
+                    const float wk = __shfl_sync(0xffffffffu, w, c * kParts + k);
+                    const float lk = __shfl_sync(0xffffffffu, sum, c * kParts + k);
+                    if (k0 + k < members && n0 + c < ncols) {
+                        l[c] = fmaf(wk, lk, l[c]);
+                        const float *v = reinterpret_cast<const float *>(&x[c][k]);
+#pragma unroll
+                        for (int e = 0; e < E; ++e) acc[c][e] = fmaf(wk, v[e], acc[c][e]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+            const int n = n0 + c;
+            if (n >= ncols) break;
+            uint32_t *out = reinterpret_cast<uint32_t *>(out0 + (int64_t)(n / A.G) * A.Hq * D + (n % A.G) * D + lane * E);
+            const float inv = l[c] == 0.f ? 0.f : 1.f / l[c];
+#pragma unroll
+            for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[c][e] * inv, acc[c][e + 1] * inv);
+        }
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreadsStep, 1)
 step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant__ CUtensorMap q_map,
@@ -268,7 +359,6 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
     extern __shared__ uint8_t dyn[];
     __shared__ Ctrl C;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = tid & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
 
     // Shared memory: ring, P and Q (once or twice), ones.
     const uint32_t ring = (smem_addr(dyn) + 1023) & ~1023u;
@@ -283,7 +373,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
     // ---- set-up: barriers, TMEM, the constant operand, the CTA's tiles -----
     if (tid == 0) {
         for (int s = 0; s < A.slots; ++s) {
-            mbar_init(&C.full[s], 1);
+            mbar_init(&C.full[s], 2);
             mbar_init(&C.empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -296,8 +386,9 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
         mbar_init(&C.drained, 1);
         C.gave_up = 0;
         C.poison = 0;
-        C.start_b = 0;
-        C.start_base = 0;
+        C.joins = 0;
+        C.start_b = C.start_unit = C.start_tile = 0;
+        C.tiles_before[0] = C.tiles_before[1] = 0;
         fence_barrier_init();
     }
     if (tid < 64) st_shared16(ones + tid * 16, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
@@ -309,83 +400,94 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
         prefetch_map(&v_map);
     }
 
+    // The list of all units' tiles, each unit with unit_cost further places in
+    // front for what it costs beside its tiles, is cut evenly.
+    const int U = A.unit_cost;
     const int per = (A.B + kThreadsStep - 1) / kThreadsStep;
     const int b_lo = min(tid * per, A.B), b_hi = min(b_lo + per, A.B);
-    long long mine = 0;
+    int my_cost = 0, my_units = 0;
     for (int b = b_lo; b < b_hi; ++b) {
         const Req r = load_req(A, b);
-        mine += (long long)r.blocks * r.nt * A.Hkv;
+        my_units += r.blocks * A.Hkv;
+        my_cost += r.blocks * A.Hkv * (r.nt + U);
     }
-    long long incl = mine;
+    int cost = my_cost, units = my_units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-    }
-    if (lane == 31) C.warp_total[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < kThreadsStep / 32; ++w) {
-        if (w < warp) before += C.warp_total[w];
-        total += C.warp_total[w];
-    }
-    // every CTA that takes part has a tile
-    const long long ctas = min((long long)gridDim.x, max(total, 1ll)), me = blockIdx.x;
-    const long long start = me < ctas ? total * me / ctas : total;
-    const long long end = me < ctas ? total * (me + 1) / ctas : total;
-    const long long excl = before + incl - mine;
-    if (start < end && excl <= start && start < excl + mine) {
-        long long at = excl;
-        for (int b = b_lo; b < b_hi; ++b) {
-            const Req r = load_req(A, b);
-            const long long x = (long long)r.blocks * r.nt * A.Hkv;
-            if (start < at + x) {
-                C.start_b = b;
-                C.start_base = at;
-                break;
-            }
-            at += x;
+        const int x = __shfl_up_sync(0xffffffffu, cost, o), y = __shfl_up_sync(0xffffffffu, units, o);
+        if (lane >= o) {
+            cost += x;
+            units += y;
         }
     }
+    if (lane == 31) {
+        C.warp_cost[warp] = cost;
+        C.warp_units[warp] = units;
+    }
+    __syncthreads();
+    cost -= my_cost;
+    units -= my_units;
+    int total = 0, all_units = 0;
+    for (int w = 0; w < kThreadsStep / 32; ++w) {
+        if (w < warp) {
+            cost += C.warp_cost[w];
+            units += C.warp_units[w];
+        }
+        total += C.warp_cost[w];
+        all_units += C.warp_units[w];
+    }
+    const Cuts cuts(total, gridDim.x);
+    const int me = blockIdx.x;
+    const int start = cuts.start(me), end = cuts.start(me + 1);
+    // the threads whose requests hold `start` and `end` say where
+    for (int side = 0; side < 2; ++side) {
+        const int x = side ? end : start;
+        if (x < cost || x >= cost + my_cost) continue;
+        int at = cost, first_unit = units;
+        for (int b = b_lo; b < b_hi; ++b) {
+            const Req r = load_req(A, b);
+            const int here = r.blocks * A.Hkv * (r.nt + U);
+            if (x < at + here) {
+                const int i = (x - at) / (r.nt + U), tile = max(x - at - i * (r.nt + U) - U, 0);
+                C.tiles_before[side] = at - U * first_unit + i * r.nt + tile;
+                if (side == 0) {
+                    C.start_b = b;
+                    C.start_unit = i;
+                    C.start_tile = tile;
+                }
+                break;
+            }
+            at += here;
+            first_unit += r.blocks * A.Hkv;
+        }
+    }
+    if (tid == 0 && end == total) C.tiles_before[1] = total - U * all_units;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int tiles = int(end - start);
+    const int tiles = start < end ? C.tiles_before[1] - C.tiles_before[0] : 0;
     const uint32_t tmem = C.tmem;
     volatile int *gave_up = &C.gave_up;
     Unit u;
-    int t = 0;  // tile in the unit
-    if (tiles > 0) t = u.start(A, C.start_b, start - C.start_base);
+    int t = C.start_tile;  // tile in the unit
+    if (tiles > 0) u.start(A, C.start_b, C.start_unit);
 
-    if (tid == 0) {
-        // The unit that is cut before this CTA, for the join.
-        CutInfo ci{};
-        ci.last = -1;
-        if (tiles > 0 && t > 0) {
-            const long long u0 = start - t, u1 = u0 + u.q.nt;
-            ci.first = int(((u0 + 1) * ctas - 1) / total);
-            ci.last = int((u1 * ctas - 1) / total);
-            ci.slot_first = total * ci.first / ctas == u0 ? 2 * ci.first : 2 * ci.first + 1;
-            ci.row0 = u.q.row0 + u.j0;
-            ci.head0 = u.h * A.G;
-            ci.ncols = u.ncols;
-        }
-        A.cut[me] = ci;
-    }
-
-    if (tiles > 0 && (warp == kWarpK || warp == kWarpV)) {
-        // ---- producers: one warp copies K tiles and the queries, one V tiles ----
-        // A lane looks up the pages of one TMA box (or of four keys: gather)
-        // one tile ahead; one elected lane issues the copies.
-        const bool is_v = warp == kWarpV;
-        const CUtensorMap *map = is_v ? &v_map : &k_map;
-        const int boxes = A.box ? kTile / A.box : 32;
-        const int span = A.box ? A.box : 4;
+    if (tiles > 0 && warp >= kWarpK && warp < kWarpMma) {
+        // ---- producers ----------------------------------------------------------
+        // One warp copies the first two thirds of a K tile's TMA boxes, and
+        // the queries, one those of a V tile, and one the rest of both.  A
+        // lane looks up the pages of one box (or of four keys: gather) one
+        // tile ahead; one elected lane issues the copies.
+        const int part = warp == kWarpBoth;
+        const int kv_lo = warp == kWarpV, kv_hi = warp == kWarpK ? 1 : 2;
+        const int span = A.box ? A.box : 4, boxes = kTile / span, most = (2 * boxes + 2) / 3;
+        const int my_box = part * most + lane;  // this lane's
+        const bool my_turn = lane < most && my_box < boxes;
         struct Ids { int page[4]; };
         auto look_up = [&](const Unit &x, int tile, Ids &ids) {
-            const int key0 = (x.q.t0 + tile) * kTile + lane * span;
+            const int key0 = (x.q.t0 + tile) * kTile + my_box * span;
             const int32_t *table = A.block_table + (int64_t)x.b * A.max_pages;
-            const bool wanted = lane < boxes && key0 < x.q.kend && key0 + span > x.q.kbeg;
+            const bool wanted = my_turn && key0 < x.q.kend && key0 + span > x.q.kbeg;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 ids.page[i] = -1;
@@ -397,11 +499,10 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
         };
         Ids ids;
         look_up(u, t, ids);
-        Ring r, rq;
-        // K and V have rings of their own: each warp meets its own loads only
-        const int my_slots = is_v ? A.slots - A.k_slots : A.k_slots, slot0 = is_v ? A.k_slots : 0;
+        Ring r[2], rq;  // K and V have rings of their own
+        const int ring_slots[2] = {A.k_slots, A.slots - A.k_slots}, ring_slot0[2] = {0, A.k_slots};
         bool first = true, ok = true;
-        int units = 0, issued = 0;  // units, and tiles of this warp
+        int units = 0, issued[2] = {0, 0};
         for (int i = 0; i < tiles; ++i) {
             Unit x = u;
             int tx = t + 1;
@@ -412,8 +513,8 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
             Ids ahead;
             if (i + 1 < tiles) look_up(x, tx, ahead);
 
-            const int tile0 = (u.q.t0 + t) * kTile, key0 = tile0 + lane * span;
-            const bool here = lane < boxes && key0 < u.q.kend && key0 + span > u.q.kbeg;
+            const int tile0 = (u.q.t0 + t) * kTile, key0 = tile0 + my_box * span;
+            const bool here = my_turn && key0 < u.q.kend && key0 + span > u.q.kbeg;
             uint32_t bad_bits = 0;  // of the lane's keys (gather) or of the whole box
             int row[4];
 #pragma unroll
@@ -433,10 +534,10 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                     uint32_t m = 0;
                     if (lane_bad) {
                         if (A.box) {
-                            const int lo = max(lane * span - 32 * q, 0), hi = min(lane * span + span - 32 * q, 32);
+                            const int lo = max(my_box * span - 32 * q, 0), hi = min(my_box * span + span - 32 * q, 32);
                             if (lo < hi) m = (hi - lo == 32 ? 0xffffffffu : ((1u << (hi - lo)) - 1u)) << lo;
-                        } else if (lane / 8 == q) {
-                            m = bad_bits << (4 * (lane % 8));
+                        } else if (my_box / 8 == q) {
+                            m = bad_bits << (4 * (my_box % 8));
                         }
                     }
                     words[q] = __reduce_or_sync(0xffffffffu, m);
@@ -444,48 +545,59 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
             }
             // the boxes to copy: a run of lanes
             const uint32_t run = __ballot_sync(0xffffffffu, here);
-            const int box_lo = __ffs(run) - 1, box_n = __popc(run);
+            const int box_lo = part * most + __ffs(run) - 1, box_n = __popc(run);
             const uint32_t bytes = box_n * uint32_t(span) * D * 2;
-            int *const rows = C.row[is_v][i & 1];
-            if (A.box) rows[lane] = row[0];
-            else *reinterpret_cast<int4 *>(rows + 4 * lane) = make_int4(row[0], row[1], row[2], row[3]);
-            const int slot = slot0 + r.slot;
-            if (i >= my_slots) ok = wait_or_give_up(&C.empty[slot], r.phase ^ 1, A.wait_ns, gave_up);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (!is_v && lane == 0)
-                *reinterpret_cast<uint4 *>(C.bad[i % kWords]) = make_uint4(words[0], words[1], words[2], words[3]);
+            int *const rows = C.row[kv_lo];
             __syncwarp();
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&C.full[slot], bytes);
-                uint32_t dst = ring + slot * kSlotBytes + box_lo * span * 128;
-                if (A.box) {
-                    const int first_key = tile0 + box_lo * span;
-                    int in_page = first_key - page_of(A, first_key) * A.page_size;
+            if (my_turn) {
+                if (A.box) rows[my_box] = row[0];
+                else *reinterpret_cast<int4 *>(rows + 4 * my_box) = make_int4(row[0], row[1], row[2], row[3]);
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                if (kv < kv_lo || kv >= kv_hi || !ok) continue;
+                const int slot = ring_slot0[kv] + r[kv].slot;
+                if (i >= ring_slots[kv]) ok = wait_or_give_up(&C.empty[slot], r[kv].phase ^ 1, A.wait_ns, gave_up);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) continue;
+                if (kv == 0 && lane == 0)
+                    *reinterpret_cast<uint4 *>(C.bad[part][i % kWords]) =
+                        make_uint4(words[0], words[1], words[2], words[3]);
+                __syncwarp();
+                if (elect_one()) {
+                    const CUtensorMap *map = kv ? &v_map : &k_map;
+                    uint64_t *full = &C.full[slot];
+                    mbar_arrive_expect_tx(full, bytes);
+                    uint32_t dst = ring + slot * kSlotBytes + box_lo * span * 128;
+                    if (A.box) {
+                        const int first_key = tile0 + box_lo * span;
+                        int in_page = first_key - page_of(A, first_key) * A.page_size;
 #pragma unroll 4
-                    for (int j = box_lo; j < box_lo + box_n; ++j) {
-                        const int page = rows[j];
-                        tma_load_4d(dst, map, &C.full[slot], 0, in_page, u.h, page);
-                        if (kHalves == 2) tma_load_4d(dst + kHalfBytes, map, &C.full[slot], 64, in_page, u.h, page);
-                        dst += span * 128;
-                        in_page += span;
-                        if (in_page == A.page_size) in_page = 0;
-                    }
-                } else {
-                    const int x0 = u.h * A.head_x;
+                        for (int j = box_lo; j < box_lo + box_n; ++j) {
+                            const int page = rows[j];
+                            tma_load_4d(dst, map, full, 0, in_page, u.h, page);
+                            if (kHalves == 2) tma_load_4d(dst + kHalfBytes, map, full, 64, in_page, u.h, page);
+                            dst += span * 128;
+                            in_page += span;
+                            if (in_page == A.page_size) in_page = 0;
+                        }
+                    } else {
+                        const int x0 = u.h * A.head_x;
 #pragma unroll 4
-                    for (int j = box_lo; j < box_lo + box_n; ++j) {
-                        const int4 k = *reinterpret_cast<const int4 *>(rows + 4 * j);
-                        tma_gather4(dst, map, &C.full[slot], x0, k.x, k.y, k.z, k.w);
-                        if (kHalves == 2) tma_gather4(dst + kHalfBytes, map, &C.full[slot], x0 + 64, k.x, k.y, k.z, k.w);
-                        dst += span * 128;
+                        for (int j = box_lo; j < box_lo + box_n; ++j) {
+                            const int4 k = *reinterpret_cast<const int4 *>(rows + 4 * j);
+                            tma_gather4(dst, map, full, x0, k.x, k.y, k.z, k.w);
+                            if (kHalves == 2) tma_gather4(dst + kHalfBytes, map, full, x0 + 64, k.x, k.y, k.z, k.w);
+                            dst += span * 128;
+                        }
                     }
                 }
+                __syncwarp();
+                ++issued[kv];
+                r[kv].next(ring_slots[kv]);
             }
-            __syncwarp();
-            ++issued;
-            r.next(my_slots);
-            if (first && !is_v) {
+            if (!ok) break;
+            if (first && warp == kWarpK) {
                 // The unit's queries: one box per row, its G heads side by side.
                 if (units > A.two_q) ok = wait_or_give_up(&C.q_empty[rq.slot], rq.phase ^ 1, A.wait_ns, gave_up);
                 ok = __all_sync(0xffffffffu, ok);
@@ -512,8 +624,10 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
         if (C.gave_up) {
             // Let the copies in flight land before the CTA ends: this warp's
             // latest copy to each slot, and the queries'.
-            for (int k = max(issued - my_slots, 0); k < issued; ++k)
-                mbar_wait_bounded(&C.full[slot0 + k % my_slots], (k / my_slots) & 1, kDrainTimeoutNs);
+            for (int kv = 0; kv < 2; ++kv)
+                for (int k = max(issued[kv] - ring_slots[kv], 0); k < issued[kv]; ++k)
+                    mbar_wait_bounded(&C.full[ring_slot0[kv] + k % ring_slots[kv]], (k / ring_slots[kv]) & 1,
+                                      kDrainTimeoutNs);
             for (int k = max(units - 1 - A.two_q, 0); k < units; ++k)
                 mbar_wait_bounded(&C.q_full[A.two_q ? k & 1 : 0], (A.two_q ? k >> 1 : k) & 1, kDrainTimeoutNs);
         }
@@ -634,7 +748,11 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 wait_or_give_up(&C.s_full[buf], (A.two_s ? i >> 1 : i) & 1, A.wait_ns, gave_up);
                 tc_fence_after();
                 const int tile = u.q.t0 + t;
-                const uint4 bw = *reinterpret_cast<const uint4 *>(C.bad[i % kWords]);
+                uint4 bw = *reinterpret_cast<const uint4 *>(C.bad[0][i % kWords]);
+                {
+                    const uint4 b1 = *reinterpret_cast<const uint4 *>(C.bad[1][i % kWords]);
+                    bw = make_uint4(bw.x | b1.x, bw.y | b1.y, bw.z | b1.z, bw.w | b1.w);
+                }
                 const bool whole = (bw.x | bw.y | bw.z | bw.w) == 0 && tile >= whole_lo && tile < whole_hi;
                 int lo = 0, hi = N;
                 if (!whole) {
@@ -654,7 +772,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                     // at the unit's end to the columns that do see them.
                     wait_or_give_up(&C.full[A.k_slots + rv.slot], rv.phase, A.wait_ns, gave_up);
                     const uint32_t vb = ring + (A.k_slots + rv.slot) * kSlotBytes + key * 128;
-                    for (int ch = grp; ch < 8 * kHalves; ch += 2) {
+                    for (int ch = grp; ch < 8 * kHalves; ch += kGroups) {
                         const uint32_t at = vb + (ch / 8) * kHalfBytes + (((ch % 8) ^ swz) << 4);
                         if (lo >= hi) {
                             st_shared16(at, 0, 0, 0, 0);
@@ -680,32 +798,35 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                         if (!first && A.two_p)
                             wait_or_give_up(&C.pv_done[pb ^ 1], ((i - 1) >> 1) & 1, A.wait_ns, gave_up);
                         tc_fence_after();
-                        for (int n = 16 * grp; n < N; n += 32) {
+                        // the warps' maxima wait in P, which is about to be written
+                        float *const colmax = reinterpret_cast<float *>(dyn + (p_smem + pb * p_bytes - smem_addr(dyn)));
+                        for (int n = 16 * grp; n < N; n += 16 * kGroups) {
                             float s[16];
                             tmem_ld16(s, s_tm + n);
                             const uint32_t seen = seen16(n, lo, hi);
                             tmem_wait_ld(s);
-                            float keep = 0.f;
+                            float keep = -INFINITY;
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 float x = ((seen >> e) & 1) ? s[e] * A.scale2 : -INFINITY;
                                 asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(x) : "f"(x));
                                 if (lane == e) keep = x;
                             }
-                            if (lane < 16) C.colmax[warp & 3][n + lane] = keep;
+                            if (lane < 16) colmax[(warp & 3) * A.ncap + n + lane] = keep;
                         }
                         soft_sync();
                         for (int n = tid; n < N; n += kSoftThreads) {
                             const float old = first ? kRefMin : C.ref[n];
-                            const float now = fmaxf(fmaxf(fmaxf(C.colmax[0][n], C.colmax[1][n]),
-                                                          fmaxf(C.colmax[2][n], C.colmax[3][n])), old);
+                            const float *const cm = colmax + n;
+                            const float now = fmaxf(fmaxf(fmaxf(cm[0], cm[A.ncap]),
+                                                          fmaxf(cm[2 * A.ncap], cm[3 * A.ncap])), old);
                             // the columns past the last weigh nothing
                             C.ref[n] = n < u.ncols ? now : INFINITY;
                             C.fac[n] = exp2_approx(old - now);
                         }
                         soft_sync();
                         if (!first) {
-                            for (int n = 16 * grp; n < N; n += 32) {
+                            for (int n = 16 * grp; n < N; n += 16 * kGroups) {
                                 float o[16], l[16];
                                 tmem_ld16(o, lane_tm + col_o + n);
                                 tmem_ld16(l, lane_tm + col_l + n);
@@ -722,24 +843,13 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                             tmem_wait_st();
                         }
                     }
-                    // two chunks of 16 columns in turn: one loads while the other is weighed
                     float top = 0.f;
-                    float s0[16], s1[16];
-                    int n = 16 * grp;
-                    if (n < N) tmem_ld16(s0, s_tm + n);
-                    for (; n < N; n += 64) {
+                    for (int n = 16 * grp; n < N; n += 16 * kGroups) {
+                        float s[16];
+                        tmem_ld16(s, s_tm + n);
                         const uint32_t at = p_row + (n / 16) * kPGroup;
-                        const bool more = n + 32 < N;
-                        tmem_wait_ld(s0);
-                        if (more) tmem_ld16(s1, s_tm + n + 32);
-                        top = fmaxf(top, whole ? weigh16<false>(s0, C.ref + n, A.scale2, 0, at, p_swz)
-                                               : weigh16<true>(s0, C.ref + n, A.scale2, seen16(n, lo, hi), at, p_swz));
-                        if (!more) break;
-                        tmem_wait_ld(s1);
-                        if (n + 64 < N) tmem_ld16(s0, s_tm + n + 64);
-                        top = fmaxf(top, whole ? weigh16<false>(s1, C.ref + n + 32, A.scale2, 0, at + 2 * kPGroup, p_swz)
-                                               : weigh16<true>(s1, C.ref + n + 32, A.scale2, seen16(n + 32, lo, hi),
-                                                               at + 2 * kPGroup, p_swz));
+                        top = fmaxf(top, whole ? weigh16<false>(s, C.ref + n, A.scale2, 0, at, p_swz)
+                                               : weigh16<true>(s, C.ref + n, A.scale2, seen16(n, lo, hi), at, p_swz));
                     }
                     fence_async_shared();
                     tc_fence_before();
@@ -756,12 +866,20 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
             const bool split = t_first > 0 || t < u.q.nt;
             const int d = key % D;
             const bool writer = key < D;
-            // the unit at the CTA's start uses the first of its two slots
-            const int slot = 2 * int(me) + (first_unit ? 0 : 1);
-            uint16_t *const out0 = A.out + ((int64_t)(u.q.row0 + u.j0) * A.Hq + u.h * A.G) * D + d;
+            // Who shares a cut unit, and the slots of their parts: a CTA's
+            // first unit uses the first of its two slots.
+            int first_cta = 0, members = 1, slot0 = 0, slot = 0;
+            if (split) {
+                const int tile0 = t_first > 0 ? start - t_first : end - t;  // the first tile's place
+                first_cta = cuts.of(tile0);
+                members = cuts.of(tile0 + u.q.nt - 1) - first_cta + 1;
+                slot0 = 2 * first_cta + (cuts.start(first_cta) >= tile0 - U ? 0 : 1);
+                slot = me == first_cta ? slot0 : 2 * me;
+            }
+            uint16_t *const out0 = A.out + ((int64_t)(u.q.row0 + u.j0) * A.Hq + u.h * A.G) * D;
             float *const part0 = A.part + (int64_t)slot * A.ncap * D + d;
             const int wrap = (A.Hq - A.G) * D;
-            for (int n = 16 * grp; n < N; n += 32) {
+            for (int n = 16 * grp; n < N; n += 16 * kGroups) {
                 float o[16], l[16];
                 tmem_ld16(o, lane_tm + col_o + n);
                 tmem_ld16(l, lane_tm + col_l + n);
@@ -782,7 +900,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                     }
                 } else {
                     int g = n % A.G;
-                    uint16_t *out = out0 + (int64_t)(n / A.G) * A.Hq * D + g * D;
+                    uint16_t *out = out0 + (int64_t)(n / A.G) * A.Hq * D + g * D + d;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float y = l[e] == 0.f ? 0.f : __fdividef(o[e], l[e]);
@@ -814,15 +932,22 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                         if (split) {
                             part0[(int64_t)n * D] += v;
                         } else {
-                            uint16_t *y = out0 + (int64_t)(n / A.G) * A.Hq * D + (n % A.G) * D;
+                            uint16_t *y = out0 + (int64_t)(n / A.G) * A.Hq * D + (n % A.G) * D + d;
                             *y = uint16_t(pack_bf16x2(bf16_lo(*y) + v, 0.f));
                         }
                     }
                 }
             }
             tc_fence_before();
+            if (split) __threadfence();
             soft_sync();  // ref, poison and O are read before the next unit writes them
-            if (tid == 0) C.poison = 0;
+            if (tid == 0) {
+                C.poison = 0;
+                if (split && atomicAdd(&A.arrived[first_cta], 1) == members - 1) {
+                    A.arrived[first_cta] = 0;  // as the next call wants it
+                    C.join[C.joins++] = Join{u.q.row0 + u.j0, u.h * A.G, u.ncols, slot0, first_cta, members};
+                }
+            }
             if (i < tiles) {
                 u.next(A);
                 t = 0;
@@ -834,55 +959,13 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
     tc_fence_after();
     if (tid == 0 && C.gave_up) atomicOr(A.status, kStatusWaitTimeout);
     if (warp == kWarpMma) tmem_free(tmem, kTmemCols);
-}
-
-// Adds the partial sums of the units that were cut, in the order of the keys.
-// CTA i takes its share of the columns of the unit that is cut before CTA i;
-// a warp takes a column.
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) step_join_kernel(const StepArgs A) {
-    constexpr int E = D / 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int me = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const CutInfo ci = A.cut[me];
-    if (ci.last < me) return;
-    const int members = ci.last - ci.first + 1;
-    const int cuts = members - 1, rank = me - ci.first - 1;
-    const int n0 = int((long long)ci.ncols * rank / cuts), n1 = int((long long)ci.ncols * (rank + 1) / cuts);
-    for (int n = n0 + warp; n < n1; n += kJoinThreads / 32) {
-        float m = kRefMin;
-        for (int k = lane; k < members; k += 32) {
-            const int slot = k == 0 ? ci.slot_first : 2 * (ci.first + k);
-            m = fmaxf(m, A.stat[(int64_t)slot * 2 * A.ncap + n]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float acc[E], l = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        for (int k0 = 0; k0 < members; k0 += 32) {
-            float wk = 0.f, lk = 0.f;
-            if (k0 + lane < members) {
-                const int k = k0 + lane, slot = k == 0 ? ci.slot_first : 2 * (ci.first + k);
-                wk = exp2_approx(A.stat[(int64_t)slot * 2 * A.ncap + n] - m);
-                lk = A.stat[((int64_t)slot * 2 + 1) * A.ncap + n];
-            }
-            const int here = min(32, members - k0);
-#pragma unroll 8
-            for (int k = 0; k < here; ++k) {
-                const float f = __shfl_sync(0xffffffffu, wk, k);
-                l += f * __shfl_sync(0xffffffffu, lk, k);
-                const int slot = k0 + k == 0 ? ci.slot_first : 2 * (ci.first + k0 + k);
-                const float *p = A.part + ((int64_t)slot * A.ncap + n) * D + lane * E;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += f * p[e];
-            }
-        }
-        const int j = n / A.G, g = n - j * A.G;
-        uint32_t *out = reinterpret_cast<uint32_t *>(A.out + ((int64_t)(ci.row0 + j) * A.Hq + ci.head0 + g) * D + lane * E);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    // The joins come last, when every warp has time and the loops above keep
+    // their registers.
+    for (int k = 0; k < C.joins; ++k) {
+        __threadfence();
+        const Join J = C.join[k];
+        if (J.members <= 2) join_columns<D, 2>(A, J, warp, lane);
+        else join_columns<D, 1>(A, J, warp, lane);
     }
 }
 
@@ -892,22 +975,27 @@ int step_columns(int Hq, int Hkv, int q_max) {
     return (step_rows(Hq, Hkv, q_max) * (Hq / Hkv) + 15) / 16 * 16;
 }
 
-constexpr size_t kHeaderBytes = 256 + (sizeof(CutInfo) * kAttnMaxCtas + 255) / 256 * 256;
+constexpr size_t kHeaderBytes = 256 + (sizeof(int32_t) * kAttnMaxCtas + 255) / 256 * 256;
 
 template <int D>
 cudaError_t launch(StepArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStream_t s) {
-    // S, P and Q are held twice where two slots for K and two for V remain: P
-    // before Q, since a tile's products need P and only a unit's first tile Q.
+    // What is held twice, against ring slots.  A tile of V waits for its
+    // tile's softmax, so three V slots carry more than a second P or Q; Q is
+    // needed twice only at a unit's border.  The first of these that leaves
+    // five slots, else four, is taken.
     A.two_s = A.ncap <= kTwoS;
     const size_t slot = size_t(D) * 2 * kTile;
     const size_t p = size_t(A.ncap / 16) * kPGroup, q = size_t(A.ncap) * D * 2;
-    const size_t room = kSmemBytes - sizeof(Ctrl) - 256 - 2048;
+    const size_t room = kSmemBytes - sizeof(Ctrl) - 2048;
     size_t fixed = 0;
-    for (int twice = 2; twice >= 0; --twice) {
-        A.two_p = A.two_s && twice >= 1;
-        A.two_q = twice == 2;
-        fixed = p * (1 + A.two_p) + q * (1 + A.two_q);
-        if (fixed + 4 * slot <= room) break;
+    for (int want = 5; want >= 4; --want) {
+        for (int twice = 2; twice >= want - 4; --twice) {
+            A.two_p = A.two_s && twice >= 1;
+            A.two_q = twice == 2;
+            fixed = p * (1 + A.two_p) + q * (1 + A.two_q);
+            if (fixed + want * slot <= room) break;
+        }
+        if (fixed + want * slot <= room) break;
     }
     A.slots = int(std::min<size_t>((room - fixed) / slot, kMaxSlots));
     A.k_slots = A.slots / 2;
@@ -916,18 +1004,7 @@ cudaError_t launch(StepArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStrea
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     step_attention_kernel<D><<<ctas, kThreadsStep, smem, s>>>(A, maps[0], maps[1], maps[2]);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (ctas == 1) return cudaSuccess;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas - 1);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, step_join_kernel<D>, A);
+    return cudaGetLastError();
 }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -961,6 +1038,12 @@ bool step_strides_ok(const dspark_attn &a) {
     return gcd(a.page_size, kTile) >= 8 || step_gather_rows(a, &row, &page_rows, &head_rows, &head_x);
 }
 
+bool step_list_fits(const dspark_attn &a) {
+    const long long blocks = (a.q_max + step_rows(a.Hq, a.Hkv, a.q_max) - 1) / step_rows(a.Hq, a.Hkv, a.q_max) + 1;
+    const long long places = (long long)a.max_pages * a.page_size / kTile + 2 + kUnitCost;
+    return places * blocks * a.Hkv <= INT32_MAX / a.B;
+}
+
 cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_ns, cudaStream_t s) {
     StepArgs A{};
     A.B = a.B; A.rows = a.rows; A.q_max = a.q_max; A.Hq = a.Hq; A.Hkv = a.Hkv; A.G = a.Hq / a.Hkv;
@@ -978,10 +1061,11 @@ cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_n
     A.out = static_cast<uint16_t *>(a.out);
     char *ws = static_cast<char *>(a.workspace);
     A.status = reinterpret_cast<int32_t *>(ws);
-    A.cut = reinterpret_cast<CutInfo *>(ws + 256);
+    A.arrived = reinterpret_cast<int32_t *>(ws + 256);
     A.part = reinterpret_cast<float *>(ws + kHeaderBytes);
     A.stat = reinterpret_cast<float *>(ws + kHeaderBytes +
                                        align256(2 * kAttnMaxCtas * size_t(A.ncap) * a.D * sizeof(float)));
+    A.unit_cost = kUnitCost;
     A.wait_ns = wait_ns;
 
     // A page of 8 k positions is copied in boxes of whole pages or parts of
