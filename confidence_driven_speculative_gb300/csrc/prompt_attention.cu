@@ -1,65 +1,568 @@
 // prompt_attention.cu -- whole prompts, causal, packed one after the other.
 //
-// One warp per (row, query head): an online softmax over the row's keys.
+// Mathematics.  For a block of rows of one query head: S = Q K^T, the weights
+// P = 2^(scale log2(e) S - m) against a running reference m per row, l the
+// sum of P, O += P V; the output is O / l.  The reference is the first tile's
+// maximum; a later tile moves it, and rescales O and l, only where its
+// maximum passes the reference by 2^32 (the weights stay in the range of fp32
+// and bfloat16 keeps its relative step), which is next to never.
+//
+// Bound: the tensor cores.  A unit is 256 rows of one head in two blocks of
+// 128, walked over tiles of 128 keys.  S and O of both blocks fill TMEM
+// (4 x 128 columns); P overwrites its S in TMEM and is the A operand of
+// P V.  While one block's softmax runs, the tensor cores work on the other
+// block: O_0 += P_0 V, S_0 of the next tile, O_1 += P_1 V, S_1 of the next tile.
+// A softmax thread owns a row, so maxima and sums stay in its registers.
+//
+// Units are handed out by a counter, the longest of a prompt first, so the
+// CTAs end together; a unit's result does not depend on who computes it.
+#include <algorithm>
+
 #include "attn.cuh"
 #include "dspark_internal.cuh"
+#include "tcgen05.cuh"
 
 namespace dspark {
 namespace {
 
+constexpr int kTile = 128;        // rows of a block, keys of a tile
+constexpr int kThreadsP = 384;
+constexpr int kScan = 128;        // threads that sum up the prompts' units
+constexpr int kWarpMmaP = 8, kWarpLoad = 9, kWarpClean = 10;  // softmax 0..7; two cleaners
+constexpr int kCleaners = 64;
+constexpr int kSlotsMax = 10;
+constexpr int kSched = 4;         // units on their way to the warps
+constexpr int kSchedReaders = 11; // warps that read them
+constexpr float kRefMin = -1e30f;
+constexpr float kRefSlack = 32.0f;
+constexpr size_t kSmemBytes = 232448;
+
+struct PromptArgs {
+    int B, rows, q_max, Hq, Hkv, G, window;
+    int slots, k_slots;
+    float scale2;
+    int64_t v_stride;
+    const uint16_t *v;
+    const int32_t *row_off;
+    uint16_t *out;
+    int32_t *counter;  // next unit, CTAs that are done
+    int32_t *status;
+    uint64_t wait_ns;
+};
+
+struct Unit {
+    int row0, n;   // the prompt's first packed row, its rows
+    int q0, h;     // first row of the unit in the prompt, query head; h < 0: no more units
+};
+
+// Tiles of keys that block a (rows q .. q + 127) of a unit walks.
+struct Span { int lo, hi; };
+__device__ __forceinline__ Span span_of(const PromptArgs &A, const Unit &u, int a) {
+    const int q = u.q0 + a * kTile;
+    if (q >= u.n) return {0, 0};
+    Span s;
+    s.lo = A.window > 0 ? max(q - A.window + 1, 0) / kTile : 0;
+    s.hi = (min(q + kTile, u.n) + kTile - 1) / kTile;
+    return s;
+}
+// Does some row of block a not see some key of tile t?
+__device__ __forceinline__ bool partial(const PromptArgs &A, const Unit &u, int a, int t) {
+    const int q = u.q0 + a * kTile;
+    return (t + 1) * kTile - 1 > q || (A.window > 0 && t * kTile <= min(q + kTile, u.n) - 1 - A.window);
+}
+
+struct Ctrl {
+    uint64_t full[kSlotsMax], empty[kSlotsMax], clean[kSlotsMax];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t sched_full[kSched], sched_empty[kSched], drained;
+    Unit unit[kSched];
+    int poisoned[8];          // by unit number % 8: the last unit + 1 that lost values
+    int pairs[kScan + 1];     // exclusive sums of the units (per head) of each thread's prompts
+    int warp_sum[kScan / 32];
+    uint32_t tmem;
+    int gave_up;
+};
+
+// Reads the next unit off the ring.
+struct SchedReader {
+    Ring r;
+    __device__ __forceinline__ Unit next(Ctrl &C, const PromptArgs &A, volatile int *gave_up, int lane) {
+        Unit u{0, 0, 0, -1};
+        bool ok = wait_or_give_up(&C.sched_full[r.slot], r.phase, A.wait_ns, gave_up);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) u = C.unit[r.slot];
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&C.sched_empty[r.slot]);
+        r.next(kSched);
+        return u;
+    }
+};
+
 template <int D>
-__global__ void __launch_bounds__(128) prompt_attention_kernel(const dspark_attn A) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int h = int(w % A.Hq);
-    const int64_t r = w / A.Hq;
-    if (r >= A.rows) return;
-    int lo = 0, hi = A.B;  // the request of row r
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (A.row_off[mid] <= r) lo = mid; else hi = mid;
+__global__ void __launch_bounds__(kThreadsP, 1)
+prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_constant__ CUtensorMap q_map,
+                        const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    constexpr int kHalves = D / 64;
+    constexpr uint32_t kHalfBytes = kTile * 128;
+    constexpr uint32_t kSlotBytes = kHalves * kHalfBytes;
+    constexpr uint32_t kColO = 2 * kTile;  // S_0, S_1, O_0, O_1
+    extern __shared__ uint8_t dyn[];
+    __shared__ Ctrl C;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const uint32_t q_smem = (smem_addr(dyn) + 1023) & ~1023u;
+    const uint32_t ring = q_smem + 2 * kSlotBytes;
+    const int v_slots = A.slots - A.k_slots;
+    const uint32_t v_ring = ring + A.k_slots * kSlotBytes;
+    volatile int *gave_up = &C.gave_up;
+
+    if (tid == 0) {
+        for (int s = 0; s < A.slots; ++s) {
+            mbar_init(&C.full[s], 1);
+            mbar_init(&C.empty[s], 1);
+            mbar_init(&C.clean[s], 2);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&C.q_full[a], 1);
+            mbar_init(&C.q_empty[a], 1);
+            mbar_init(&C.s_full[a], 1);
+            mbar_init(&C.p_full[a], 4);
+            mbar_init(&C.o_full[a], 2);
+        }
+        for (int s = 0; s < kSched; ++s) {
+            mbar_init(&C.sched_full[s], 1);
+            mbar_init(&C.sched_empty[s], kSchedReaders);
+        }
+        mbar_init(&C.drained, 1);
+        for (int i = 0; i < 8; ++i) C.poisoned[i] = 0;
+        C.gave_up = 0;
+        fence_barrier_init();
     }
-    const int r0 = A.row_off[lo];
-    if (r < r0 || r >= A.row_off[lo + 1] || r - r0 >= A.q_max) return;
-    const int kvh = h / (A.Hq / A.Hkv);
-    const uint16_t *q = static_cast<const uint16_t *>(A.q_rot) + (r * A.Hq + h) * D + lane * E;
-    float x[E], o[E];
-    for (int e = 0; e < E; ++e) { x[e] = bf16_lo(q[e]); o[e] = 0.f; }
-    const float sc = A.scale * 1.4426950408889634f;
-    float m = -INFINITY, l = 0.f;
-    const int64_t first = A.window > 0 ? max((int64_t)r0, r - A.window + 1) : r0;
-    for (int64_t k = first; k <= r; ++k) {
-        const uint16_t *kp = static_cast<const uint16_t *>(A.k_rot) + (k * A.Hkv + kvh) * D + lane * E;
-        const uint16_t *vp = static_cast<const uint16_t *>(A.v) + k * A.v_stride + kvh * D + lane * E;
-        float d = 0.f;
-        for (int e = 0; e < E; ++e) d += x[e] * bf16_lo(kp[e]);
-        d = warp_sum(d) * sc;
-        const float mn = fmaxf(m, d);
-        const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
-        const float p = mn == -INFINITY ? 0.f : exp2_approx(d - mn);
-        l = l * f + p;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * bf16_lo(vp[e]);
-        m = mn;
+    if (warp == kWarpMmaP) tmem_alloc(&C.tmem, 512);
+    if (warp == kWarpLoad && lane == 0) {
+        prefetch_map(&q_map);
+        prefetch_map(&k_map);
+        prefetch_map(&v_map);
     }
-    uint16_t *out = static_cast<uint16_t *>(A.out) + (r * A.Hq + h) * D + lane * E;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int e = 0; e < E; ++e) {
-        uint32_t y;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(0.f), "f"(o[e] * inv));
-        out[e] = uint16_t(y);
+    // Units of each thread's prompts.
+    const int per = (A.B + kScan - 1) / kScan;
+    auto prompt = [&](int b, int &row0) {
+        row0 = min(max(A.row_off[b], 0), A.rows);
+        return min(min(max(A.row_off[b + 1], row0), A.rows) - row0, A.q_max);
+    };
+    int mine = 0;
+    for (int b = min(tid * per, A.B); tid < kScan && b < min(tid * per + per, A.B); ++b) {
+        int row0;
+        mine += (prompt(b, row0) + 2 * kTile - 1) / (2 * kTile);
     }
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+    }
+    if (lane == 31 && tid < kScan) C.warp_sum[warp] = sum;
+    __syncthreads();
+    if (tid < kScan) {
+        for (int w = 0; w < warp; ++w) sum += C.warp_sum[w];
+        C.pairs[tid] = sum - mine;
+        if (tid == kScan - 1) C.pairs[kScan] = sum;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = C.tmem;
+
+    if (warp == kWarpLoad) {
+        // ---- units, and their queries, keys and values -----------------------
+        const int total = C.pairs[kScan] * A.Hq;  // at most 2^17 * 2^8
+        Ring rs, rk, rv;
+        uint32_t q_uses[2] = {0, 0};
+        int issued[2] = {0, 0}, published = 0;
+        bool ok = true;
+        int claim = 0;
+        if (lane == 0) claim = atomicAdd(A.counter, 1);
+        while (ok) {
+            const int idx = __shfl_sync(0xffffffffu, claim, 0);
+            Unit u{0, 0, 0, -1};
+            if (idx < total) {
+                if (lane == 0) claim = atomicAdd(A.counter, 1);  // the next one, on its way
+                const int pair = idx / A.Hq;
+                u.h = idx - pair * A.Hq;
+                int lo = 0, hi = kScan;  // the thread whose prompts hold it
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (C.pairs[mid] <= pair) lo = mid; else hi = mid;
+                }
+                int left = pair - C.pairs[lo];
+                for (int b = lo * per; b < A.B; ++b) {
+                    u.n = prompt(b, u.row0);
+                    const int units = (u.n + 2 * kTile - 1) / (2 * kTile);
+                    if (left < units) {
+                        u.q0 = (units - 1 - left) * 2 * kTile;  // the longest first
+                        break;
+                    }
+                    left -= units;
+                }
+            }
+            if (published >= kSched)
+                ok = wait_or_give_up(&C.sched_empty[rs.slot], rs.phase ^ 1, A.wait_ns, gave_up);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                C.unit[rs.slot] = u;
+                mbar_arrive(&C.sched_full[rs.slot]);
+            }
+            rs.next(kSched);
+            ++published;
+            if (u.h < 0) break;
+
+            const Span s0 = span_of(A, u, 0), s1 = span_of(A, u, 1);
+            const int t_lo = s0.lo, t_hi = max(s0.hi, s1.hi), kvh = u.h / A.G;
+            for (int a = 0; a < 2 && ok; ++a) {
+                if (a == 1 && s1.hi == 0) break;
+                if (q_uses[a] > 0) ok = wait_or_give_up(&C.q_empty[a], (q_uses[a] - 1) & 1, A.wait_ns, gave_up);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&C.q_full[a], kSlotBytes);
+                    for (int hf = 0; hf < kHalves; ++hf)
+                        tma_load_3d(q_smem + a * kSlotBytes + hf * kHalfBytes, &q_map, &C.q_full[a], hf * 64, u.h,
+                                    u.row0 + u.q0 + a * kTile);
+                }
+                __syncwarp();
+                ++q_uses[a];
+            }
+            for (int t = t_lo; t < t_hi && ok; ++t) {
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    Ring &r = kv ? rv : rk;
+                    const int slots = kv ? v_slots : A.k_slots, slot = (kv ? A.k_slots : 0) + r.slot;
+                    if (issued[kv] >= slots) ok = wait_or_give_up(&C.empty[slot], r.phase ^ 1, A.wait_ns, gave_up);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&C.full[slot], kSlotBytes);
+                        for (int hf = 0; hf < kHalves; ++hf)
+                            tma_load_3d(ring + slot * kSlotBytes + hf * kHalfBytes, kv ? &v_map : &k_map, &C.full[slot],
+                                        hf * 64, kvh, u.row0 + t * kTile);
+                    }
+                    __syncwarp();
+                    r.next(slots);
+                    ++issued[kv];
+                }
+            }
+        }
+        if (C.gave_up) {
+            // Let the copies in flight land before the CTA ends.
+            for (int kv = 0; kv < 2; ++kv) {
+                const int slots = kv ? v_slots : A.k_slots;
+                for (int k = max(issued[kv] - slots, 0); k < issued[kv]; ++k)
+                    mbar_wait_bounded(&C.full[(kv ? A.k_slots : 0) + k % slots], (k / slots) & 1, kDrainTimeoutNs);
+            }
+            for (int a = 0; a < 2; ++a)
+                if (q_uses[a]) mbar_wait_bounded(&C.q_full[a], (q_uses[a] - 1) & 1, kDrainTimeoutNs);
+        }
+        if (lane == 0) {
+            // The last CTA leaves the counter as the next call wants it.
+            __threadfence();
+            if (atomicAdd(A.counter + 1, 1) == int(gridDim.x) - 1) {
+                A.counter[0] = 0;
+                A.counter[1] = 0;
+            }
+        }
+    } else if (warp == kWarpMmaP) {
+        // ---- MMA issuer -----------------------------------------------------
+        const uint64_t qd = smem_desc(q_smem, 16, 1024), kd0 = smem_desc(ring, 16, 1024);
+        const uint64_t vd0 = smem_desc(v_ring, kHalfBytes, 1024);
+        constexpr uint32_t id_s = mma_idesc(128, kTile, false, false), id_o = mma_idesc(128, D, false, true);
+        SchedReader sched;
+        Ring rk, rv;
+        uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t phase) {
+            ok = ok && wait_or_give_up(bar, phase, A.wait_ns, gave_up);
+            ok = __all_sync(0xffffffffu, ok);
+        };
+        while (ok) {
+            const Unit u = sched.next(C, A, gave_up, lane);
+            if (u.h < 0) break;
+            const Span sp[2] = {span_of(A, u, 0), span_of(A, u, 1)};
+            const int t_lo = sp[0].lo, t_hi = max(sp[0].hi, sp[1].hi);
+            // S of block a and tile t, whose K is in slot rk
+            auto issue_s = [&](int a, int t) {
+                if (t == sp[a].lo) {
+                    wait(&C.q_full[a], q_uses[a] & 1);
+                    ++q_uses[a];
+                }
+                wait(&C.full[rk.slot], rk.phase);
+                if (!ok) return;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t kd = kd0 + uint32_t(rk.slot) * (kSlotBytes >> 4);
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d) {
+                        const uint32_t at = ((d / 4) * kHalfBytes + (d % 4) * 32) >> 4;
+                        mma_ss(tmem + a * kTile, qd + a * (kSlotBytes >> 4) + at, kd + at, id_s, d > 0);
+                    }
+                    mma_commit(&C.s_full[a]);
+                    if (t == sp[a].hi - 1) mma_commit(&C.q_empty[a]);
+                }
+                __syncwarp();
+            };
+            auto free_k = [&] {
+                if (elect_one()) mma_commit(&C.empty[rk.slot]);
+                __syncwarp();
+                rk.next(A.k_slots);
+            };
+            for (int a = 0; a < 2 && ok; ++a)
+                if (t_lo >= sp[a].lo && t_lo < sp[a].hi) issue_s(a, t_lo);
+            if (!ok) break;
+            free_k();
+            for (int t = t_lo; t < t_hi && ok; ++t) {
+                for (int a = 0; a < 2 && ok; ++a) {
+                    if (t >= sp[a].lo && t < sp[a].hi) {
+                        wait(&C.p_full[a], p_uses[a] & 1);
+                        ++p_uses[a];
+                        wait(&C.clean[A.k_slots + rv.slot], rv.phase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t vd = vd0 + uint32_t(rv.slot) * (kSlotBytes >> 4);
+#pragma unroll
+                            for (int k = 0; k < kTile / 16; ++k)
+                                mma_ts(tmem + kColO + a * D, tmem + a * kTile + k * 8, vd + k * (2048 >> 4), id_o,
+                                       !(t == sp[a].lo && k == 0));
+                            if (t == sp[a].hi - 1) {
+                                mbar_arrive(&C.o_full[a]);  // passes the cleaners' word on
+                                mma_commit(&C.o_full[a]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (t + 1 >= sp[a].lo && t + 1 < sp[a].hi) issue_s(a, t + 1);
+                }
+                if (!ok) break;
+                if (elect_one()) mma_commit(&C.empty[A.k_slots + rv.slot]);
+                __syncwarp();
+                rv.next(v_slots);
+                if (t + 1 < t_hi) free_k();
+            }
+        }
+        if (C.gave_up) {
+            if (elect_one()) mma_commit(&C.drained);
+            __syncwarp();
+            mbar_wait_bounded(&C.drained, 0, kDrainTimeoutNs);
+        }
+    } else if (warp >= kWarpClean) {
+        // ---- cleaners: masked keys must not reach O through 0 * infinity.  A
+        // value tile that some row does not see in full loses its NaN and
+        // infinities; the epilogue adds them to the rows that see them. -----
+        SchedReader sched;
+        Ring rv;
+        const int id = tid - kWarpClean * 32;
+        bool ok = true;
+        for (int unit = 0; ok; ++unit) {
+            const Unit u = sched.next(C, A, gave_up, lane);
+            if (u.h < 0) break;
+            const Span s0 = span_of(A, u, 0), s1 = span_of(A, u, 1);
+            for (int t = s0.lo; t < max(s0.hi, s1.hi); ++t) {
+                const int slot = A.k_slots + rv.slot;
+                ok = wait_or_give_up(&C.full[slot], rv.phase, A.wait_ns, gave_up);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if ((t >= s0.lo && t < s0.hi && partial(A, u, 0, t)) ||
+                    (t >= s1.lo && t < s1.hi && partial(A, u, 1, t))) {
+                    const uint32_t at0 = v_ring + rv.slot * kSlotBytes + id * 16;
+                    bool lost = false;
+#pragma unroll 4
+                    for (uint32_t c = 0; c < kSlotBytes; c += kCleaners * 16) {
+                        const uint4 x = ld_shared16(at0 + c);
+                        const uint32_t mx = nonfinite_mask(x.x), my = nonfinite_mask(x.y),
+                                       mz = nonfinite_mask(x.z), mw = nonfinite_mask(x.w);
+                        if (mx | my | mz | mw) {
+                            st_shared16(at0 + c, x.x & ~mx, x.y & ~my, x.z & ~mz, x.w & ~mw);
+                            lost = true;
+                        }
+                    }
+                    if (lost) C.poisoned[unit % 8] = unit + 1;
+                    fence_async_shared();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&C.clean[slot]);
+                rv.next(v_slots);
+            }
+        }
+    } else {
+        // ---- softmax and output: thread = row of block a -----------------------
+        const int a = warp >> 2, row = tid & 127;
+        const uint32_t lane_tm = tmem + (uint32_t((warp & 3) * 32) << 16);
+        const uint32_t s_tm = lane_tm + a * kTile, o_tm = lane_tm + kColO + a * D;
+        SchedReader sched;
+        uint32_t s_uses = 0, o_uses = 0;
+        bool ok = true;
+        for (int unit = 0; ok; ++unit) {
+            const Unit u = sched.next(C, A, gave_up, lane);
+            if (u.h < 0) break;
+            const Span sp = span_of(A, u, a);
+            if (sp.hi == 0) continue;
+            const int q = u.q0 + a * kTile + row;  // the thread's row; past the prompt: computed, not stored
+            float ref = 0.f;
+            float2 l2 = make_float2(0.f, 0.f);
+            for (int t = sp.lo; t < sp.hi; ++t) {
+                ok = wait_or_give_up(&C.s_full[a], s_uses & 1, A.wait_ns, gave_up);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ++s_uses;
+                tc_fence_after();
+                float s[kTile];
+#pragma unroll
+                for (int c = 0; c < kTile; c += 32) tmem_ld32(s + c, s_tm + c);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                for (int c = 0; c < kTile; c += 32) tmem_use32(s + c);
+                if (partial(A, u, a, t)) {
+                    const int hi = q - t * kTile, lo = A.window > 0 ? hi - A.window : -1;  // sees (lo, hi]
+#pragma unroll
+                    for (int e = 0; e < kTile; ++e)
+                        if (e > hi || e <= lo) s[e] = -INFINITY;
+                }
+                float m0 = max3(s[0], s[1], s[2]), m1 = max3(s[3], s[4], s[5]);
+#pragma unroll
+                for (int e = 6; e < kTile - 2; e += 4) {
+                    m0 = max3(m0, s[e], s[e + 1]);
+                    m1 = max3(m1, s[e + 2], s[e + 3]);
+                }
+                const float m = max3(m0, m1, fmaxf(s[kTile - 2], s[kTile - 1])) * A.scale2;
+                if (t == sp.lo) {
+                    ref = fmaxf(m, kRefMin);
+                } else if (__any_sync(0xffffffffu, m > ref + kRefSlack)) {
+                    const float now = m > ref + kRefSlack ? m : ref;
+                    const float f = exp2_approx(ref - now);
+                    ref = now;
+                    l2.x *= f;
+                    l2.y *= f;
+#pragma unroll
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        tmem_ld16(o, o_tm + c);
+                        tmem_wait_ld(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= f;
+                        tmem_st16(o_tm + c, o);
+                    }
+                }
+                const float2 sc = make_float2(A.scale2, A.scale2), nr = make_float2(-ref, -ref);
+#pragma unroll
+                for (int c = 0; c < kTile; c += 32) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 x = fma2(make_float2(s[c + e], s[c + e + 1]), sc, nr);
+                        x.x = exp2_approx(x.x);
+                        x.y = exp2_approx(x.y);
+                        l2 = add2(l2, x);
+                        p[e / 2] = pack_bf16x2(x.x, x.y);
+                    }
+                    tmem_st16u(s_tm + c / 2, p);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&C.p_full[a]);
+            }
+            if (!ok) break;
+            ok = wait_or_give_up(&C.o_full[a], o_uses & 1, A.wait_ns, gave_up);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ++o_uses;
+            tc_fence_after();
+            const float l = l2.x + l2.y, inv = l == 0.f ? 0.f : 1.f / l;
+            uint16_t *const out = A.out + ((int64_t)(u.row0 + q) * A.Hq + u.h) * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(o, o_tm + c);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                tmem_use32(o);
+                if (q < u.n) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 y;
+                        y.x = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+                        y.y = pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv);
+                        y.z = pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv);
+                        y.w = pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv);
+                        *reinterpret_cast<uint4 *>(out + c + e) = y;
+                    }
+                }
+            }
+            tc_fence_before();
+            if (C.poisoned[unit % 8] == unit + 1 && q < u.n) {
+                // what the cleaners took out of the values that this row sees
+                for (int t = sp.lo; t < sp.hi; ++t) {
+                    const bool mixed = partial(A, u, a, t) ||
+                                       (span_of(A, u, a ^ 1).hi > t && span_of(A, u, a ^ 1).lo <= t && partial(A, u, a ^ 1, t));
+                    if (!mixed) continue;
+                    for (int k = t * kTile; k < min((t + 1) * kTile, q + 1); ++k) {
+                        if (A.window > 0 && k <= q - A.window) continue;
+                        const uint16_t *v = A.v + (int64_t)(u.row0 + k) * A.v_stride + (u.h / A.G) * D;
+                        for (int d = 0; d < D; ++d) {
+                            const float x = bf16_lo(v[d]);
+                            if (!isfinite(x)) out[d] = uint16_t(pack_bf16x2(bf16_lo(out[d]) + x, 0.f));
+                        }
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && C.gave_up) atomicOr(A.status, kStatusWaitTimeout);
+    if (warp == kWarpMmaP) tmem_free(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(PromptArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStream_t s) {
+    const size_t slot = size_t(D) * 2 * kTile;
+    A.slots = int(std::min<size_t>((kSmemBytes - sizeof(Ctrl) - 1024 - 2 * slot) / slot, kSlotsMax));
+    A.k_slots = A.slots / 2;
+    const size_t smem = 1024 + (2 + A.slots) * slot;
+    const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    prompt_attention_kernel<D><<<ctas, kThreadsP, smem, s>>>(A, maps[0], maps[1], maps[2]);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_attention(const dspark_attn &a, int sms, uint64_t wait_ns, cudaStream_t s) {
-    (void)sms; (void)wait_ns;
-    const int64_t warps = (int64_t)a.rows * a.Hq;
-    const unsigned grid = unsigned((warps + 3) / 4);
-    if (a.D == 128) prompt_attention_kernel<128><<<grid, 128, 0, s>>>(a);
-    else prompt_attention_kernel<64><<<grid, 128, 0, s>>>(a);
-    return cudaGetLastError();
+    PromptArgs A{};
+    A.B = a.B; A.rows = a.rows; A.q_max = a.q_max; A.Hq = a.Hq; A.Hkv = a.Hkv; A.G = a.Hq / a.Hkv;
+    A.window = a.window;
+    A.scale2 = float(double(a.scale) * 1.4426950408889634);
+    A.v_stride = a.v_stride;
+    A.v = static_cast<const uint16_t *>(a.v);
+    A.row_off = a.row_off;
+    A.out = static_cast<uint16_t *>(a.out);
+    A.status = static_cast<int32_t *>(a.workspace);
+    A.counter = static_cast<int32_t *>(a.workspace) + 1;
+    A.wait_ns = wait_ns;
+    CUtensorMap maps[3];
+    const void *base[3] = {a.q_rot, a.k_rot, a.v};
+    const int heads[3] = {a.Hq, a.Hkv, a.Hkv};
+    const int64_t stride[3] = {(int64_t)a.Hq * a.D, (int64_t)a.Hkv * a.D, a.v_stride};
+    for (int i = 0; i < 3; ++i) {
+        const uint64_t dims[3] = {uint64_t(a.D), uint64_t(heads[i]), uint64_t(a.rows)};
+        const uint64_t st[2] = {uint64_t(a.D) * 2, uint64_t(stride[i]) * 2};
+        const uint32_t box[3] = {64, 1, kTile};
+        const cudaError_t e = encode_map(&maps[i], base[i], 3, dims, st, box);
+        if (e != cudaSuccess) return e;
+    }
+    const int ctas = std::min(sms, kAttnMaxCtas);
+    return a.D == 128 ? launch<128>(A, maps, ctas, s) : launch<64>(A, maps, ctas, s);
 }
 
 }  // namespace dspark

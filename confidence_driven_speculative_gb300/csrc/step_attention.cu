@@ -166,15 +166,6 @@ struct Cuts {
     }
 };
 
-// Slot and phase of a ring walked in order.
-struct Ring {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next(int slots) {
-        if (++slot == slots) { slot = 0; phase ^= 1; }
-    }
-};
-
 // A unit that was cut and whose last part this CTA wrote: it joins the parts.
 struct Join {
     int row0, head0, ncols;             // its first packed row, first query head, columns
@@ -212,24 +203,6 @@ __device__ __forceinline__ bool soft_any(bool x) {
 // Is phase `parity` of `bar` over?  One answer for the whole warp.
 __device__ __forceinline__ bool warp_test(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
-}
-
-__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-// Does either half of the word hold a NaN or an infinity?
-__device__ __forceinline__ uint32_t nonfinite_mask(uint32_t w) {
-    uint32_t m = 0;
-    if ((w & 0x7f80u) == 0x7f80u) m |= 0xffffu;
-    if ((w & 0x7f800000u) == 0x7f800000u) m |= 0xffff0000u;
-    return m;
 }
 
 // The columns [lo, hi) of the unit that see the key at `kpos`.
