@@ -73,7 +73,8 @@ __device__ __forceinline__ bool partial(const PromptArgs &A, const Unit &u, int 
 
 struct Ctrl {
     uint64_t full[kSlotsMax], empty[kSlotsMax], clean[kSlotsMax];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], o_full[2];
+    uint64_t p_full[2][2];    // by block and half of the keys
     uint64_t sched_full[kSched], sched_empty[kSched], drained;
     Unit unit[kSched];
     int poisoned[8];          // by unit number % 8: the last unit + 1 that lost values
@@ -114,6 +115,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
     const uint32_t ring = q_smem + 2 * kSlotBytes;
     const int v_slots = A.slots - A.k_slots;
     const uint32_t v_ring = ring + A.k_slots * kSlotBytes;
+    const uint32_t stage = ring + A.slots * kSlotBytes;  // 4 KB for each softmax warp
     volatile int *gave_up = &C.gave_up;
 
     if (tid == 0) {
@@ -126,7 +128,8 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
             mbar_init(&C.q_full[a], 1);
             mbar_init(&C.q_empty[a], 1);
             mbar_init(&C.s_full[a], 1);
-            mbar_init(&C.p_full[a], 4);
+            mbar_init(&C.p_full[a][0], 4);
+            mbar_init(&C.p_full[a][1], 4);
             mbar_init(&C.o_full[a], 2);
         }
         for (int s = 0; s < kSched; ++s) {
@@ -180,13 +183,13 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
         uint32_t q_uses[2] = {0, 0};
         int issued[2] = {0, 0}, published = 0;
         bool ok = true;
-        int claim = 0;
-        if (lane == 0) claim = atomicAdd(A.counter, 1);
-        while (ok) {
-            const int idx = __shfl_sync(0xffffffffu, claim, 0);
+        // The next unit off the counter, published to the other warps.
+        auto claim = [&] {
             Unit u{0, 0, 0, -1};
+            int idx = 0;
+            if (lane == 0) idx = atomicAdd(A.counter, 1);
+            idx = __shfl_sync(0xffffffffu, idx, 0);
             if (idx < total) {
-                if (lane == 0) claim = atomicAdd(A.counter, 1);  // the next one, on its way
                 const int pair = idx / A.Hq;
                 u.h = idx - pair * A.Hq;
                 int lo = 0, hi = kScan;  // the thread whose prompts hold it
@@ -208,15 +211,20 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
             if (published >= kSched)
                 ok = wait_or_give_up(&C.sched_empty[rs.slot], rs.phase ^ 1, A.wait_ns, gave_up);
             ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane == 0) {
+            if (ok && lane == 0) {
                 C.unit[rs.slot] = u;
                 mbar_arrive(&C.sched_full[rs.slot]);
             }
+            __syncwarp();
             rs.next(kSched);
             ++published;
-            if (u.h < 0) break;
-
+            return u;
+        };
+        Unit ahead = claim();
+        while (ok && ahead.h >= 0) {
+            const Unit u = ahead;
+            ahead = claim();
+            if (!ok) break;
             const Span s0 = span_of(A, u, 0), s1 = span_of(A, u, 1);
             const int t_lo = s0.lo, t_hi = max(s0.hi, s1.hi), kvh = u.h / A.G;
             for (int a = 0; a < 2 && ok; ++a) {
@@ -280,74 +288,102 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
         Ring rk, rv;
         uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
         bool ok = true;
+        auto warp_test = [&](uint64_t *bar, uint32_t phase) {
+            return __all_sync(0xffffffffu, mbar_test_wait(bar, phase));
+        };
         auto wait = [&](uint64_t *bar, uint32_t phase) {
             ok = ok && wait_or_give_up(bar, phase, A.wait_ns, gave_up);
             ok = __all_sync(0xffffffffu, ok);
         };
-        while (ok) {
-            const Unit u = sched.next(C, A, gave_up, lane);
-            if (u.h < 0) break;
-            const Span sp[2] = {span_of(A, u, 0), span_of(A, u, 1)};
-            const int t_lo = sp[0].lo, t_hi = max(sp[0].hi, sp[1].hi);
-            // S of block a and tile t, whose K is in slot rk
-            auto issue_s = [&](int a, int t) {
-                if (t == sp[a].lo) {
-                    wait(&C.q_full[a], q_uses[a] & 1);
-                    ++q_uses[a];
-                }
-                wait(&C.full[rk.slot], rk.phase);
-                if (!ok) return;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t kd = kd0 + uint32_t(rk.slot) * (kSlotBytes >> 4);
+        struct Work { Unit u; Span sp[2]; int lo, hi; };
+        auto fetch = [&] {
+            Work w;
+            w.u = sched.next(C, A, gave_up, lane);
+            w.sp[0] = w.u.h < 0 ? Span{0, 0} : span_of(A, w.u, 0);
+            w.sp[1] = w.u.h < 0 ? Span{0, 0} : span_of(A, w.u, 1);
+            w.lo = w.sp[0].lo;
+            w.hi = max(w.sp[0].hi, w.sp[1].hi);
+            return w;
+        };
+        // S of block a and tile t, whose K is in slot rk
+        auto issue_s = [&](const Work &w, int a, int t) {
+            if (t < w.sp[a].lo || t >= w.sp[a].hi) return;
+            if (t == w.sp[a].lo) {
+                wait(&C.q_full[a], q_uses[a] & 1);
+                ++q_uses[a];
+            }
+            wait(&C.full[rk.slot], rk.phase);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t kd = kd0 + uint32_t(rk.slot) * (kSlotBytes >> 4);
 #pragma unroll
-                    for (int d = 0; d < D / 16; ++d) {
-                        const uint32_t at = ((d / 4) * kHalfBytes + (d % 4) * 32) >> 4;
-                        mma_ss(tmem + a * kTile, qd + a * (kSlotBytes >> 4) + at, kd + at, id_s, d > 0);
-                    }
-                    mma_commit(&C.s_full[a]);
-                    if (t == sp[a].hi - 1) mma_commit(&C.q_empty[a]);
+                for (int d = 0; d < D / 16; ++d) {
+                    const uint32_t at = ((d / 4) * kHalfBytes + (d % 4) * 32) >> 4;
+                    mma_ss(tmem + a * kTile, qd + a * (kSlotBytes >> 4) + at, kd + at, id_s, d > 0);
                 }
-                __syncwarp();
-            };
-            auto free_k = [&] {
-                if (elect_one()) mma_commit(&C.empty[rk.slot]);
-                __syncwarp();
-                rk.next(A.k_slots);
-            };
-            for (int a = 0; a < 2 && ok; ++a)
-                if (t_lo >= sp[a].lo && t_lo < sp[a].hi) issue_s(a, t_lo);
-            if (!ok) break;
-            free_k();
-            for (int t = t_lo; t < t_hi && ok; ++t) {
-                for (int a = 0; a < 2 && ok; ++a) {
-                    if (t >= sp[a].lo && t < sp[a].hi) {
-                        wait(&C.p_full[a], p_uses[a] & 1);
-                        ++p_uses[a];
+                mma_commit(&C.s_full[a]);
+                if (t == w.sp[a].hi - 1) mma_commit(&C.q_empty[a]);
+            }
+            __syncwarp();
+        };
+        auto free_k = [&] {
+            if (elect_one()) mma_commit(&C.empty[rk.slot]);
+            __syncwarp();
+            rk.next(A.k_slots);
+        };
+        Work w = fetch();
+        for (int a = 0; a < 2 && ok; ++a) issue_s(w, a, w.lo);
+        if (w.hi > 0 && ok) free_k();
+        while (ok && w.hi > 0) {
+            Work nx = w;
+            for (int t = w.lo; t < w.hi && ok; ++t) {
+                // S of the step after this one goes between the two blocks'
+                // products; at a unit's end that is the next unit's.
+                const bool last = t + 1 == w.hi;
+                if (last) nx = fetch();
+                const int tn = last ? nx.lo : t + 1;
+                const bool more = tn < nx.hi;
+                bool s0_late = false;
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    if (t >= w.sp[a].lo && t < w.sp[a].hi) {
                         wait(&C.clean[A.k_slots + rv.slot], rv.phase);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            const uint64_t vd = vd0 + uint32_t(rv.slot) * (kSlotBytes >> 4);
+                        const uint64_t vd = vd0 + uint32_t(rv.slot) * (kSlotBytes >> 4);
 #pragma unroll
-                            for (int k = 0; k < kTile / 16; ++k)
-                                mma_ts(tmem + kColO + a * D, tmem + a * kTile + k * 8, vd + k * (2048 >> 4), id_o,
-                                       !(t == sp[a].lo && k == 0));
-                            if (t == sp[a].hi - 1) {
-                                mbar_arrive(&C.o_full[a]);  // passes the cleaners' word on
-                                mma_commit(&C.o_full[a]);
+                        for (int half = 0; half < 2; ++half) {
+                            wait(&C.p_full[a][half], p_uses[a] & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int k = 4 * half; k < 4 * half + 4; ++k)
+                                    mma_ts(tmem + kColO + a * D, tmem + a * kTile + k * 8, vd + k * (2048 >> 4), id_o,
+                                           !(t == w.sp[a].lo && k == 0));
+                                if (half == 1 && t == w.sp[a].hi - 1) {
+                                    mbar_arrive(&C.o_full[a]);  // passes the cleaners' word on
+                                    mma_commit(&C.o_full[a]);
+                                }
                             }
+                            __syncwarp();
                         }
-                        __syncwarp();
+                        ++p_uses[a];
                     }
-                    if (t + 1 >= sp[a].lo && t + 1 < sp[a].hi) issue_s(a, t + 1);
+                    if (!ok) break;
+                    if (!more) continue;
+                    if (a == 0 && last && !(warp_test(&C.q_full[0], q_uses[0] & 1) && warp_test(&C.full[rk.slot], rk.phase)))
+                        s0_late = true;  // not there yet: block 1's product goes first
+                    else
+                        issue_s(nx, a, tn);
                 }
                 if (!ok) break;
+                if (s0_late) issue_s(nx, 0, tn);
                 if (elect_one()) mma_commit(&C.empty[A.k_slots + rv.slot]);
                 __syncwarp();
                 rv.next(v_slots);
-                if (t + 1 < t_hi) free_k();
+                if (more && ok) free_k();
             }
+            w = nx;
         }
         if (C.gave_up) {
             if (elect_one()) mma_commit(&C.drained);
@@ -422,10 +458,23 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
 #pragma unroll
                 for (int c = 0; c < kTile; c += 32) tmem_use32(s + c);
                 if (partial(A, u, a, t)) {
-                    const int hi = q - t * kTile, lo = A.window > 0 ? hi - A.window : -1;  // sees (lo, hi]
+                    // The row sees keys (lo, hi] of the tile.  By 32 keys, what
+                    // the warp's rows all see stays as it is.
+                    const int hi = q - t * kTile, lo = A.window > 0 ? hi - A.window : -1;
+                    const int hi0 = hi - lane, lo31 = lo + 31 - lane;  // its first row's, its last row's
 #pragma unroll
-                    for (int e = 0; e < kTile; ++e)
-                        if (e > hi || e <= lo) s[e] = -INFINITY;
+                    for (int c = 0; c < kTile; c += 32) {
+                        if (c + 31 > hi0) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (c + e > hi) s[c + e] = -INFINITY;
+                        }
+                        if (A.window > 0 && c <= lo31) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (c + e <= lo) s[c + e] = -INFINITY;
+                        }
+                    }
                 }
                 float m0 = max3(s[0], s[1], s[2]), m1 = max3(s[3], s[4], s[5]);
 #pragma unroll
@@ -465,11 +514,13 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                         p[e / 2] = pack_bf16x2(x.x, x.y);
                     }
                     tmem_st16u(s_tm + c / 2, p);
+                    if (c % 64 == 32) {  // half of the keys: their product may begin
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&C.p_full[a][c / 64]);
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&C.p_full[a]);
             }
             if (!ok) break;
             ok = wait_or_give_up(&C.o_full[a], o_uses & 1, A.wait_ns, gave_up);
@@ -479,25 +530,35 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
             tc_fence_after();
             const float l = l2.x + l2.y, inv = l == 0.f ? 0.f : 1.f / l;
             uint16_t *const out = A.out + ((int64_t)(u.row0 + q) * A.Hq + u.h) * D;
+            // 64 entries of the warp's 32 rows at a time go through shared
+            // memory, so that eight lanes write a row's 128 bytes.
+            const uint32_t mine = stage + warp * 4096;
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(o, o_tm + c);
-                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                tmem_use32(o);
-                if (q < u.n) {
+            for (int c = 0; c < D; c += 64) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 y;
-                        y.x = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-                        y.y = pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv);
-                        y.z = pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv);
-                        y.w = pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv);
-                        *reinterpret_cast<uint4 *>(out + c + e) = y;
-                    }
+                for (int half = 0; half < 64; half += 32) {
+                    float o[32];
+                    tmem_ld32(o, o_tm + c + half);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                    tmem_use32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        st_shared16(mine + lane * 128 + ((((half + e) / 8) ^ (lane & 7)) << 4),
+                                    pack_bf16x2(o[e] * inv, o[e + 1] * inv), pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
+                                    pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv), pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
                 }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const int r = i + lane / 8, ch = lane % 8;
+                    if (q - lane + r < u.n)
+                        *reinterpret_cast<uint4 *>(out + (int64_t)(r - lane) * A.Hq * D + c + ch * 8) =
+                            ld_shared16(mine + r * 128 + ((ch ^ (r & 7)) << 4));
+                }
+                __syncwarp();
             }
             tc_fence_before();
+            __syncwarp();  // the row was written by other lanes
             if (C.poisoned[unit % 8] == unit + 1 && q < u.n) {
                 // what the cleaners took out of the values that this row sees
                 for (int t = sp.lo; t < sp.hi; ++t) {
@@ -526,9 +587,10 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
 template <int D>
 cudaError_t launch(PromptArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStream_t s) {
     const size_t slot = size_t(D) * 2 * kTile;
-    A.slots = int(std::min<size_t>((kSmemBytes - sizeof(Ctrl) - 1024 - 2 * slot) / slot, kSlotsMax));
+    constexpr size_t stage = 8 * 4096;
+    A.slots = int(std::min<size_t>((kSmemBytes - sizeof(Ctrl) - 1024 - stage - 2 * slot) / slot, kSlotsMax));
     A.k_slots = A.slots / 2;
-    const size_t smem = 1024 + (2 + A.slots) * slot;
+    const size_t smem = 1024 + (2 + A.slots) * slot + stage;
     const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
