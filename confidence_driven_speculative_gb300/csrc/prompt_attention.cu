@@ -26,13 +26,12 @@ namespace dspark {
 namespace {
 
 constexpr int kTile = 128;        // rows of a block, keys of a tile
-constexpr int kThreadsP = 384;
+constexpr int kThreadsP = 640;
 constexpr int kScan = 128;        // threads that sum up the prompts' units
-constexpr int kWarpMmaP = 8, kWarpLoad = 9, kWarpClean = 10;  // softmax 0..7; two cleaners
-constexpr int kCleaners = 64;
+constexpr int kWarpMma = 0, kWarpLoad = 1, kWarpReady = 2, kWarpSoft = 4;  // 3: idle; softmax 4..19
 constexpr int kSlotsMax = 10;
 constexpr int kSched = 4;         // units on their way to the warps
-constexpr int kSchedReaders = 11; // warps that read them
+constexpr int kSchedReaders = 18; // warps that read them
 constexpr float kRefMin = -1e30f;
 constexpr float kRefSlack = 32.0f;
 constexpr size_t kSmemBytes = 232448;
@@ -40,6 +39,7 @@ constexpr size_t kSmemBytes = 232448;
 struct PromptArgs {
     int B, rows, q_max, Hq, Hkv, G, window;
     int slots, k_slots;
+    int wide_out;      // out is 32-byte aligned
     float scale2;
     int64_t v_stride;
     const uint16_t *v;
@@ -72,17 +72,30 @@ __device__ __forceinline__ bool partial(const PromptArgs &A, const Unit &u, int 
 }
 
 struct Ctrl {
-    uint64_t full[kSlotsMax], empty[kSlotsMax], clean[kSlotsMax];
+    uint64_t full[kSlotsMax], empty[kSlotsMax];
     uint64_t q_full[2], q_empty[2], s_full[2], o_full[2];
-    uint64_t p_full[2][2];    // by block and half of the keys
+    uint64_t p_full[2];       // P is written, and V of its tile and K of the next one are there
     uint64_t sched_full[kSched], sched_empty[kSched], drained;
     Unit unit[kSched];
     int poisoned[8];          // by unit number % 8: the last unit + 1 that lost values
     int pairs[kScan + 1];     // exclusive sums of the units (per head) of each thread's prompts
     int warp_sum[kScan / 32];
+    float swap[2][2][2][kTile];  // between the two threads of a row (maxima, sums): by block and half
     uint32_t tmem;
     int gave_up;
 };
+
+// 16 bfloat16 of one row: a whole sector where the alignment allows.
+__device__ __forceinline__ void st_global32(uint16_t *p, const uint32_t (&y)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     ::"l"(p), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+}
 
 // Reads the next unit off the ring.
 struct SchedReader {
@@ -115,21 +128,18 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
     const uint32_t ring = q_smem + 2 * kSlotBytes;
     const int v_slots = A.slots - A.k_slots;
     const uint32_t v_ring = ring + A.k_slots * kSlotBytes;
-    const uint32_t stage = ring + A.slots * kSlotBytes;  // 4 KB for each softmax warp
     volatile int *gave_up = &C.gave_up;
 
     if (tid == 0) {
         for (int s = 0; s < A.slots; ++s) {
             mbar_init(&C.full[s], 1);
             mbar_init(&C.empty[s], 1);
-            mbar_init(&C.clean[s], 2);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&C.q_full[a], 1);
             mbar_init(&C.q_empty[a], 1);
             mbar_init(&C.s_full[a], 1);
-            mbar_init(&C.p_full[a][0], 4);
-            mbar_init(&C.p_full[a][1], 4);
+            mbar_init(&C.p_full[a], 9);
             mbar_init(&C.o_full[a], 2);
         }
         for (int s = 0; s < kSched; ++s) {
@@ -141,7 +151,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
         C.gave_up = 0;
         fence_barrier_init();
     }
-    if (warp == kWarpMmaP) tmem_alloc(&C.tmem, 512);
+    if (warp == kWarpMma) tmem_alloc(&C.tmem, 512);
     if (warp == kWarpLoad && lane == 0) {
         prefetch_map(&q_map);
         prefetch_map(&k_map);
@@ -279,109 +289,133 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                 A.counter[1] = 0;
             }
         }
-    } else if (warp == kWarpMmaP) {
+    } else if (warp == kWarpMma) {
         // ---- MMA issuer -----------------------------------------------------
         const uint64_t qd = smem_desc(q_smem, 16, 1024), kd0 = smem_desc(ring, 16, 1024);
         const uint64_t vd0 = smem_desc(v_ring, kHalfBytes, 1024);
         constexpr uint32_t id_s = mma_idesc(128, kTile, false, false), id_o = mma_idesc(128, D, false, true);
         SchedReader sched;
         Ring rk, rv;
-        uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+        uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
         bool ok = true;
-        auto warp_test = [&](uint64_t *bar, uint32_t phase) {
-            return __all_sync(0xffffffffu, mbar_test_wait(bar, phase));
-        };
         auto wait = [&](uint64_t *bar, uint32_t phase) {
             ok = ok && wait_or_give_up(bar, phase, A.wait_ns, gave_up);
             ok = __all_sync(0xffffffffu, ok);
         };
-        struct Work { Unit u; Span sp[2]; int lo, hi; };
+        // A unit's tiles.  They come from lane 0 by shuffles, which the
+        // compiler knows to be the same in all lanes.
+        struct Work { Span sp[2]; int lo, hi; };
         auto fetch = [&] {
             Work w;
-            w.u = sched.next(C, A, gave_up, lane);
-            w.sp[0] = w.u.h < 0 ? Span{0, 0} : span_of(A, w.u, 0);
-            w.sp[1] = w.u.h < 0 ? Span{0, 0} : span_of(A, w.u, 1);
+            const Unit u = sched.next(C, A, gave_up, lane);
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                w.sp[a] = u.h < 0 ? Span{0, 0} : span_of(A, u, a);
+                w.sp[a].lo = __shfl_sync(0xffffffffu, w.sp[a].lo, 0);
+                w.sp[a].hi = __shfl_sync(0xffffffffu, w.sp[a].hi, 0);
+            }
             w.lo = w.sp[0].lo;
             w.hi = max(w.sp[0].hi, w.sp[1].hi);
             return w;
         };
-        // S of block a and tile t, whose K is in slot rk
-        auto issue_s = [&](const Work &w, int a, int t) {
-            if (t < w.sp[a].lo || t >= w.sp[a].hi) return;
-            if (t == w.sp[a].lo) {
-                wait(&C.q_full[a], q_uses[a] & 1);
-                ++q_uses[a];
-            }
-            wait(&C.full[rk.slot], rk.phase);
-            if (!ok) return;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t kd = kd0 + uint32_t(rk.slot) * (kSlotBytes >> 4);
+        auto has = [](const Span &s, int t) { return t >= s.lo && t < s.hi; };
+        // S of block a and the tile whose K is in slot rk; by one lane
+        auto issue_s = [&](int a, bool last) {
+            const uint64_t kd = kd0 + uint32_t(rk.slot) * (kSlotBytes >> 4);
 #pragma unroll
-                for (int d = 0; d < D / 16; ++d) {
-                    const uint32_t at = ((d / 4) * kHalfBytes + (d % 4) * 32) >> 4;
-                    mma_ss(tmem + a * kTile, qd + a * (kSlotBytes >> 4) + at, kd + at, id_s, d > 0);
-                }
-                mma_commit(&C.s_full[a]);
-                if (t == w.sp[a].hi - 1) mma_commit(&C.q_empty[a]);
+            for (int d = 0; d < D / 16; ++d) {
+                const uint32_t at = ((d / 4) * kHalfBytes + (d % 4) * 32) >> 4;
+                mma_ss(tmem + a * kTile, qd + a * (kSlotBytes >> 4) + at, kd + at, id_s, d > 0);
             }
-            __syncwarp();
+            mma_commit(&C.s_full[a]);
+            if (last) mma_commit(&C.q_empty[a]);
         };
-        auto free_k = [&] {
+        Work w = fetch();
+        if (w.hi > 0) {
+            wait(&C.full[rk.slot], rk.phase);
+            for (int a = 0; a < 2; ++a) {
+                if (!has(w.sp[a], w.lo)) continue;
+                wait(&C.q_full[a], q_phase[a]);
+                q_phase[a] ^= 1;
+                tc_fence_after();
+                if (elect_one()) issue_s(a, w.sp[a].hi == w.lo + 1);
+                __syncwarp();
+            }
             if (elect_one()) mma_commit(&C.empty[rk.slot]);
             __syncwarp();
             rk.next(A.k_slots);
+        }
+        // O += P V of block a's tile, whose V is in slot rv; by one lane
+        auto issue_o = [&](int a, bool first) {
+            const uint64_t vd = vd0 + uint32_t(rv.slot) * (kSlotBytes >> 4);
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(tmem + kColO + a * D, tmem + a * kTile + k * 8, vd + k * (2048 >> 4), id_o, !(first && k == 0));
         };
-        Work w = fetch();
-        for (int a = 0; a < 2 && ok; ++a) issue_s(w, a, w.lo);
-        if (w.hi > 0 && ok) free_k();
         while (ok && w.hi > 0) {
             Work nx = w;
+            // O += P V of a step and S of the next one go out together for a
+            // block: 16 products behind one wait, since the tensor cores queue
+            // hardly any and idle while this warp waits and tests.
             for (int t = w.lo; t < w.hi && ok; ++t) {
-                // S of the step after this one goes between the two blocks'
-                // products; at a unit's end that is the next unit's.
+                if (t > w.sp[0].lo && t > w.sp[1].lo && t + 1 < w.sp[0].hi && t + 1 < w.sp[1].hi) {
+                    // both blocks, neither at an end: as little as can be
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        wait(&C.p_full[a], p_phase[a]);
+                        p_phase[a] ^= 1;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            issue_o(a, false);
+                            issue_s(a, t + 2 == w.sp[a].hi);
+                            if (a == 1) {
+                                mma_commit(&C.empty[A.k_slots + rv.slot]);
+                                mma_commit(&C.empty[rk.slot]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    rv.next(v_slots);
+                    rk.next(A.k_slots);
+                    continue;
+                }
                 const bool last = t + 1 == w.hi;
-                if (last) nx = fetch();
+                if (last) nx = fetch();  // S of the next step is the next unit's
                 const int tn = last ? nx.lo : t + 1;
                 const bool more = tn < nx.hi;
-                bool s0_late = false;
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    if (t >= w.sp[a].lo && t < w.sp[a].hi) {
-                        wait(&C.clean[A.k_slots + rv.slot], rv.phase);
-                        const uint64_t vd = vd0 + uint32_t(rv.slot) * (kSlotBytes >> 4);
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            wait(&C.p_full[a][half], p_uses[a] & 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                            if (elect_one()) {
-#pragma unroll
-                                for (int k = 4 * half; k < 4 * half + 4; ++k)
-                                    mma_ts(tmem + kColO + a * D, tmem + a * kTile + k * 8, vd + k * (2048 >> 4), id_o,
-                                           !(t == w.sp[a].lo && k == 0));
-                                if (half == 1 && t == w.sp[a].hi - 1) {
-                                    mbar_arrive(&C.o_full[a]);  // passes the cleaners' word on
-                                    mma_commit(&C.o_full[a]);
-                                }
-                            }
-                            __syncwarp();
-                        }
-                        ++p_uses[a];
+                    const bool pv = has(w.sp[a], t), s = more && has(nx.sp[a], tn);
+                    if (s && tn == nx.sp[a].lo) {
+                        wait(&C.q_full[a], q_phase[a]);
+                        q_phase[a] ^= 1;
+                    }
+                    if (pv) {
+                        wait(&C.p_full[a], p_phase[a]);
+                        p_phase[a] ^= 1;
+                    } else if (s) {
+                        wait(&C.full[rk.slot], rk.phase);
                     }
                     if (!ok) break;
-                    if (!more) continue;
-                    if (a == 0 && last && !(warp_test(&C.q_full[0], q_uses[0] & 1) && warp_test(&C.full[rk.slot], rk.phase)))
-                        s0_late = true;  // not there yet: block 1's product goes first
-                    else
-                        issue_s(nx, a, tn);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (pv) {
+                            issue_o(a, t == w.sp[a].lo);
+                            if (t == w.sp[a].hi - 1) {
+                                mbar_arrive(&C.o_full[a]);  // passes on what was lost of V
+                                mma_commit(&C.o_full[a]);
+                            }
+                        }
+                        if (s) issue_s(a, tn == nx.sp[a].hi - 1);
+                        if (a == 1) {
+                            mma_commit(&C.empty[A.k_slots + rv.slot]);
+                            if (more) mma_commit(&C.empty[rk.slot]);
+                        }
+                    }
+                    __syncwarp();
                 }
-                if (!ok) break;
-                if (s0_late) issue_s(nx, 0, tn);
-                if (elect_one()) mma_commit(&C.empty[A.k_slots + rv.slot]);
-                __syncwarp();
                 rv.next(v_slots);
-                if (more && ok) free_k();
+                if (more) rk.next(A.k_slots);
             }
             w = nx;
         }
@@ -390,80 +424,103 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
             __syncwarp();
             mbar_wait_bounded(&C.drained, 0, kDrainTimeoutNs);
         }
-    } else if (warp >= kWarpClean) {
-        // ---- cleaners: masked keys must not reach O through 0 * infinity.  A
-        // value tile that some row does not see in full loses its NaN and
-        // infinities; the epilogue adds them to the rows that see them. -----
+    } else if (warp == kWarpReady) {
+        // ---- the last of P's arrivals: V of its tile and K of the next are there,
+        // so that the MMA issuer has one barrier to test and not three ----------
         SchedReader sched;
-        Ring rv;
-        const int id = tid - kWarpClean * 32;
+        Ring rk, rv;
+        rk.next(A.k_slots);  // the first K is waited for by the MMA issuer
+        uint32_t uses[2] = {0, 0};
         bool ok = true;
-        for (int unit = 0; ok; ++unit) {
-            const Unit u = sched.next(C, A, gave_up, lane);
-            if (u.h < 0) break;
-            const Span s0 = span_of(A, u, 0), s1 = span_of(A, u, 1);
-            for (int t = s0.lo; t < max(s0.hi, s1.hi); ++t) {
-                const int slot = A.k_slots + rv.slot;
-                ok = wait_or_give_up(&C.full[slot], rv.phase, A.wait_ns, gave_up);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if ((t >= s0.lo && t < s0.hi && partial(A, u, 0, t)) ||
-                    (t >= s1.lo && t < s1.hi && partial(A, u, 1, t))) {
-                    const uint32_t at0 = v_ring + rv.slot * kSlotBytes + id * 16;
-                    bool lost = false;
-#pragma unroll 4
-                    for (uint32_t c = 0; c < kSlotBytes; c += kCleaners * 16) {
-                        const uint4 x = ld_shared16(at0 + c);
-                        const uint32_t mx = nonfinite_mask(x.x), my = nonfinite_mask(x.y),
-                                       mz = nonfinite_mask(x.z), mw = nonfinite_mask(x.w);
-                        if (mx | my | mz | mw) {
-                            st_shared16(at0 + c, x.x & ~mx, x.y & ~my, x.z & ~mz, x.w & ~mw);
-                            lost = true;
-                        }
-                    }
-                    if (lost) C.poisoned[unit % 8] = unit + 1;
-                    fence_async_shared();
+        Unit u = sched.next(C, A, gave_up, lane);
+        while (ok && u.h >= 0) {
+            const Span sp[2] = {span_of(A, u, 0), span_of(A, u, 1)};
+            const int t_hi = max(sp[0].hi, sp[1].hi);
+            Unit nx = u;
+            for (int t = sp[0].lo; t < t_hi && ok; ++t) {
+                ok = wait_or_give_up(&C.full[A.k_slots + rv.slot], rv.phase, A.wait_ns, gave_up);
+                if (t + 1 == t_hi) nx = sched.next(C, A, gave_up, lane);
+                if (nx.h >= 0) {
+                    ok = ok && wait_or_give_up(&C.full[rk.slot], rk.phase, A.wait_ns, gave_up);
+                    rk.next(A.k_slots);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&C.clean[slot]);
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    if (t < sp[a].lo || t >= sp[a].hi) continue;
+                    // not before the tile before is through
+                    if (uses[a] > 0)
+                        ok = ok && wait_or_give_up(&C.p_full[a], (uses[a] - 1) & 1, A.wait_ns, gave_up);
+                    ++uses[a];
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (ok && lane == 0) mbar_arrive(&C.p_full[a]);
+                }
+                ok = __all_sync(0xffffffffu, ok);
                 rv.next(v_slots);
             }
+            u = nx;
         }
-    } else {
-        // ---- softmax and output: thread = row of block a -----------------------
-        const int a = warp >> 2, row = tid & 127;
+    } else if (warp >= kWarpSoft) {
+        // ---- softmax and output --------------------------------------------------
+        // Two threads share a row of block a: thread `half` takes 64 keys of
+        // each tile, and 64 (32) entries of O.  The halves' warps meet twice
+        // where they must: both have read S before either writes P over it,
+        // and both know of a reference that moves.
+        const int sw = warp - kWarpSoft, a = sw >> 3, half = (sw >> 2) & 1, row = (warp & 3) * 32 + lane;
+        constexpr int kKeys = kTile / 2, kEntries = D / 2;
         const uint32_t lane_tm = tmem + (uint32_t((warp & 3) * 32) << 16);
-        const uint32_t s_tm = lane_tm + a * kTile, o_tm = lane_tm + kColO + a * D;
+        const uint32_t s_tm = lane_tm + a * kTile, o_tm = lane_tm + kColO + a * D + half * kEntries;
+        const uint32_t pair_bar = 1 + a * 4 + (warp & 3);
+        auto pair_any = [&](bool x) {
+            uint32_t r;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.u32 q, %2, 0;\n\t"
+                "barrier.cta.red.or.pred p, %1, 64, q;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(r) : "r"(pair_bar), "r"(uint32_t(x)) : "memory");
+            return r != 0;
+        };
+        auto pair_sync = [&] { asm volatile("barrier.cta.sync %0, 64;" ::"r"(pair_bar) : "memory"); };
+        // The other thread's x.  A pair_any lies between two uses of a kind.
+        auto exchange = [&](int kind, float x) {
+            C.swap[kind][a][half][row] = x;
+            pair_sync();
+            return C.swap[kind][a][half ^ 1][row];
+        };
         SchedReader sched;
+        Ring rv;  // of the block's next tile
         uint32_t s_uses = 0, o_uses = 0;
-        bool ok = true;
-        for (int unit = 0; ok; ++unit) {
+        for (int unit = 0;; ++unit) {
             const Unit u = sched.next(C, A, gave_up, lane);
-            if (u.h < 0) break;
-            const Span sp = span_of(A, u, a);
+            if (pair_any(u.h < 0)) break;
+            const Span sp = span_of(A, u, a), other = span_of(A, u, a ^ 1);
+            const int t_lo = a ? other.lo : sp.lo, t_hi = max(sp.hi, other.hi);
+            for (int t = t_lo; t < (sp.hi == 0 ? t_hi : sp.lo); ++t) rv.next(v_slots);
             if (sp.hi == 0) continue;
-            const int q = u.q0 + a * kTile + row;  // the thread's row; past the prompt: computed, not stored
+            const int q = u.q0 + a * kTile + row;  // the row; past the prompt: computed, not stored
             float ref = 0.f;
             float2 l2 = make_float2(0.f, 0.f);
+            // Once a wait has given up, the others return at once and the
+            // loops run to their ends on whatever there is; the status tells.
             for (int t = sp.lo; t < sp.hi; ++t) {
-                ok = wait_or_give_up(&C.s_full[a], s_uses & 1, A.wait_ns, gave_up);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                wait_or_give_up(&C.s_full[a], s_uses & 1, A.wait_ns, gave_up);
+                __syncwarp();
                 ++s_uses;
                 tc_fence_after();
-                float s[kTile];
+                float s[kKeys];
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32) tmem_ld32(s + c, s_tm + c);
+                for (int c = 0; c < kKeys; c += 32) tmem_ld32(s + c, s_tm + half * kKeys + c);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32) tmem_use32(s + c);
-                if (partial(A, u, a, t)) {
-                    // The row sees keys (lo, hi] of the tile.  By 32 keys, what
-                    // the warp's rows all see stays as it is.
-                    const int hi = q - t * kTile, lo = A.window > 0 ? hi - A.window : -1;
+                for (int c = 0; c < kKeys; c += 32) tmem_use32(s + c);
+                const bool cut = partial(A, u, a, t);
+                if (cut) {
+                    // The row sees keys (lo, hi] of the half tile.  By 32 keys,
+                    // what the warp's rows all see stays as it is.
+                    const int hi = q - t * kTile - half * kKeys, lo = A.window > 0 ? hi - A.window : -1;
                     const int hi0 = hi - lane, lo31 = lo + 31 - lane;  // its first row's, its last row's
 #pragma unroll
-                    for (int c = 0; c < kTile; c += 32) {
+                    for (int c = 0; c < kKeys; c += 32) {
                         if (c + 31 > hi0) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
@@ -478,32 +535,38 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                 }
                 float m0 = max3(s[0], s[1], s[2]), m1 = max3(s[3], s[4], s[5]);
 #pragma unroll
-                for (int e = 6; e < kTile - 2; e += 4) {
+                for (int e = 6; e < kKeys - 2; e += 4) {
                     m0 = max3(m0, s[e], s[e + 1]);
                     m1 = max3(m1, s[e + 2], s[e + 3]);
                 }
-                const float m = max3(m0, m1, fmaxf(s[kTile - 2], s[kTile - 1])) * A.scale2;
-                if (t == sp.lo) {
-                    ref = fmaxf(m, kRefMin);
-                } else if (__any_sync(0xffffffffu, m > ref + kRefSlack)) {
-                    const float now = m > ref + kRefSlack ? m : ref;
-                    const float f = exp2_approx(ref - now);
-                    ref = now;
-                    l2.x *= f;
-                    l2.y *= f;
+                const float m = max3(m0, m1, fmaxf(s[kKeys - 2], s[kKeys - 1])) * A.scale2;
+                const bool first = t == sp.lo;
+                if (pair_any(first || m > ref + kRefSlack)) {
+                    const float now = fmaxf(fmaxf(m, exchange(0, m)), kRefMin);
+                    if (first) {
+                        ref = now;
+                    } else {
+                        const float to = now > ref + kRefSlack ? now : ref, f = exp2_approx(ref - to);
+                        ref = to;
+                        l2.x *= f;
+                        l2.y *= f;
 #pragma unroll
-                    for (int c = 0; c < D; c += 16) {
-                        float o[16];
-                        tmem_ld16(o, o_tm + c);
-                        tmem_wait_ld(o);
+                        for (int c = 0; c < kEntries; c += 16) {
+                            float o[16];
+                            tmem_ld16(o, o_tm + c);
+                            tmem_wait_ld(o);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] *= f;
-                        tmem_st16(o_tm + c, o);
+                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            tmem_st16(o_tm + c, o);
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
+                        pair_sync();  // all of O is rescaled before either half's P is used
                     }
                 }
                 const float2 sc = make_float2(A.scale2, A.scale2), nr = make_float2(-ref, -ref);
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32) {
+                for (int c = 0; c < kKeys; c += 32) {
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
@@ -513,62 +576,68 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                         l2 = add2(l2, x);
                         p[e / 2] = pack_bf16x2(x.x, x.y);
                     }
-                    tmem_st16u(s_tm + c / 2, p);
-                    if (c % 64 == 32) {  // half of the keys: their product may begin
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&C.p_full[a][c / 64]);
+                    tmem_st16u(s_tm + (half * kKeys + c) / 2, p);
+                }
+                if (cut) {
+                    // Masked keys must not reach O through 0 * infinity: a value
+                    // tile that some row does not see in full loses its NaN and
+                    // infinities; the rows that see them get them back at the
+                    // unit's end.  (The other block may read the tile before or
+                    // after: what it then gets back it already has, or lacks.)
+                    wait_or_give_up(&C.full[A.k_slots + rv.slot], rv.phase, A.wait_ns, gave_up);
+                    __syncwarp();
+                    const uint32_t at0 = v_ring + rv.slot * kSlotBytes + (half * kTile + row) * 16;
+                    bool lost = false;
+#pragma unroll
+                    for (uint32_t c = 0; c < kSlotBytes; c += 2 * kTile * 16) {
+                        const uint4 x = ld_shared16(at0 + c);
+                        if (nonfinite_any(x)) {
+                            st_shared16(at0 + c, x.x & ~nonfinite_mask(x.x), x.y & ~nonfinite_mask(x.y),
+                                        x.z & ~nonfinite_mask(x.z), x.w & ~nonfinite_mask(x.w));
+                            lost = true;
+                        }
+                    }
+                    if (lost) C.poisoned[unit % 8] = unit + 1;
+                    fence_async_shared();
+                }
+                rv.next(v_slots);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&C.p_full[a]);
+            }
+            for (int t = sp.hi; t < t_hi; ++t) rv.next(v_slots);
+            const float mine = l2.x + l2.y, l = mine + exchange(1, mine), inv = l == 0.f ? 0.f : 1.f / l;
+            wait_or_give_up(&C.o_full[a], o_uses & 1, A.wait_ns, gave_up);
+            __syncwarp();
+            ++o_uses;
+            tc_fence_after();
+            uint16_t *const out = A.out + ((int64_t)(u.row0 + q) * A.Hq + u.h) * D + half * kEntries;
+#pragma unroll
+            for (int c = 0; c < kEntries; c += 32) {
+                float o[32];
+                tmem_ld32(o, o_tm + c);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                tmem_use32(o);
+                if (c + 32 == kEntries) tc_fence_before();
+                if (q < u.n) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(o[e + 2 * i] * inv, o[e + 2 * i + 1] * inv);
+                        st_global32(out + c + e, y, A.wide_out);
                     }
                 }
             }
-            if (!ok) break;
-            ok = wait_or_give_up(&C.o_full[a], o_uses & 1, A.wait_ns, gave_up);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            ++o_uses;
-            tc_fence_after();
-            const float l = l2.x + l2.y, inv = l == 0.f ? 0.f : 1.f / l;
-            uint16_t *const out = A.out + ((int64_t)(u.row0 + q) * A.Hq + u.h) * D;
-            // 64 entries of the warp's 32 rows at a time go through shared
-            // memory, so that eight lanes write a row's 128 bytes.
-            const uint32_t mine = stage + warp * 4096;
-#pragma unroll
-            for (int c = 0; c < D; c += 64) {
-#pragma unroll
-                for (int half = 0; half < 64; half += 32) {
-                    float o[32];
-                    tmem_ld32(o, o_tm + c + half);
-                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                    tmem_use32(o);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        st_shared16(mine + lane * 128 + ((((half + e) / 8) ^ (lane & 7)) << 4),
-                                    pack_bf16x2(o[e] * inv, o[e + 1] * inv), pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
-                                    pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv), pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
-                }
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const int r = i + lane / 8, ch = lane % 8;
-                    if (q - lane + r < u.n)
-                        *reinterpret_cast<uint4 *>(out + (int64_t)(r - lane) * A.Hq * D + c + ch * 8) =
-                            ld_shared16(mine + r * 128 + ((ch ^ (r & 7)) << 4));
-                }
-                __syncwarp();
-            }
-            tc_fence_before();
-            __syncwarp();  // the row was written by other lanes
             if (C.poisoned[unit % 8] == unit + 1 && q < u.n) {
-                // what the cleaners took out of the values that this row sees
+                // what was taken out of the values that this row sees
                 for (int t = sp.lo; t < sp.hi; ++t) {
-                    const bool mixed = partial(A, u, a, t) ||
-                                       (span_of(A, u, a ^ 1).hi > t && span_of(A, u, a ^ 1).lo <= t && partial(A, u, a ^ 1, t));
-                    if (!mixed) continue;
+                    if (!partial(A, u, a, t) && !(t >= other.lo && t < other.hi && partial(A, u, a ^ 1, t))) continue;
                     for (int k = t * kTile; k < min((t + 1) * kTile, q + 1); ++k) {
                         if (A.window > 0 && k <= q - A.window) continue;
-                        const uint16_t *v = A.v + (int64_t)(u.row0 + k) * A.v_stride + (u.h / A.G) * D;
-                        for (int d = 0; d < D; ++d) {
+                        const uint16_t *v = A.v + (int64_t)(u.row0 + k) * A.v_stride + (u.h / A.G) * D + half * kEntries;
+                        for (int d = 0; d < kEntries; ++d) {
                             const float x = bf16_lo(v[d]);
                             if (!isfinite(x)) out[d] = uint16_t(pack_bf16x2(bf16_lo(out[d]) + x, 0.f));
                         }
@@ -581,16 +650,15 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && C.gave_up) atomicOr(A.status, kStatusWaitTimeout);
-    if (warp == kWarpMmaP) tmem_free(tmem, 512);
+    if (warp == kWarpMma) tmem_free(tmem, 512);
 }
 
 template <int D>
 cudaError_t launch(PromptArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStream_t s) {
     const size_t slot = size_t(D) * 2 * kTile;
-    constexpr size_t stage = 8 * 4096;
-    A.slots = int(std::min<size_t>((kSmemBytes - sizeof(Ctrl) - 1024 - stage - 2 * slot) / slot, kSlotsMax));
+    A.slots = int(std::min<size_t>((kSmemBytes - sizeof(Ctrl) - 1024 - 2 * slot) / slot, kSlotsMax));
     A.k_slots = A.slots / 2;
-    const size_t smem = 1024 + (2 + A.slots) * slot + stage;
+    const size_t smem = 1024 + (2 + A.slots) * slot;
     const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
@@ -609,6 +677,7 @@ cudaError_t launch_prompt_attention(const dspark_attn &a, int sms, uint64_t wait
     A.v = static_cast<const uint16_t *>(a.v);
     A.row_off = a.row_off;
     A.out = static_cast<uint16_t *>(a.out);
+    A.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
     A.status = static_cast<int32_t *>(a.workspace);
     A.counter = static_cast<int32_t *>(a.workspace) + 1;
     A.wait_ns = wait_ns;

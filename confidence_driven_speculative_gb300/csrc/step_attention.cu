@@ -683,13 +683,12 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 polls = 0;
                 continue;
             }
-            if (polls == 0) since = global_timer_ns();
-            if ((++polls & 63u) == 0) {
-                const bool over = *gave_up || global_timer_ns() - since > A.wait_ns;
-                if (__any_sync(0xffffffffu, over)) {
-                    *gave_up = 1;
-                    break;
-                }
+            if ((++polls & 255u) != 0) continue;
+            const uint64_t now = global_timer_ns();
+            if (polls == 256) since = now;
+            if (__any_sync(0xffffffffu, *gave_up || now - since > A.wait_ns)) {
+                *gave_up = 1;
+                break;
             }
         }
         if (C.gave_up) {

@@ -190,6 +190,13 @@ __device__ __forceinline__ uint32_t nonfinite_mask(uint32_t w) {
     return m;
 }
 
+// Is there one among the eight?  Adding one to a field of ones carries into
+// the sign's place, which the mask has cleared.
+__device__ __forceinline__ bool nonfinite_any(const uint4 &x) {
+    const uint32_t e = 0x7f807f80u, one = 0x00800080u;
+    return ((((x.x & e) + one) | ((x.y & e) + one) | ((x.z & e) + one) | ((x.w & e) + one)) & 0x80008000u) != 0;
+}
+
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
@@ -250,15 +257,19 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 }
 
 // Wait for phase `parity` of `bar`; false after `limit_ns`, or once another
-// warp of the CTA has given up (*gave_up).
+// warp of the CTA has given up (*gave_up).  The timer is read only after some
+// polls: reading it takes longer than an ordinary wait.
 __device__ __forceinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
                                                 volatile int *gave_up) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
+    uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
-        if (*gave_up) return false;
         if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 15u) == 0 && global_timer_ns() - t0 > limit_ns) {
+        if ((it & 31u) != 0) continue;
+        if (*gave_up) return false;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) {
+            t0 = now;
+        } else if (now - t0 > limit_ns) {
             *gave_up = 1;
             return false;
         }
