@@ -157,6 +157,10 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
         prefetch_map(&k_map);
         prefetch_map(&v_map);
     }
+    // Nothing before this line reads or writes memory that another kernel may
+    // touch: the launch may overlap the end of the kernel before it.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Units of each thread's prompts.
     const int per = (A.B + kScan - 1) / kScan;
     auto prompt = [&](int b, int &row0) {
@@ -662,8 +666,7 @@ cudaError_t launch(PromptArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStr
     const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    prompt_attention_kernel<D><<<ctas, kThreadsP, smem, s>>>(A, maps[0], maps[1], maps[2]);
-    return cudaGetLastError();
+    return launch_overlapped(prompt_attention_kernel<D>, ctas, kThreadsP, smem, s, A, maps[0], maps[1], maps[2]);
 }
 
 }  // namespace

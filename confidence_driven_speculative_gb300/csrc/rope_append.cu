@@ -14,6 +14,7 @@
 // heads are in flight before the angles are needed.
 #include "attn.cuh"
 #include "dspark_internal.cuh"
+#include "tcgen05.cuh"
 
 namespace dspark {
 namespace {
@@ -63,6 +64,8 @@ template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs A) {
     constexpr int kLanes = D / 16;  // threads of a head, two 16-byte chunks each
     constexpr int kHeads = kRopeThreads / kLanes;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int r = blockIdx.x;
     const int b = A.row_req[r];
     const int pos = A.packed_pos[r];
@@ -141,8 +144,7 @@ cudaError_t launch_rope_append(const dspark_attn &a, cudaStream_t s) {
     if (!a.k) A.page_size = 1;  // not checked, not used
     auto *kernel = a.D == 128 ? (a.interleaved ? rope_append_kernel<128, true> : rope_append_kernel<128, false>)
                               : (a.interleaved ? rope_append_kernel<64, true> : rope_append_kernel<64, false>);
-    kernel<<<a.rows, kRopeThreads, 0, s>>>(A);
-    return cudaGetLastError();
+    return launch_overlapped(kernel, a.rows, kRopeThreads, 0, s, A);
 }
 
 }  // namespace dspark

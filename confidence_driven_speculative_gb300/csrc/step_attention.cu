@@ -51,6 +51,7 @@ constexpr int kThreadsStep = 640;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRefMin = -1e30f;  // reference of a column without a score yet
 constexpr float kRefSlack = 32.0f; // log2: how far a score may pass the reference
+constexpr int kWarpScan = 128;         // up to so many requests, every warp finds the cut by itself
 constexpr int kUnitCost = 2;           // what a unit costs beside its tiles, in tiles
 constexpr size_t kSmemBytes = 232448;  // shared memory of a CTA
 
@@ -124,9 +125,9 @@ struct Unit {
         ncols = min(q.per, q.n - j0) * A.G;
     }
     // Unit `i` of request b's list.
-    __device__ __forceinline__ void start(const StepArgs &A, int b_, int i) {
+    __device__ __forceinline__ void start(const StepArgs &A, int b_, const Req &q_, int i) {
         b = b_;
-        q = load_req(A, b);
+        q = q_;
         h = i / q.blocks;
         blk = i - h * q.blocks;
         shape(A);
@@ -151,6 +152,7 @@ struct Unit {
 // the last one that is not.
 struct Cuts {
     int parts, each, more;
+    Cuts() = default;
     __device__ __forceinline__ Cuts(int total, int ctas) {
         parts = min(ctas, max(total, 1));
         each = total / parts;
@@ -344,106 +346,184 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
     const uint32_t col_o = A.ncap * (1 + A.two_s), col_l = col_o + A.ncap;
 
     // ---- set-up: barriers, TMEM, the constant operand, the CTA's tiles -----
-    if (tid == 0) {
-        for (int s = 0; s < A.slots; ++s) {
-            mbar_init(&C.full[s], 2);
-            mbar_init(&C.empty[s], 1);
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&C.q_full[s], 1);
-            mbar_init(&C.q_empty[s], 1);
-            mbar_init(&C.s_full[s], 2);
-            mbar_init(&C.p_full[s], 1);
-            mbar_init(&C.pv_done[s], 1);
-        }
+    if (warp == kWarpMma) tmem_alloc(&C.tmem, kTmemCols);
+    if (tid < kMaxSlots) {
+        mbar_init(&C.full[tid], 2);
+        mbar_init(&C.empty[tid], 1);
+    } else if (tid >= 32 && tid < 34) {
+        const int s = tid - 32;
+        mbar_init(&C.q_full[s], 1);
+        mbar_init(&C.q_empty[s], 1);
+        mbar_init(&C.s_full[s], 2);
+        mbar_init(&C.p_full[s], 1);
+        mbar_init(&C.pv_done[s], 1);
+    } else if (tid == 64) {
         mbar_init(&C.drained, 1);
-        C.gave_up = 0;
-        C.poison = 0;
-        C.joins = 0;
+        C.gave_up = C.poison = C.joins = 0;
         C.start_b = C.start_unit = C.start_tile = 0;
         C.tiles_before[0] = C.tiles_before[1] = 0;
-        fence_barrier_init();
-    }
-    if (tid < 64) st_shared16(ones + tid * 16, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-    fence_async_shared();
-    if (warp == kWarpMma) tmem_alloc(&C.tmem, kTmemCols);
-    if (warp == kWarpK && lane == 0) {
+    } else if (tid == 96) {
         prefetch_map(&q_map);
         prefetch_map(&k_map);
         prefetch_map(&v_map);
+    } else if (tid >= 128 && tid < 192) {
+        st_shared16(ones + (tid - 128) * 16, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
     }
+    fence_barrier_init();
+
+    // Nothing before this line reads or writes memory that another kernel may
+    // touch: the launch may overlap the end of the kernel before it.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // The list of all units' tiles, each unit with unit_cost further places in
     // front for what it costs beside its tiles, is cut evenly.
-    const int U = A.unit_cost;
-    const int per = (A.B + kThreadsStep - 1) / kThreadsStep;
-    const int b_lo = min(tid * per, A.B), b_hi = min(b_lo + per, A.B);
-    int my_cost = 0, my_units = 0;
-    for (int b = b_lo; b < b_hi; ++b) {
-        const Req r = load_req(A, b);
-        my_units += r.blocks * A.Hkv;
-        my_cost += r.blocks * A.Hkv * (r.nt + U);
-    }
-    int cost = my_cost, units = my_units;
+    const int U = A.unit_cost, me = blockIdx.x;
+    auto cost_of = [&](const Req &r) { return r.blocks * A.Hkv * (r.nt + U); };
+    Cuts cuts;
+    int start, end, tiles, t, start_b, start_unit;
+    Req start_req;
+    if (A.B <= kWarpScan) {
+        // Few requests: every warp finds out by itself, a lane for each
+        // kWarpScan / 32 of them.
+        constexpr int kEach = kWarpScan / 32;
+        Req r[kEach];
+        int my_cost = 0, my_units = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, cost, o), y = __shfl_up_sync(0xffffffffu, units, o);
-        if (lane >= o) {
-            cost += x;
-            units += y;
+        for (int k = 0; k < kEach; ++k) {
+            const int b = lane * kEach + k;
+            if (b < A.B) r[k] = load_req(A, b);
+            else r[k] = Req{};
+            my_cost += cost_of(r[k]);
+            my_units += r[k].blocks * A.Hkv;
         }
-    }
-    if (lane == 31) {
-        C.warp_cost[warp] = cost;
-        C.warp_units[warp] = units;
-    }
-    __syncthreads();
-    cost -= my_cost;
-    units -= my_units;
-    int total = 0, all_units = 0;
-    for (int w = 0; w < kThreadsStep / 32; ++w) {
-        if (w < warp) {
-            cost += C.warp_cost[w];
-            units += C.warp_units[w];
+        int cost = my_cost, units = my_units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, cost, o), y = __shfl_up_sync(0xffffffffu, units, o);
+            if (lane >= o) {
+                cost += x;
+                units += y;
+            }
         }
-        total += C.warp_cost[w];
-        all_units += C.warp_units[w];
-    }
-    const Cuts cuts(total, gridDim.x);
-    const int me = blockIdx.x;
-    const int start = cuts.start(me), end = cuts.start(me + 1);
-    // the threads whose requests hold `start` and `end` say where
-    for (int side = 0; side < 2; ++side) {
-        const int x = side ? end : start;
-        if (x < cost || x >= cost + my_cost) continue;
-        int at = cost, first_unit = units;
+        const int total = __shfl_sync(0xffffffffu, cost, 31), all_units = __shfl_sync(0xffffffffu, units, 31);
+        cuts = Cuts(total, gridDim.x);
+        start = cuts.start(me);
+        end = cuts.start(me + 1);
+        int before[2] = {0, total - U * all_units};
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            const int x = side ? end : start;
+            const uint32_t who = __ballot_sync(0xffffffffu, x >= cost - my_cost && x < cost);
+            if (!who) continue;  // the list's end
+            const int src = __ffs(who) - 1;
+            int at = cost - my_cost, first_unit = units - my_units, k = 0;
+#pragma unroll
+            for (int j = 0; j < kEach - 1; ++j) {
+                if (k == j && x >= at + cost_of(r[j])) {
+                    at += cost_of(r[j]);
+                    first_unit += r[j].blocks * A.Hkv;
+                    k = j + 1;
+                }
+            }
+            Req q = r[0];
+#pragma unroll
+            for (int j = 1; j < kEach; ++j)
+                if (k == j) q = r[j];
+            const int i = (x - at) / (q.nt + U), tile = max(x - at - i * (q.nt + U) - U, 0);
+            before[side] = __shfl_sync(0xffffffffu, at - U * first_unit + i * q.nt + tile, src);
+            if (side == 0) {
+                start_b = __shfl_sync(0xffffffffu, lane * kEach + k, src);
+                start_unit = __shfl_sync(0xffffffffu, i, src);
+                t = __shfl_sync(0xffffffffu, tile, src);
+                start_req.row0 = __shfl_sync(0xffffffffu, q.row0, src);
+                start_req.n = __shfl_sync(0xffffffffu, q.n, src);
+                start_req.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
+                start_req.kbeg = __shfl_sync(0xffffffffu, q.kbeg, src);
+                start_req.kend = __shfl_sync(0xffffffffu, q.kend, src);
+                start_req.t0 = __shfl_sync(0xffffffffu, q.t0, src);
+                start_req.nt = __shfl_sync(0xffffffffu, q.nt, src);
+                start_req.blocks = __shfl_sync(0xffffffffu, q.blocks, src);
+                start_req.per = __shfl_sync(0xffffffffu, q.per, src);
+            }
+        }
+        tiles = start < end ? before[1] - before[0] : 0;
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    } else {
+        const int per = (A.B + kThreadsStep - 1) / kThreadsStep;
+        const int b_lo = min(tid * per, A.B), b_hi = min(b_lo + per, A.B);
+        int my_cost = 0, my_units = 0;
         for (int b = b_lo; b < b_hi; ++b) {
             const Req r = load_req(A, b);
-            const int here = r.blocks * A.Hkv * (r.nt + U);
-            if (x < at + here) {
-                const int i = (x - at) / (r.nt + U), tile = max(x - at - i * (r.nt + U) - U, 0);
-                C.tiles_before[side] = at - U * first_unit + i * r.nt + tile;
-                if (side == 0) {
-                    C.start_b = b;
-                    C.start_unit = i;
-                    C.start_tile = tile;
-                }
-                break;
-            }
-            at += here;
-            first_unit += r.blocks * A.Hkv;
+            my_units += r.blocks * A.Hkv;
+            my_cost += cost_of(r);
         }
+        int cost = my_cost, units = my_units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, cost, o), y = __shfl_up_sync(0xffffffffu, units, o);
+            if (lane >= o) {
+                cost += x;
+                units += y;
+            }
+        }
+        if (lane == 31) {
+            C.warp_cost[warp] = cost;
+            C.warp_units[warp] = units;
+        }
+        __syncthreads();
+        cost -= my_cost;
+        units -= my_units;
+        int total = 0, all_units = 0;
+        for (int w = 0; w < kThreadsStep / 32; ++w) {
+            if (w < warp) {
+                cost += C.warp_cost[w];
+                units += C.warp_units[w];
+            }
+            total += C.warp_cost[w];
+            all_units += C.warp_units[w];
+        }
+        cuts = Cuts(total, gridDim.x);
+        start = cuts.start(me);
+        end = cuts.start(me + 1);
+        // the threads whose requests hold `start` and `end` say where
+        for (int side = 0; side < 2; ++side) {
+            const int x = side ? end : start;
+            if (x < cost || x >= cost + my_cost) continue;
+            int at = cost, first_unit = units;
+            for (int b = b_lo; b < b_hi; ++b) {
+                const Req r = load_req(A, b);
+                const int here = cost_of(r);
+                if (x < at + here) {
+                    const int i = (x - at) / (r.nt + U), tile = max(x - at - i * (r.nt + U) - U, 0);
+                    C.tiles_before[side] = at - U * first_unit + i * r.nt + tile;
+                    if (side == 0) {
+                        C.start_b = b;
+                        C.start_unit = i;
+                        C.start_tile = tile;
+                    }
+                    break;
+                }
+                at += here;
+                first_unit += r.blocks * A.Hkv;
+            }
+        }
+        if (tid == 0 && end == total) C.tiles_before[1] = total - U * all_units;
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        tiles = start < end ? C.tiles_before[1] - C.tiles_before[0] : 0;
+        t = C.start_tile;
+        start_b = C.start_b;
+        start_unit = C.start_unit;
+        if (tiles > 0) start_req = load_req(A, start_b);
     }
-    if (tid == 0 && end == total) C.tiles_before[1] = total - U * all_units;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const int tiles = start < end ? C.tiles_before[1] - C.tiles_before[0] : 0;
     const uint32_t tmem = C.tmem;
     volatile int *gave_up = &C.gave_up;
     Unit u;
-    int t = C.start_tile;  // tile in the unit
-    if (tiles > 0) u.start(A, C.start_b, C.start_unit);
+    if (tiles > 0) u.start(A, start_b, start_req, start_unit);  // at its tile t
 
     if (tiles > 0 && warp >= kWarpK && warp < kWarpMma) {
         // ---- producers ----------------------------------------------------------
@@ -911,10 +991,10 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 }
             }
             tc_fence_before();
-            if (split) __threadfence();
             soft_sync();  // ref, poison and O are read before the next unit writes them
             if (tid == 0) {
                 C.poison = 0;
+                if (split) __threadfence();  // all the CTA's writes of the part: they came before the barrier
                 if (split && atomicAdd(&A.arrived[first_cta], 1) == members - 1) {
                     A.arrived[first_cta] = 0;  // as the next call wants it
                     C.join[C.joins++] = Join{u.q.row0 + u.j0, u.h * A.G, u.ncols, slot0, first_cta, members};
@@ -975,8 +1055,7 @@ cudaError_t launch(StepArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStrea
     cudaError_t e = cudaFuncSetAttribute(step_attention_kernel<D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    step_attention_kernel<D><<<ctas, kThreadsStep, smem, s>>>(A, maps[0], maps[1], maps[2]);
-    return cudaGetLastError();
+    return launch_overlapped(step_attention_kernel<D>, ctas, kThreadsStep, smem, s, A, maps[0], maps[1], maps[2]);
 }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }

@@ -276,6 +276,23 @@ __device__ __forceinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity, 
     }
 }
 
+// Host: a launch whose set-up may overlap the end of the kernel before it in
+// the stream; the kernel waits (griddepcontrol.wait) before it touches memory.
+template <typename... P, typename... T>
+cudaError_t launch_overlapped(void (*kernel)(P...), int grid, int block, size_t smem, cudaStream_t s, const T &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Host: cuTensorMapEncodeTiled for bfloat16 with the 128-byte swizzle.
 cudaError_t encode_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
                        const uint64_t *strides_bytes, const uint32_t *box);
