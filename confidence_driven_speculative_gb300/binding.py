@@ -72,6 +72,8 @@ def lib_path() -> str:
 def load():
     """Load libdspark.so (built by ``_build.build()``); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -126,10 +128,15 @@ class DsparkError(RuntimeError):
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        import torch
+    """The stream's handle; None is torch's current stream, asked for without
+    building a Stream object where torch has the call (0.3 us and not 3)."""
+    if stream is not None:
+        return int(stream)
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
         return torch.cuda.current_stream().cuda_stream
-    return int(stream)
+    return raw(torch.cuda.current_device())
 
 
 def _call(name: str, step, stream, check: bool) -> int:
