@@ -324,7 +324,9 @@ __device__ __forceinline__ void join_columns(const StepArgs &A, const Join &J, i
     }
 }
 
-template <int D>
+// kBox: pages go in TMA boxes; else gathered key by key.  (One kernel for
+// both: more code for every warp to fetch, 10 % slower at long caches.)
+template <int D, bool kBox>
 __global__ void __launch_bounds__(kThreadsStep, 1)
 step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
@@ -533,7 +535,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
         // tile ahead; one elected lane issues the copies.
         const int part = warp == kWarpBoth;
         const int kv_lo = warp == kWarpV, kv_hi = warp == kWarpK ? 1 : 2;
-        const int span = A.box ? A.box : 4, boxes = kTile / span, most = (2 * boxes + 2) / 3;
+        const int span = kBox ? A.box : 4, boxes = kTile / span, most = (2 * boxes + 2) / 3;
         const int my_box = part * most + lane;  // this lane's
         const bool my_turn = lane < most && my_box < boxes;
         struct Ids { int page[4]; };
@@ -544,7 +546,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 ids.page[i] = -1;
-                if ((i == 0 || !A.box) && wanted) {
+                if ((i == 0 || !kBox) && wanted) {
                     const int pi = page_of(A, key0 + i);
                     if (pi < A.max_pages) ids.page[i] = table[pi];
                 }
@@ -575,18 +577,18 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 const bool good = ids.page[j] >= 0 && ids.page[j] < A.num_pages;
                 if (!good) bad_bits |= 1u << j;
                 const int page = good ? ids.page[j] : 0;  // masked; any memory will do
-                row[j] = A.box ? page
+                row[j] = kBox ? page
                                : page * A.page_rows + u.h * A.head_rows + key0 + j -
                                      page_of(A, key0 + j) * A.page_size;
             }
-            const bool lane_bad = here && (A.box ? (bad_bits & 1) : bad_bits != 0);
+            const bool lane_bad = here && (kBox ? (bad_bits & 1) : bad_bits != 0);
             uint32_t words[4] = {0, 0, 0, 0};
             if (__any_sync(0xffffffffu, lane_bad)) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t m = 0;
                     if (lane_bad) {
-                        if (A.box) {
+                        if (kBox) {
                             const int lo = max(my_box * span - 32 * q, 0), hi = min(my_box * span + span - 32 * q, 32);
                             if (lo < hi) m = (hi - lo == 32 ? 0xffffffffu : ((1u << (hi - lo)) - 1u)) << lo;
                         } else if (my_box / 8 == q) {
@@ -603,7 +605,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
             int *const rows = C.row[kv_lo];
             __syncwarp();
             if (my_turn) {
-                if (A.box) rows[my_box] = row[0];
+                if (kBox) rows[my_box] = row[0];
                 else *reinterpret_cast<int4 *>(rows + 4 * my_box) = make_int4(row[0], row[1], row[2], row[3]);
             }
 #pragma unroll
@@ -622,7 +624,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                     uint64_t *full = &C.full[slot];
                     mbar_arrive_expect_tx(full, bytes);
                     uint32_t dst = ring + slot * kSlotBytes + box_lo * span * 128;
-                    if (A.box) {
+                    if (kBox) {
                         const int first_key = tile0 + box_lo * span;
                         int in_page = first_key - page_of(A, first_key) * A.page_size;
 #pragma unroll 4
@@ -1029,7 +1031,7 @@ int step_columns(int Hq, int Hkv, int q_max) {
 
 constexpr size_t kHeaderBytes = 256 + (sizeof(int32_t) * kAttnMaxCtas + 255) / 256 * 256;
 
-template <int D>
+template <int D, bool kBox>
 cudaError_t launch(StepArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStream_t s) {
     // What is held twice, against ring slots.  A tile of V waits for its
     // tile's softmax, so three V slots carry more than a second P or Q; Q is
@@ -1052,10 +1054,10 @@ cudaError_t launch(StepArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStrea
     A.slots = int(std::min<size_t>((room - fixed) / slot, kMaxSlots));
     A.k_slots = A.slots / 2;
     const size_t smem = 2048 + fixed + A.slots * slot;
-    cudaError_t e = cudaFuncSetAttribute(step_attention_kernel<D>,
+    cudaError_t e = cudaFuncSetAttribute(step_attention_kernel<D, kBox>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    return launch_overlapped(step_attention_kernel<D>, ctas, kThreadsStep, smem, s, A, maps[0], maps[1], maps[2]);
+    return launch_overlapped(step_attention_kernel<D, kBox>, ctas, kThreadsStep, smem, s, A, maps[0], maps[1], maps[2]);
 }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -1156,7 +1158,8 @@ cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_n
         }
     }
     const int ctas = std::min(sms, kAttnMaxCtas);
-    return a.D == 128 ? launch<128>(A, maps, ctas, s) : launch<64>(A, maps, ctas, s);
+    if (A.box) return a.D == 128 ? launch<128, true>(A, maps, ctas, s) : launch<64, true>(A, maps, ctas, s);
+    return a.D == 128 ? launch<128, false>(A, maps, ctas, s) : launch<64, false>(A, maps, ctas, s);
 }
 
 }  // namespace dspark
