@@ -57,18 +57,20 @@ struct Unit {
 
 // Tiles of keys that block a (rows q .. q + 127) of a unit walks.
 struct Span { int lo, hi; };
+template <bool kWindow>
 __device__ __forceinline__ Span span_of(const PromptArgs &A, const Unit &u, int a) {
     const int q = u.q0 + a * kTile;
     if (q >= u.n) return {0, 0};
     Span s;
-    s.lo = A.window > 0 ? max(q - A.window + 1, 0) / kTile : 0;
+    s.lo = kWindow ? max(q - A.window + 1, 0) / kTile : 0;
     s.hi = (min(q + kTile, u.n) + kTile - 1) / kTile;
     return s;
 }
 // Does some row of block a not see some key of tile t?
+template <bool kWindow>
 __device__ __forceinline__ bool partial(const PromptArgs &A, const Unit &u, int a, int t) {
     const int q = u.q0 + a * kTile;
-    return (t + 1) * kTile - 1 > q || (A.window > 0 && t * kTile <= min(q + kTile, u.n) - 1 - A.window);
+    return (t + 1) * kTile - 1 > q || (kWindow && t * kTile <= min(q + kTile, u.n) - 1 - A.window);
 }
 
 struct Ctrl {
@@ -112,7 +114,9 @@ struct SchedReader {
     }
 };
 
-template <int D>
+// kWindow: is there one?  Code that an unwindowed call does not run is code that
+// its warps need not fetch past.
+template <int D, bool kWindow>
 __global__ void __launch_bounds__(kThreadsP, 1)
 prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_constant__ CUtensorMap q_map,
                         const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
@@ -239,7 +243,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
             const Unit u = ahead;
             ahead = claim();
             if (!ok) break;
-            const Span s0 = span_of(A, u, 0), s1 = span_of(A, u, 1);
+            const Span s0 = span_of<kWindow>(A, u, 0), s1 = span_of<kWindow>(A, u, 1);
             const int t_lo = s0.lo, t_hi = max(s0.hi, s1.hi), kvh = u.h / A.G;
             for (int a = 0; a < 2 && ok; ++a) {
                 if (a == 1 && s1.hi == 0) break;
@@ -314,7 +318,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
             const Unit u = sched.next(C, A, gave_up, lane);
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
-                w.sp[a] = u.h < 0 ? Span{0, 0} : span_of(A, u, a);
+                w.sp[a] = u.h < 0 ? Span{0, 0} : span_of<kWindow>(A, u, a);
                 w.sp[a].lo = __shfl_sync(0xffffffffu, w.sp[a].lo, 0);
                 w.sp[a].hi = __shfl_sync(0xffffffffu, w.sp[a].hi, 0);
             }
@@ -438,7 +442,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
         bool ok = true;
         Unit u = sched.next(C, A, gave_up, lane);
         while (ok && u.h >= 0) {
-            const Span sp[2] = {span_of(A, u, 0), span_of(A, u, 1)};
+            const Span sp[2] = {span_of<kWindow>(A, u, 0), span_of<kWindow>(A, u, 1)};
             const int t_hi = max(sp[0].hi, sp[1].hi);
             Unit nx = u;
             for (int t = sp[0].lo; t < t_hi && ok; ++t) {
@@ -497,7 +501,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
         for (int unit = 0;; ++unit) {
             const Unit u = sched.next(C, A, gave_up, lane);
             if (pair_any(u.h < 0)) break;
-            const Span sp = span_of(A, u, a), other = span_of(A, u, a ^ 1);
+            const Span sp = span_of<kWindow>(A, u, a), other = span_of<kWindow>(A, u, a ^ 1);
             const int t_lo = a ? other.lo : sp.lo, t_hi = max(sp.hi, other.hi);
             for (int t = t_lo; t < (sp.hi == 0 ? t_hi : sp.lo); ++t) rv.next(v_slots);
             if (sp.hi == 0) continue;
@@ -517,11 +521,11 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 32) tmem_use32(s + c);
-                const bool cut = partial(A, u, a, t);
+                const bool cut = partial<kWindow>(A, u, a, t);
                 if (cut) {
                     // The row sees keys (lo, hi] of the half tile.  By 32 keys,
                     // what the warp's rows all see stays as it is.
-                    const int hi = q - t * kTile - half * kKeys, lo = A.window > 0 ? hi - A.window : -1;
+                    const int hi = q - t * kTile - half * kKeys, lo = kWindow ? hi - A.window : -1;
                     const int hi0 = hi - lane, lo31 = lo + 31 - lane;  // its first row's, its last row's
 #pragma unroll
                     for (int c = 0; c < kKeys; c += 32) {
@@ -530,7 +534,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                             for (int e = 0; e < 32; ++e)
                                 if (c + e > hi) s[c + e] = -INFINITY;
                         }
-                        if (A.window > 0 && c <= lo31) {
+                        if (kWindow && c <= lo31) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 if (c + e <= lo) s[c + e] = -INFINITY;
@@ -545,7 +549,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                 }
                 const float m = max3(m0, m1, fmaxf(s[kKeys - 2], s[kKeys - 1])) * A.scale2;
                 const bool first = t == sp.lo;
-                if (pair_any(first || m > ref + kRefSlack)) {
+                if (__builtin_expect(pair_any(first || m > ref + kRefSlack), 0)) {
                     const float now = fmaxf(fmaxf(m, exchange(0, m)), kRefMin);
                     if (first) {
                         ref = now;
@@ -554,7 +558,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                         ref = to;
                         l2.x *= f;
                         l2.y *= f;
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < kEntries; c += 16) {
                             float o[16];
                             tmem_ld16(o, o_tm + c);
@@ -591,18 +595,19 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                     wait_or_give_up(&C.full[A.k_slots + rv.slot], rv.phase, A.wait_ns, gave_up);
                     __syncwarp();
                     const uint32_t at0 = v_ring + rv.slot * kSlotBytes + (half * kTile + row) * 16;
-                    bool lost = false;
+                    bool odd = false;
 #pragma unroll
-                    for (uint32_t c = 0; c < kSlotBytes; c += 2 * kTile * 16) {
-                        const uint4 x = ld_shared16(at0 + c);
-                        if (nonfinite_any(x)) {
+                    for (uint32_t c = 0; c < kSlotBytes; c += 2 * kTile * 16) odd |= nonfinite_any(ld_shared16(at0 + c));
+                    if (__builtin_expect(odd, 0)) {
+#pragma unroll 1
+                        for (uint32_t c = 0; c < kSlotBytes; c += 2 * kTile * 16) {
+                            const uint4 x = ld_shared16(at0 + c);
                             st_shared16(at0 + c, x.x & ~nonfinite_mask(x.x), x.y & ~nonfinite_mask(x.y),
                                         x.z & ~nonfinite_mask(x.z), x.w & ~nonfinite_mask(x.w));
-                            lost = true;
                         }
+                        C.poisoned[unit % 8] = unit + 1;
+                        fence_async_shared();
                     }
-                    if (lost) C.poisoned[unit % 8] = unit + 1;
-                    fence_async_shared();
                 }
                 rv.next(v_slots);
                 tmem_wait_st();
@@ -617,13 +622,12 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
             ++o_uses;
             tc_fence_after();
             uint16_t *const out = A.out + ((int64_t)(u.row0 + q) * A.Hq + u.h) * D + half * kEntries;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kEntries; c += 32) {
                 float o[32];
                 tmem_ld32(o, o_tm + c);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                 tmem_use32(o);
-                if (c + 32 == kEntries) tc_fence_before();
                 if (q < u.n) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 16) {
@@ -634,13 +638,15 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                     }
                 }
             }
-            if (C.poisoned[unit % 8] == unit + 1 && q < u.n) {
+            tc_fence_before();
+            if (__builtin_expect(C.poisoned[unit % 8] == unit + 1, 0) && q < u.n) {
                 // what was taken out of the values that this row sees
                 for (int t = sp.lo; t < sp.hi; ++t) {
-                    if (!partial(A, u, a, t) && !(t >= other.lo && t < other.hi && partial(A, u, a ^ 1, t))) continue;
+                    if (!partial<kWindow>(A, u, a, t) && !(t >= other.lo && t < other.hi && partial<kWindow>(A, u, a ^ 1, t))) continue;
                     for (int k = t * kTile; k < min((t + 1) * kTile, q + 1); ++k) {
-                        if (A.window > 0 && k <= q - A.window) continue;
+                        if (kWindow && k <= q - A.window) continue;
                         const uint16_t *v = A.v + (int64_t)(u.row0 + k) * A.v_stride + (u.h / A.G) * D + half * kEntries;
+#pragma unroll 1
                         for (int d = 0; d < kEntries; ++d) {
                             const float x = bf16_lo(v[d]);
                             if (!isfinite(x)) out[d] = uint16_t(pack_bf16x2(bf16_lo(out[d]) + x, 0.f));
@@ -657,16 +663,16 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
     if (warp == kWarpMma) tmem_free(tmem, 512);
 }
 
-template <int D>
+template <int D, bool kWindow>
 cudaError_t launch(PromptArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStream_t s) {
     const size_t slot = size_t(D) * 2 * kTile;
     A.slots = int(std::min<size_t>((kSmemBytes - sizeof(Ctrl) - 1024 - 2 * slot) / slot, kSlotsMax));
     A.k_slots = A.slots / 2;
     const size_t smem = 1024 + (2 + A.slots) * slot;
-    const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D>,
+    const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D, kWindow>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    return launch_overlapped(prompt_attention_kernel<D>, ctas, kThreadsP, smem, s, A, maps[0], maps[1], maps[2]);
+    return launch_overlapped(prompt_attention_kernel<D, kWindow>, ctas, kThreadsP, smem, s, A, maps[0], maps[1], maps[2]);
 }
 
 }  // namespace
@@ -696,7 +702,9 @@ cudaError_t launch_prompt_attention(const dspark_attn &a, int sms, uint64_t wait
         if (e != cudaSuccess) return e;
     }
     const int ctas = std::min(sms, kAttnMaxCtas);
-    return a.D == 128 ? launch<128>(A, maps, ctas, s) : launch<64>(A, maps, ctas, s);
+    if (a.window > 0)
+        return a.D == 128 ? launch<128, true>(A, maps, ctas, s) : launch<64, true>(A, maps, ctas, s);
+    return a.D == 128 ? launch<128, false>(A, maps, ctas, s) : launch<64, false>(A, maps, ctas, s);
 }
 
 }  // namespace dspark
