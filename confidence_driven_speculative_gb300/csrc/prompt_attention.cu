@@ -281,13 +281,14 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
         }
         if (C.gave_up) {
             // Let the copies in flight land before the CTA ends.
+            bool landed = true;
             for (int kv = 0; kv < 2; ++kv) {
                 const int slots = kv ? v_slots : A.k_slots;
-                for (int k = max(issued[kv] - slots, 0); k < issued[kv]; ++k)
-                    mbar_wait_bounded(&C.full[(kv ? A.k_slots : 0) + k % slots], (k / slots) & 1, kDrainTimeoutNs);
+                for (int k = max(issued[kv] - slots, 0); landed && k < issued[kv]; ++k)
+                    landed = mbar_wait_bounded(&C.full[(kv ? A.k_slots : 0) + k % slots], (k / slots) & 1, kDrainTimeoutNs);
             }
             for (int a = 0; a < 2; ++a)
-                if (q_uses[a]) mbar_wait_bounded(&C.q_full[a], (q_uses[a] - 1) & 1, kDrainTimeoutNs);
+                if (landed && q_uses[a]) landed = mbar_wait_bounded(&C.q_full[a], (q_uses[a] - 1) & 1, kDrainTimeoutNs);
         }
         if (lane == 0) {
             // The last CTA leaves the counter as the next call wants it.

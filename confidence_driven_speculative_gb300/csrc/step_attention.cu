@@ -678,13 +678,15 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
         }
         if (C.gave_up) {
             // Let the copies in flight land before the CTA ends: this warp's
-            // latest copy to each slot, and the queries'.
+            // latest copy to each slot, and the queries'.  A phase that another
+            // warp leaves open ends the wait at its limit; by then all has landed.
+            bool landed = true;
             for (int kv = 0; kv < 2; ++kv)
-                for (int k = max(issued[kv] - ring_slots[kv], 0); k < issued[kv]; ++k)
-                    mbar_wait_bounded(&C.full[ring_slot0[kv] + k % ring_slots[kv]], (k / ring_slots[kv]) & 1,
-                                      kDrainTimeoutNs);
-            for (int k = max(units - 1 - A.two_q, 0); k < units; ++k)
-                mbar_wait_bounded(&C.q_full[A.two_q ? k & 1 : 0], (A.two_q ? k >> 1 : k) & 1, kDrainTimeoutNs);
+                for (int k = max(issued[kv] - ring_slots[kv], 0); landed && k < issued[kv]; ++k)
+                    landed = mbar_wait_bounded(&C.full[ring_slot0[kv] + k % ring_slots[kv]], (k / ring_slots[kv]) & 1,
+                                               kDrainTimeoutNs);
+            for (int k = max(units - 1 - A.two_q, 0); landed && k < units; ++k)
+                landed = mbar_wait_bounded(&C.q_full[A.two_q ? k & 1 : 0], (A.two_q ? k >> 1 : k) & 1, kDrainTimeoutNs);
         }
     } else if (tiles > 0 && warp == kWarpMma) {
         // ---- MMA issuer: S of the next tile and O, L of this one, whichever's

@@ -264,7 +264,7 @@ __device__ __forceinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity, 
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 31u) != 0) continue;
+        if ((it & 7u) != 0) continue;
         if (*gave_up) return false;
         const uint64_t now = global_timer_ns();
         if (t0 == 0) {

@@ -145,3 +145,26 @@ def test_same_bits_every_time_on_any_stream_and_in_a_graph(cuda_lib):
         g.replay()
         torch.cuda.synchronize()
         assert np.array_equal(wide(c.h.out), first)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_an_output_on_a_16_byte_border(cuda_lib, D):
+    c = Case(11, [300, 31], Hq=4, Hkv=2, D=D)
+    want = c.call()
+    room = torch.full((c.rows * 4 * D + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.h.attn.out = room.data_ptr() + 16
+    binding.dspark_prompt_attention(c.h.attn)
+    torch.cuda.synchronize()
+    assert c.h.device_status() == 0
+    got = wide(room)
+    assert np.all(got[:8] == 7.0) and np.array_equal(got[8:].reshape(want.shape), want)
+
+
+@pytest.mark.parametrize("grow", [200.0, 900.0])
+def test_scores_far_past_the_first_tiles(cuda_lib, grow):
+    """Later keys are longer by far: scores rise past the first tile's by more than the weights'
+    slack, and by more than fp32's exponent holds."""
+    c = Case(12, [700], Hq=4, Hkv=2, D=128)
+    at = torch.arange(c.rows, device="cuda")[:, None, None]
+    c.k.copy_((c.k.float() * (1.0 + grow / 30.0 * (at // 128))).to(torch.bfloat16))
+    c.check(pick=edges)

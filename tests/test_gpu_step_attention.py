@@ -281,3 +281,40 @@ def test_append_then_attend_is_the_attention_of_the_whole_sequence(cuda_lib):
             assert_close(got[r0:r1], o, spread, ds, ctx[b] + n[b])
         ctx = [c + m for c, m in zip(ctx, n)]
     assert bits(kc).any()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 6, 8, 10, 12, 14, 16, 18, 20, 23])
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_width_of_a_block(cuda_lib, rows, D):
+    """8 to 184 columns of one cached head: each way of holding S, P and the queries once or twice,
+    and the division into blocks."""
+    Case(15, ctx=[333, 1000 - rows, 5], n=[rows, rows, max(rows - 3, 1)], Hq=8, Hkv=1, D=D, page=16).check()
+
+
+def test_one_cached_head_for_128_query_heads(cuda_lib):
+    Case(16, ctx=[150, 40], n=[3, 2], Hq=128, Hkv=1, D=128, page=16).check()
+
+
+@pytest.mark.parametrize("page", [1, 16])
+def test_many_requests_of_very_different_lengths(cuda_lib, page):
+    """More requests than one warp looks at, a few of them long: units cut over many CTAs between
+    short ones."""
+    ctx = [(7 * i) % 40 for i in range(300)]
+    ctx[3], ctx[150], ctx[299] = 3000, 1700, 2222
+    Case(17, ctx=ctx, n=[1 + i % 3 for i in range(300)], Hq=4, Hkv=2, D=64, page=page).check()
+
+
+@pytest.mark.parametrize("page", [1, 3, 16])
+@pytest.mark.parametrize("heads_first", [False, True])
+def test_keys_and_values_in_one_tensor(cuda_lib, page, heads_first):
+    """The caches are two views of one [pages, 2, ...] tensor: pages further apart than they are
+    long."""
+    c = Case(18, ctx=[140, 9], n=[4, 2], Hq=8, Hkv=2, D=128, page=page)
+    shape = (c.num_pages, 2, 2, page, 128) if heads_first else (c.num_pages, 2, page, 2, 128)
+    both = torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    k, v = (both[:, i].transpose(1, 2) if heads_first else both[:, i] for i in (0, 1))
+    k.copy_(c.kc)
+    v.copy_(c.vc)
+    c.kc, c.vc = k, v
+    c.bind()
+    c.check()
