@@ -821,13 +821,14 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 const uint32_t p_row = p_smem + pb * p_bytes + key * 32;
                 if (i > A.two_p)  // P's last reader
                     wait_or_give_up(&C.pv_done[pb], ((A.two_p ? i >> 1 : i) - 1) & 1, A.wait_ns, gave_up);
-                if (!whole && (lo > 0 || hi < u.ncols)) {
+                if (__builtin_expect(!whole, 0) && (lo > 0 || hi < u.ncols)) {
                     // Masked keys must not reach O through 0 * infinity: a
                     // value row that no column sees is cleared, and one that
                     // some see loses its NaN and infinities, which are added
                     // at the unit's end to the columns that do see them.
                     wait_or_give_up(&C.full[A.k_slots + rv.slot], rv.phase, A.wait_ns, gave_up);
                     const uint32_t vb = ring + (A.k_slots + rv.slot) * kSlotBytes + key * 128;
+#pragma unroll 1
                     for (int ch = grp; ch < 8 * kHalves; ch += kGroups) {
                         const uint32_t at = vb + (ch / 8) * kHalfBytes + (((ch % 8) ^ swz) << 4);
                         if (lo >= hi) {
@@ -835,10 +836,9 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                             continue;
                         }
                         const uint4 x = ld_shared16(at);
-                        const uint32_t mx = nonfinite_mask(x.x), my = nonfinite_mask(x.y),
-                                       mz = nonfinite_mask(x.z), mw = nonfinite_mask(x.w);
-                        if (mx | my | mz | mw) {
-                            st_shared16(at, x.x & ~mx, x.y & ~my, x.z & ~mz, x.w & ~mw);
+                        if (__builtin_expect(nonfinite_any(x), 0)) {
+                            st_shared16(at, x.x & ~nonfinite_mask(x.x), x.y & ~nonfinite_mask(x.y),
+                                        x.z & ~nonfinite_mask(x.z), x.w & ~nonfinite_mask(x.w));
                             C.poison = 1;
                         }
                     }
@@ -850,7 +850,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 // tile sets the reference before, a tile that passes it by
                 // too much moves it and starts again (once: then none does).
                 for (int turn = 0; turn < 2; ++turn) {
-                    if (move) {
+                    if (__builtin_expect(move, 0)) {
                         if (!first && A.two_p)
                             wait_or_give_up(&C.pv_done[pb ^ 1], ((i - 1) >> 1) & 1, A.wait_ns, gave_up);
                         tc_fence_after();
@@ -910,7 +910,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                     fence_async_shared();
                     tc_fence_before();
                     move = soft_any(top > kRefSlack);
-                    if (!move) break;
+                    if (__builtin_expect(!move, 1)) break;
                 }
                 if (tid == 0) mbar_arrive(&C.p_full[pb]);
             }
@@ -970,11 +970,12 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 }
             }
             if (C.poison) soft_sync();  // the other group's outputs are written
-            if (C.poison && writer && grp == 0) {
+            if (__builtin_expect(C.poison, 0) && writer && grp == 0) {
                 // What was taken out of V: for the keys of this CTA's
                 // tiles that some columns see and others do not.
                 const int k0 = max((u.q.t0 + t_first) * kTile, u.q.kbeg);
                 const int k1 = min((u.q.t0 + t) * kTile, u.q.kend);
+#pragma unroll 1
                 for (int k = k0; k < k1; ++k) {
                     int vlo, vhi;
                     visible_columns(A, u, k, false, vlo, vhi);
@@ -984,6 +985,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                     const float v = bf16_lo(A.v_cache[page * A.page_stride + (k % A.page_size) * A.slot_stride +
                                                       u.h * A.head_stride + d]);
                     if (isfinite(v)) continue;
+#pragma unroll 1
                     for (int n = vlo; n < vhi; ++n) {
                         if (split) {
                             part0[(int64_t)n * D] += v;
