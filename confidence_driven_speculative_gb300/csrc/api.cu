@@ -724,7 +724,7 @@ dspark_status dspark_rope_append(const dspark_attn *a, dspark_stream_t stream) {
     }
     DeviceInfo *dev;
     if ((st = device_info(&dev))) return st;
-    cudaError_t e = dspark::launch_rope_append(*a, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e = dspark::launch_rope_append(*a, dev->sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rope_append_kernel launch");
     return DSPARK_OK;
 }

@@ -20,7 +20,7 @@ bool step_strides_ok(const dspark_attn &a);
 // Is the list of a step's tiles counted in 32 bits?
 bool step_list_fits(const dspark_attn &a);
 
-cudaError_t launch_rope_append(const dspark_attn &a, cudaStream_t s);
+cudaError_t launch_rope_append(const dspark_attn &a, int sms, cudaStream_t s);
 cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_ns, cudaStream_t s);
 cudaError_t launch_prompt_attention(const dspark_attn &a, int sms, uint64_t wait_ns, cudaStream_t s);
 

@@ -8,10 +8,15 @@
 // for sincospif.  The rotation is fp32, rounded once to bfloat16.
 //
 // Bound: bytes.  A row of Hq + 2 Hkv heads is read once and written once.
-// One CTA of 128 threads takes one row.  A thread keeps one pair of 16-byte
-// chunks (8 rotation pairs) of a head and walks the heads with it, so its 8
-// sines and cosines are computed once per row, and the loads of up to four
-// heads are in flight before the angles are needed.
+// A CTA of 128 threads takes a row.  A thread keeps one pair of 16-byte chunks
+// (8 rotation pairs) of a head and walks the heads with it, so its 8 sines and
+// cosines are computed once per row, and the loads of up to four heads are in
+// flight before the angles are needed.
+//
+// Bound by memory: each row's heads are read and written once.  Hq = 32,
+// Hkv = 8, D = 128, k_rot too, 20 425 rows of 32 768 slots: 84.8 us = 6.4 TB/s, 95 % of the
+// rate of a copy.  One request's 17 rows: 3.8 us a call, which is the host's
+// part and the launch.
 #include "attn.cuh"
 #include "dspark_internal.cuh"
 #include "tcgen05.cuh"
@@ -61,14 +66,9 @@ __device__ __forceinline__ void rotate(uint4 &a, uint4 &b, const float (&c)[8], 
 }
 
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs A) {
+__device__ __forceinline__ void append_row(const RopeArgs &A, int r, int b, int pos) {
     constexpr int kLanes = D / 16;  // threads of a head, two 16-byte chunks each
     constexpr int kHeads = kRopeThreads / kLanes;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int r = blockIdx.x;
-    const int b = A.row_req[r];
-    const int pos = A.packed_pos[r];
     if (b < 0 || b >= A.B || pos < 0) return;
     const int c = threadIdx.x % kLanes;
     // The thread's two chunks of a head (element offsets) and its first
@@ -131,9 +131,38 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
     }
 }
 
+// A CTA for each row slot.
+template <int D, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs A) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    append_row<D, kInterleaved>(A, blockIdx.x, A.row_req[blockIdx.x], A.packed_pos[blockIdx.x]);
+}
+
+// The CTAs walk the row slots; the next one's place is asked for before this
+// one's work.
+template <int D, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_walk_kernel(const RopeArgs A) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int b = A.row_req[blockIdx.x], pos = A.packed_pos[blockIdx.x];
+    for (int r = blockIdx.x; r < A.rows;) {
+        const int next = r + gridDim.x;
+        int b_next = -1, pos_next = -1;
+        if (next < A.rows) {
+            b_next = A.row_req[next];
+            pos_next = A.packed_pos[next];
+        }
+        append_row<D, kInterleaved>(A, r, b, pos);
+        r = next;
+        b = b_next;
+        pos = pos_next;
+    }
+}
+
 }  // namespace
 
-cudaError_t launch_rope_append(const dspark_attn &a, cudaStream_t s) {
+cudaError_t launch_rope_append(const dspark_attn &a, int sms, cudaStream_t s) {
     RopeArgs A{a.B, a.rows, a.Hq, a.Hkv, a.page_size, a.num_pages, a.max_pages, a.rot_dim,
                a.q_stride, a.k_stride, a.v_stride, a.page_stride, a.slot_stride, a.head_stride,
                static_cast<const uint16_t *>(a.q), static_cast<const uint16_t *>(a.k),
@@ -142,9 +171,20 @@ cudaError_t launch_rope_append(const dspark_attn &a, cudaStream_t s) {
                static_cast<uint16_t *>(a.v_cache), a.row_req, a.packed_pos, a.block_table,
                a.rope_freq};
     if (!a.k) A.page_size = 1;  // not checked, not used
-    auto *kernel = a.D == 128 ? (a.interleaved ? rope_append_kernel<128, true> : rope_append_kernel<128, false>)
-                              : (a.interleaved ? rope_append_kernel<64, true> : rope_append_kernel<64, false>);
-    return launch_overlapped(kernel, a.rows, kRopeThreads, 0, s, A);
+    // Walking pays where most slots are padding, as in a batch of steps: a CTA
+    // that finds an empty slot costs a launch, a walker a load that is already
+    // under way.  4352 slots with 1024 rows: 7.6 us with a CTA a slot, 6.4
+    // with 14 walkers an SM.  Where the slots are full it costs a little
+    // (4096 rows: 20.6 us against 21.5; 8192: 36.7 against 37.4), and more the
+    // longer the walk (32768: 134 against 150), so long lists keep a CTA a slot.
+    const int walkers = 14 * sms;
+    const bool walk = a.rows > walkers && a.rows <= 4 * walkers;
+    auto *kernel =
+        walk ? (a.D == 128 ? (a.interleaved ? rope_append_walk_kernel<128, true> : rope_append_walk_kernel<128, false>)
+                           : (a.interleaved ? rope_append_walk_kernel<64, true> : rope_append_walk_kernel<64, false>))
+             : (a.D == 128 ? (a.interleaved ? rope_append_kernel<128, true> : rope_append_kernel<128, false>)
+                           : (a.interleaved ? rope_append_kernel<64, true> : rope_append_kernel<64, false>));
+    return launch_overlapped(kernel, walk ? walkers : a.rows, kRopeThreads, 0, s, A);
 }
 
 }  // namespace dspark
