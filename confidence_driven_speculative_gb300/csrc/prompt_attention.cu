@@ -7,15 +7,30 @@
 // maximum passes the reference by 2^32 (the weights stay in the range of fp32
 // and bfloat16 keeps its relative step), which is next to never.
 //
+// The weights are rounded to bfloat16 for the tensor core, by a relative 2^-8
+// at most; l sums them unrounded, in registers.
+//
 // Bound: the tensor cores.  A unit is 256 rows of one head in two blocks of
 // 128, walked over tiles of 128 keys.  S and O of both blocks fill TMEM
 // (4 x 128 columns); P overwrites its S in TMEM and is the A operand of
 // P V.  While one block's softmax runs, the tensor cores work on the other
-// block: O_0 += P_0 V, S_0 of the next tile, O_1 += P_1 V, S_1 of the next tile.
-// A softmax thread owns a row, so maxima and sums stay in its registers.
+// block: O_0 += P_0 V with S_0 of the next tile, then O_1 += P_1 V with S_1.
+// Two threads share a row, 64 keys each: one thread a row had twice the chain
+// of exponentials between two products (359 us against 346 for the long
+// prompts below).
 //
 // Units are handed out by a counter, the longest of a prompt first, so the
 // CTAs end together; a unit's result does not depend on who computes it.
+//
+// Measured, D = 128: one prompt of 8192 rows and 32 heads 316 us at full
+// clocks, 1.74 PFLOP/s where a library product reaches 1.91 (the power limit
+// can take it to 350); 24 prompts of 20 to 2000 rows and 40 heads 228 us, 113
+// at that rate.  A step (both blocks' products, 2048 clocks) takes about 2900:
+// a block's chain is 1024 clocks of its own products, 220 until the softmax
+// sees them, 450 for loads and maxima, 240 for the halves' vote, 700 for the
+// weights, 150 back, and TMEM has no room for a second S.  A unit's border
+// costs some 4000 clocks more (last product, outputs, diagonal masks), and
+// short prompts have few steps to a unit.
 #include <algorithm>
 
 #include "attn.cuh"
@@ -512,6 +527,31 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
             // Once a wait has given up, the others return at once and the
             // loops run to their ends on whatever there is; the status tells.
             for (int t = sp.lo; t < sp.hi; ++t) {
+                const bool cut = partial<kWindow>(A, u, a, t);
+                if (cut) {
+                    // Masked keys must not reach O through 0 * infinity: a value
+                    // tile that some row does not see in full loses its NaN and
+                    // infinities; the rows that see them get them back at the
+                    // unit's end.  (The other block may read the tile before or
+                    // after: what it then gets back it already has, or lacks.)
+                    // The tile's scores are still being made.
+                    wait_or_give_up(&C.full[A.k_slots + rv.slot], rv.phase, A.wait_ns, gave_up);
+                    __syncwarp();
+                    const uint32_t at0 = v_ring + rv.slot * kSlotBytes + (half * kTile + row) * 16;
+                    bool odd = false;
+#pragma unroll
+                    for (uint32_t c = 0; c < kSlotBytes; c += 2 * kTile * 16) odd |= nonfinite_any(ld_shared16(at0 + c));
+                    if (__builtin_expect(odd, 0)) {
+#pragma unroll 1
+                        for (uint32_t c = 0; c < kSlotBytes; c += 2 * kTile * 16) {
+                            const uint4 x = ld_shared16(at0 + c);
+                            st_shared16(at0 + c, x.x & ~nonfinite_mask(x.x), x.y & ~nonfinite_mask(x.y),
+                                        x.z & ~nonfinite_mask(x.z), x.w & ~nonfinite_mask(x.w));
+                        }
+                        C.poisoned[unit % 8] = unit + 1;
+                        fence_async_shared();
+                    }
+                }
                 wait_or_give_up(&C.s_full[a], s_uses & 1, A.wait_ns, gave_up);
                 __syncwarp();
                 ++s_uses;
@@ -522,24 +562,17 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 32) tmem_use32(s + c);
-                const bool cut = partial<kWindow>(A, u, a, t);
                 if (cut) {
-                    // The row sees keys (lo, hi] of the half tile.  By 32 keys,
-                    // what the warp's rows all see stays as it is.
+                    // The row sees keys (lo, hi] of the half tile.
                     const int hi = q - t * kTile - half * kKeys, lo = kWindow ? hi - A.window : -1;
-                    const int hi0 = hi - lane, lo31 = lo + 31 - lane;  // its first row's, its last row's
 #pragma unroll
                     for (int c = 0; c < kKeys; c += 32) {
-                        if (c + 31 > hi0) {
+                        uint32_t seen = hi < c ? 0u : 0xffffffffu >> max(31 + c - hi, 0);
+                        if (kWindow) seen &= lo < c ? 0xffffffffu : lo >= c + 31 ? 0u : 0xfffffffeu << (lo - c);
+                        if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (c + e > hi) s[c + e] = -INFINITY;
-                        }
-                        if (kWindow && c <= lo31) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (c + e <= lo) s[c + e] = -INFINITY;
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!(seen >> e & 1)) s[c + e] = -INFINITY;
                     }
                 }
                 float m0 = max3(s[0], s[1], s[2]), m1 = max3(s[3], s[4], s[5]);
@@ -586,29 +619,6 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                         p[e / 2] = pack_bf16x2(x.x, x.y);
                     }
                     tmem_st16u(s_tm + (half * kKeys + c) / 2, p);
-                }
-                if (cut) {
-                    // Masked keys must not reach O through 0 * infinity: a value
-                    // tile that some row does not see in full loses its NaN and
-                    // infinities; the rows that see them get them back at the
-                    // unit's end.  (The other block may read the tile before or
-                    // after: what it then gets back it already has, or lacks.)
-                    wait_or_give_up(&C.full[A.k_slots + rv.slot], rv.phase, A.wait_ns, gave_up);
-                    __syncwarp();
-                    const uint32_t at0 = v_ring + rv.slot * kSlotBytes + (half * kTile + row) * 16;
-                    bool odd = false;
-#pragma unroll
-                    for (uint32_t c = 0; c < kSlotBytes; c += 2 * kTile * 16) odd |= nonfinite_any(ld_shared16(at0 + c));
-                    if (__builtin_expect(odd, 0)) {
-#pragma unroll 1
-                        for (uint32_t c = 0; c < kSlotBytes; c += 2 * kTile * 16) {
-                            const uint4 x = ld_shared16(at0 + c);
-                            st_shared16(at0 + c, x.x & ~nonfinite_mask(x.x), x.y & ~nonfinite_mask(x.y),
-                                        x.z & ~nonfinite_mask(x.z), x.w & ~nonfinite_mask(x.w));
-                        }
-                        C.poisoned[unit % 8] = unit + 1;
-                        fence_async_shared();
-                    }
                 }
                 rv.next(v_slots);
                 tmem_wait_st();

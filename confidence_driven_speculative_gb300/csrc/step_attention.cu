@@ -12,22 +12,42 @@
 //     S^T [128 keys x N]  = K [128 x D] Q^T          (K and Q K-major)
 //     O^T [D x N]        += V^T [D x 128] P^T        (V and P MN-major)
 //     L   [D x N]        += 1 [D x 128] P^T          (sum of the rounded weights)
-// Each softmax thread owns one key, so the exponentials are spread over all
-// 128 threads however few the columns are.  S, O and L live in TMEM.  The
-// reference is the first tile's maximum and moves only when some score
-// passes it by 2^8 (the weights stay in range of fp32 and bfloat16 keeps its
-// relative step), so an ordinary tile needs no reduction over keys at all:
-// one vote of the 128 threads.
+// S, O and L live in TMEM.  A softmax thread owns one key and, of a tile's
+// columns, every fourth group of 16: four groups of 128 threads share a tile
+// (two groups: static 71 us against 66 below).
 //
-// Bound: bytes of the cache.  One persistent CTA per SM keeps a ring of
-// 32 KB K and V tiles (128 keys x 128) filled by TMA; a tile's chain (S, softmax, O)
-// is shorter than its copy, so one chain in flight is enough.
+// The reference is the first tile's maximum and moves only when some score
+// passes it by 2^32, which fp32 sums and bfloat16 weights hold with an unchanged
+// relative step.  So an ordinary tile needs no reduction over keys, only the
+// threads' vote that nothing passed.  Weights are rounded to bfloat16 for the
+// tensor core, by a relative 2^-8 at most, and L sums the rounded ones, so
+// that the errors of numerator and denominator partly cancel.
 //
-// Split.  The tiles of all (request, cached head, block of columns) units
-// form one list, cut evenly over the CTAs; the cut points come from a scan of
-// the lengths in every CTA, on the device.  A unit that is cut leaves partial
-// (o, m, l) in the workspace, in fp32, and step_join_kernel adds them in the order of
-// the keys, so the result does not depend on timing.
+// Bound: bytes of the cache.  One persistent CTA per SM (four softmax groups
+// want its registers) keeps a ring of K and V tiles, 128 keys each, filled by TMA.
+// The K producer, the V producer and a third that shares both look up pages a
+// tile ahead.  A page of 8 k positions goes in boxes of whole pages or parts of
+// them.  Other pages are gathered four keys a copy: 31 clocks per 512 bytes
+// whichever warp issues them, at most 70 % of a copy's rate; copies by the
+// lanes themselves were slower (123 us against 89 for the window below).
+//
+// Split.  The tiles of all (request, cached head, block of rows) units form
+// one list, cut evenly over the CTAs; a unit counts for two tiles more than it
+// has, what its start and end cost (without: 42 to 85 us a CTA where 49 to 61
+// are now).  The cut points come from a scan of the lengths in every CTA, on
+// the device.  A unit that is cut leaves partial (o, m, l) in the workspace,
+// in fp32, and the CTA that writes its last part adds them in the order of the
+// keys: the result does not depend on timing.
+//
+// Measured, 8 cached heads of 128, against the cache's bytes at a copy's 6.79
+// TB/s: 256 requests of 16 to 4095 keys with 1 to 7 rows of 32 heads 311 to
+// 318 us (floor 297); 2 of 131 000 keys with 9 rows of 64 heads 170 (158); 32
+// of 16 to 4095 keys with 17 rows 62 (42); one row over 4096 keys 13.4 (2.5);
+// 64 requests with a window of 1024 over single-position pages 84 (39).
+// Long caches run at the memory's rate.  Otherwise a unit's end costs what two
+// to three tiles do (the wait for its last product, the outputs, the fences of
+// its parts), and one request alone is a chain of latencies: launch, cut, tile,
+// join.
 #include <algorithm>
 #include <type_traits>
 

@@ -337,8 +337,9 @@ dspark_status dspark_fit_sts_tau(int32_t N, int32_t gamma, const float *conf,
  *   - Element type: q, k, v, the caches and the outputs are bfloat16
  *     (dtype = DSPARK_BF16; another code is DSPARK_EDTYPE).  Scores, softmax
  *     statistics and sums are fp32; each output is rounded once.  Softmax
- *     weights are rounded to bfloat16 before they multiply v, and their sum
- *     is taken over the rounded weights.
+ *     weights are rounded to bfloat16 before they multiply v; their sum is
+ *     taken over the rounded weights in dspark_step_attention, over the
+ *     unrounded ones in dspark_prompt_attention.
  *   - Packed rows: row r belongs to request row_req[r] (-1: padding) and sits
  *     at position packed_pos[r]; request b owns rows row_off[b] ..
  *     row_off[b+1], at consecutive positions.  These are the arrays that
