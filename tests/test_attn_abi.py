@@ -119,6 +119,31 @@ def test_step_attention_refusals(lib):
         assert status(lib, f, valid(**kw)) == binding.DSPARK_EALIGN, kw
 
 
+def test_step_attention_refuses_a_wide_group(lib):
+    f = "dspark_step_attention"
+    size = binding.dspark_attn_workspace_size(256, 1, 128, 9)
+    wide = dict(Hq=256, Hkv=1, workspace_bytes=size, head_stride=128)
+    assert status(lib, f, valid(**wide)) == binding.DSPARK_EINVAL
+    assert "256 query heads" in binding.last_error()
+
+
+def test_step_attention_refuses_pages_it_cannot_view(lib):
+    """Pages whose size has no factor of 8 are gathered: heads and pages must then lie a whole
+    number of slots apart, or all heads within one slot."""
+    f = "dspark_step_attention"
+    for kw in (dict(page_size=12, page_stride=12 * 256 + 128),                    # half a slot over
+               dict(page_size=12, slot_stride=128, head_stride=12 * 128 + 64, page_stride=32 * 128)):
+        assert status(lib, f, valid(**kw)) == binding.DSPARK_EINVAL, kw
+        assert "multiple of 8" in binding.last_error()
+
+
+def test_step_attention_refuses_a_batch_past_32_bits(lib):
+    f = "dspark_step_attention"
+    kw = dict(B=65536, rows=65536, max_pages=1 << 20, page_size=64, page_stride=64 * 256)
+    assert status(lib, f, valid(**kw)) == binding.DSPARK_EINVAL
+    assert "too large a batch" in binding.last_error()
+
+
 def test_prompt_attention_refusals(lib):
     f = "dspark_prompt_attention"
     for kw in (dict(k_rot=None), dict(v=None), dict(v_stride=128)):
