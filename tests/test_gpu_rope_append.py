@@ -162,3 +162,16 @@ def test_a_cache_past_two_to_the_31_elements(cuda_lib):
     torch.cuda.synchronize()
     assert torch.equal(kc[-1, -2:], k) and torch.equal(vc[-1, -2:], v)
     assert int(kc[:-1].count_nonzero()) == 0 and int(vc[:-1].count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rows", [2127, 2129, 4400, 8512, 8514])
+def test_long_lists_of_row_slots(cuda_lib, rows, interleaved, D):
+    """Lists that CTAs walk and lists with a CTA for each slot, a few rows in front of padding or
+    every slot in use (the last one too)."""
+    n = [(5 * i) % 8 for i in range(250)]
+    if rows != 4400:
+        n.append(rows - sum(n))
+    run_case(6, ctx=[(11 * i) % 90 for i in range(len(n))], n=n, rows=rows, Hq=2, Hkv=1, D=D, page=16,
+             rot=D, theta=1.0e4, interleaved=interleaved, heads_first=False, k_rot=True)
