@@ -22,15 +22,15 @@
 // Units are handed out by a counter, the longest of a prompt first, so the
 // CTAs end together; a unit's result does not depend on who computes it.
 //
-// Measured, D = 128: one prompt of 8192 rows and 32 heads 316 us at full
-// clocks, 1.74 PFLOP/s where a library product reaches 1.91 (the power limit
-// can take it to 350); 24 prompts of 20 to 2000 rows and 40 heads 228 us, 113
-// at that rate.  A step (both blocks' products, 2048 clocks) takes about 2900:
-// a block's chain is 1024 clocks of its own products, 220 until the softmax
-// sees them, 450 for loads and maxima, 240 for the halves' vote, 700 for the
-// weights, 150 back, and TMEM has no room for a second S.  A unit's border
-// costs some 4000 clocks more (last product, outputs, diagonal masks), and
-// short prompts have few steps to a unit.
+// Measured, D = 128: one prompt of 8192 rows and 32 heads 316 us at 2070 MHz,
+// 1.74 PFLOP/s where a library product reaches 1.91; after some seconds the
+// power limit holds both back, 350 us = 1.57 against 1.72.  24 prompts of 20 to
+// 2000 rows and 40 heads 228 us, 113 at the library's rate.  A step's products
+// are 2048 clocks by the tensor cores' nominal rate and 2770 at the library's; a
+// step takes about 2900.  The softmax hides behind that: without the halves'
+// vote (240 clocks of a block's chain) the same prompts take 319 us against
+// 321.  A unit's border costs some 4000 clocks more (last product, outputs,
+// diagonal masks), and short prompts have few steps to a unit.
 #include <algorithm>
 
 #include "attn.cuh"
