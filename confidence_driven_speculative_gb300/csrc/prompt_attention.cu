@@ -32,6 +32,7 @@
 // 321.  A unit's border costs some 4000 clocks more (last product, outputs,
 // diagonal masks), and short prompts have few steps to a unit.
 #include <algorithm>
+#include <cmath>
 
 #include "attn.cuh"
 #include "dspark_internal.cuh"
@@ -47,15 +48,22 @@ constexpr int kWarpMma = 0, kWarpLoad = 1, kWarpReady = 2, kWarpSoft = 4;  // 3:
 constexpr int kSlotsMax = 10;
 constexpr int kSched = 4;         // units on their way to the warps
 constexpr int kSchedReaders = 18; // warps that read them
-constexpr float kRefMin = -1e30f;
+constexpr float kRefMin = -3.402823466e38f;  // reference of a row without a score yet: no score is lower
 constexpr float kRefSlack = 32.0f;
+// log2: from here on a reference is far.  A weight is 2^(s * scale - reference), fused, so half a step of the
+// rounded reference is an error of the exponent, the same for all of a row: 2^4 below this limit, more than
+// fp32's range from 2^32 on.  A far row is scaled by a power of two instead: its products are exact.  That
+// changes no weight that counts: fp32 scores of that size are equal or lie 2^4 apart at least.  (Rounding the
+// products instead, in all rows: packed 231 us against 236, long 349 against 358.)
+constexpr float kFar = 536870912.0f;
 constexpr size_t kSmemBytes = 232448;
 
 struct PromptArgs {
     int B, rows, q_max, Hq, Hkv, G, window;
     int slots, k_slots;
     int wide_out;      // out is 32-byte aligned
-    float scale2;
+    float scale2;      // scale * log2(e)
+    float far_scale;   // the power of two at or above it
     int64_t v_stride;
     const uint16_t *v;
     const int32_t *row_off;
@@ -522,7 +530,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
             for (int t = t_lo; t < (sp.hi == 0 ? t_hi : sp.lo); ++t) rv.next(v_slots);
             if (sp.hi == 0) continue;
             const int q = u.q0 + a * kTile + row;  // the row; past the prompt: computed, not stored
-            float ref = 0.f;
+            float ref = 0.f, scale2 = A.scale2;  // the row's; far_scale where its scores are far
             float2 l2 = make_float2(0.f, 0.f);
             // Once a wait has given up, the others return at once and the
             // loops run to their ends on whatever there is; the status tells.
@@ -581,15 +589,24 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                     m0 = max3(m0, s[e], s[e + 1]);
                     m1 = max3(m1, s[e + 2], s[e + 3]);
                 }
-                const float m = max3(m0, m1, fmaxf(s[kKeys - 2], s[kKeys - 1])) * A.scale2;
+                const float m = max3(m0, m1, fmaxf(s[kKeys - 2], s[kKeys - 1]));
                 const bool first = t == sp.lo;
-                if (__builtin_expect(pair_any(first || m > ref + kRefSlack), 0)) {
-                    const float now = fmaxf(fmaxf(m, exchange(0, m)), kRefMin);
+                if (__builtin_expect(pair_any(first || m * scale2 > ref + kRefSlack), 0)) {
+                    const float top = fmaxf(m, exchange(0, m)), near = top * A.scale2;
+                    const float to_scale = fabsf(near) > kFar ? A.far_scale : A.scale2;
+                    const float to = fmaxf(top * to_scale, kRefMin);
                     if (first) {
-                        ref = now;
-                    } else {
-                        const float to = now > ref + kRefSlack ? now : ref, f = exp2_approx(ref - to);
                         ref = to;
+                        scale2 = to_scale;
+                    } else {
+                        // From near to far the difference is one of near values; from far to
+                        // near it is beyond any exponent, and f is 0.
+                        const bool moves = top * scale2 > ref + kRefSlack;
+                        const float f = moves ? exp2_approx(ref - (to_scale == scale2 ? to : near)) : 1.f;
+                        if (moves) {
+                            ref = to;
+                            scale2 = to_scale;
+                        }
                         l2.x *= f;
                         l2.y *= f;
 #pragma unroll 1
@@ -606,7 +623,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                         pair_sync();  // all of O is rescaled before either half's P is used
                     }
                 }
-                const float2 sc = make_float2(A.scale2, A.scale2), nr = make_float2(-ref, -ref);
+                const float2 sc = make_float2(scale2, scale2), nr = make_float2(-ref, -ref);
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 32) {
                     uint32_t p[16];
@@ -693,6 +710,8 @@ cudaError_t launch_prompt_attention(const dspark_attn &a, int sms, uint64_t wait
     A.B = a.B; A.rows = a.rows; A.q_max = a.q_max; A.Hq = a.Hq; A.Hkv = a.Hkv; A.G = a.Hq / a.Hkv;
     A.window = a.window;
     A.scale2 = float(double(a.scale) * 1.4426950408889634);
+    int exponent;
+    A.far_scale = std::frexp(A.scale2, &exponent) == 0.5f ? A.scale2 : std::ldexp(1.0f, exponent);
     A.v_stride = a.v_stride;
     A.v = static_cast<const uint16_t *>(a.v);
     A.row_off = a.row_off;
