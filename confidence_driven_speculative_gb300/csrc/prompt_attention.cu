@@ -2,10 +2,12 @@
 //
 // Mathematics.  For a block of rows of one query head: S = Q K^T, the weights
 // P = 2^(scale log2(e) S - m) against a running reference m per row, l the
-// sum of P, O += P V; the output is O / l.  The reference is the first tile's
-// maximum; a later tile moves it, and rescales O and l, only where its
-// maximum passes the reference by 2^32 (the weights stay in the range of fp32
-// and bfloat16 keeps its relative step), which is next to never.
+// sum of P, O += P V; the output is O / l.  The reference lies 16 above the first
+// tile's maximum; a later tile moves it, and rescales O and l, only where a score
+// passes it, which is next to never (with 8 in place of 16: long 358 us against 353).  So no
+// weight passes 1, and O overflows only where the values' own sum does; a row's
+// largest weight is 2^-16 at least, which fp32 sums and bfloat16 hold with an
+// unchanged relative step.
 //
 // The weights are rounded to bfloat16 for the tensor core, by a relative 2^-8
 // at most; l sums them unrounded, in registers.
@@ -49,7 +51,7 @@ constexpr int kSlotsMax = 10;
 constexpr int kSched = 4;         // units on their way to the warps
 constexpr int kSchedReaders = 18; // warps that read them
 constexpr float kRefMin = -3.402823466e38f;  // reference of a row without a score yet: no score is lower
-constexpr float kRefSlack = 32.0f;
+constexpr float kHeadroom = 16.0f;  // log2: the reference over the maximum that sets it
 // log2: from here on a reference is far.  A weight is 2^(s * scale - reference), fused, so half a step of the
 // rounded reference is an error of the exponent, the same for all of a row: 2^4 below this limit, more than
 // fp32's range from 2^32 on.  A far row is scaled by a power of two instead: its products are exact.  That
@@ -591,17 +593,17 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                 }
                 const float m = max3(m0, m1, fmaxf(s[kKeys - 2], s[kKeys - 1]));
                 const bool first = t == sp.lo;
-                if (__builtin_expect(pair_any(first || m * scale2 > ref + kRefSlack), 0)) {
-                    const float top = fmaxf(m, exchange(0, m)), near = top * A.scale2;
+                if (__builtin_expect(pair_any(first || m * scale2 > ref), 0)) {
+                    const float top = fmaxf(m, exchange(0, m)), near = top * A.scale2 + kHeadroom;
                     const float to_scale = fabsf(near) > kFar ? A.far_scale : A.scale2;
-                    const float to = fmaxf(top * to_scale, kRefMin);
+                    const float to = fmaxf(top * to_scale + kHeadroom, kRefMin);
                     if (first) {
                         ref = to;
                         scale2 = to_scale;
                     } else {
                         // From near to far the difference is one of near values; from far to
                         // near it is beyond any exponent, and f is 0.
-                        const bool moves = top * scale2 > ref + kRefSlack;
+                        const bool moves = top * scale2 > ref;
                         const float f = moves ? exp2_approx(ref - (to_scale == scale2 ? to : near)) : 1.f;
                         if (moves) {
                             ref = to;

@@ -16,9 +16,11 @@
 // columns, every fourth group of 16: four groups of 128 threads share a tile
 // (two groups: static 71 us against 66 below).
 //
-// The reference is the first tile's maximum and moves only when some score
-// passes it by 2^32, which fp32 sums and bfloat16 weights hold with an unchanged
-// relative step.  So an ordinary tile needs no reduction over keys, only the
+// The reference lies 16 above the first tile's maximum and moves only when some
+// score passes it (with 8 in place of 16: window 85.4 us against 83.8).  So no weight passes 1,
+// and O overflows only where the values' own sum does; a column's largest weight
+// is 2^-16 at least, which fp32 sums and bfloat16 hold with an unchanged relative
+// step.  An ordinary tile needs no reduction over keys, only the
 // threads' vote that nothing passed.  Weights are rounded to bfloat16 for the
 // tensor core, by a relative 2^-8 at most, and L sums the rounded ones, so
 // that the errors of numerator and denominator partly cancel.
@@ -70,7 +72,7 @@ constexpr int kWarpK = 16, kWarpV = 17, kWarpBoth = 18, kWarpMma = 19;
 constexpr int kThreadsStep = 640;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRefMin = -3.402823466e38f;  // reference of a column without a score yet: no score is lower
-constexpr float kRefSlack = 32.0f; // log2: how far a score may pass the reference
+constexpr float kHeadroom = 16.0f; // log2: the reference over the maximum that sets it
 constexpr int kWarpScan = 128;         // up to so many requests, every warp finds the cut by itself
 constexpr int kUnitCost = 2;           // what a unit costs beside its tiles, in tiles
 constexpr size_t kSmemBytes = 232448;  // shared memory of a CTA
@@ -254,8 +256,8 @@ __device__ __forceinline__ float weigh16(float (&s)[16], const float *ref, float
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
         // The product is rounded as the reference's was: the maximum's exponent is then exactly 0 however
-        // far the scores lie from 0.  Fused, it is off by half a step of the reference, by more than fp32's
-        // range from scores of 2^32 on (and 1 % faster: static 62.2 us against 62.8).
+        // far the scores lie from 0 (or what kHeadroom leaves).  Fused, it is off by half a step of the reference,
+        // by more than fp32's range from scores of 2^32 on (and 1 % faster: static 62.2 us against 62.8).
         float x = __fmul_rn(s[e], scale2) - r[e], y = __fmul_rn(s[e + 1], scale2) - r[e + 1];
         if (kMasked) {
             if (!((seen >> e) & 1)) x = -INFINITY;
@@ -870,8 +872,8 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 __syncwarp();
 
                 // Weights of the tile against the reference.  A unit's first
-                // tile sets the reference before, a tile that passes it by
-                // too much moves it and starts again (once: then none does).
+                // tile sets the reference before, a tile that passes it
+                // moves it and starts again (once: then none does).
                 for (int turn = 0; turn < 2; ++turn) {
                     if (__builtin_expect(move, 0)) {
                         if (!first && A.two_p)
@@ -897,8 +899,8 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                         for (int n = tid; n < N; n += kSoftThreads) {
                             const float old = first ? kRefMin : C.ref[n];
                             const float *const cm = colmax + n;
-                            const float now = fmaxf(fmaxf(fmaxf(cm[0], cm[A.ncap]),
-                                                          fmaxf(cm[2 * A.ncap], cm[3 * A.ncap])), old);
+                            const float top = fmaxf(fmaxf(cm[0], cm[A.ncap]), fmaxf(cm[2 * A.ncap], cm[3 * A.ncap]));
+                            const float now = fmaxf(top + kHeadroom, old);
                             // the columns past the last weigh nothing
                             C.ref[n] = n < u.ncols ? now : INFINITY;
                             C.fac[n] = exp2_approx(old - now);
@@ -932,7 +934,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                     }
                     fence_async_shared();
                     tc_fence_before();
-                    move = soft_any(top > kRefSlack);
+                    move = soft_any(top > 0.f);
                     if (__builtin_expect(!move, 1)) break;
                 }
                 if (tid == 0) mbar_arrive(&C.p_full[pb]);

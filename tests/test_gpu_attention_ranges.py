@@ -1,6 +1,6 @@
-"""The attention calls at the ends of the number range: scores far from zero.
+"""The attention calls at the ends of the number range: scores far from zero, large values.
 
-The rows and keys here lie along one entry of the head, with powers of two or
+In the first tests the rows and keys lie along one entry of the head, with powers of two or
 few bits, so every score is exact in fp32 and a softmax over them is uniform
 over the keys that tie for the maximum: the weights are exactly 1 and 0, and
 what is left is the output's own rounding and the fp32 sums (the harness's
@@ -11,6 +11,7 @@ import pytest
 import torch
 
 from confidence_driven_speculative_gb300 import binding
+from oracle import attention as oa
 from tests.attn_harness import assert_close, dev, make_table, offsets, wide
 
 pytestmark = pytest.mark.gpu
@@ -101,3 +102,21 @@ def test_scores_far_from_zero(cuda_lib, call, D, power, sign):
     check_ties(call, D, q, early * unit)
     check_ties(call, D, q, late * unit)
     check_ties(call, D, q, (73 + sign * (j // 64)) * unit)  # each tile passes the one before
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("rise", [4.0, 10.0, 11.5, 20.0, 21.5, 60.0])
+@pytest.mark.parametrize("power", [100, 115])
+def test_large_finite_values_under_a_late_maximum(cuda_lib, call, D, rise, power):
+    """Values near 2^power whose averages are as large.  From the second tile on the scores lie
+    ``rise`` above the first tile's."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    v = (2.0 ** power * torch.randn((KEYS, 2, D), generator=gen, device="cuda")).to(torch.bfloat16)
+    k = np.where(np.arange(KEYS) < 128, 0.0, rise)
+    n, Hq = 3, 4
+    q, keys = along([1.0] * n, Hq, D), along(k, 2, D)
+    got = CALLS[call](q, keys, v, 1.0)
+    o, spread, ds = oa.attend(wide(q), wide(keys), wide(v), KEYS - n, 1.0)
+    for out in got:
+        assert_close(out, o, spread, ds, KEYS, (call, rise))
