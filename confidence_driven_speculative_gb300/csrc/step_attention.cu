@@ -201,7 +201,8 @@ struct Ctrl {
     uint64_t q_full[2], q_empty[2], s_full[2];
     uint64_t p_full[2], pv_done[2], drained;
     uint32_t tmem;
-    int gave_up, poison, joins;
+    int gave_up, joins;
+    int poison;  // the CTA's last unit, counted from 1, that lost values (a tag: nobody has to clear it)
     Join join[2];
     int warp_cost[kThreadsStep / 32], warp_units[kThreadsStep / 32];
     int tiles_before[2];  // tiles of the list before this CTA's and up to its last
@@ -815,7 +816,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
         Ring rv;
         const int v_slots = A.slots - A.k_slots;
         int i = 0;  // tile of the CTA
-        for (bool first_unit = true; i < tiles; first_unit = false) {
+        for (int unit = 1; i < tiles; ++unit) {
             const int N = (u.ncols + 15) & ~15, t_first = t;
             const int here = min(u.q.nt - t, tiles - i);
             // tiles that every column sees in full: [whole_lo, whole_hi)
@@ -864,7 +865,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                         if (__builtin_expect(nonfinite_any(x), 0)) {
                             st_shared16(at, x.x & ~nonfinite_mask(x.x), x.y & ~nonfinite_mask(x.y),
                                         x.z & ~nonfinite_mask(x.z), x.w & ~nonfinite_mask(x.w));
-                            C.poison = 1;
+                            C.poison = unit;
                         }
                     }
                 }
@@ -994,8 +995,9 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                     }
                 }
             }
-            if (C.poison) soft_sync();  // the other group's outputs are written
-            if (__builtin_expect(C.poison, 0) && writer && grp == 0) {
+            const bool poisoned = C.poison == unit;
+            if (poisoned) soft_sync();  // the other groups' outputs are written
+            if (__builtin_expect(poisoned, 0) && writer && grp == 0) {
                 // What was taken out of V: for the keys of this CTA's
                 // tiles that some columns see and others do not.
                 const int k0 = max((u.q.t0 + t_first) * kTile, u.q.kbeg);
@@ -1024,7 +1026,6 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
             tc_fence_before();
             soft_sync();  // ref, poison and O are read before the next unit writes them
             if (tid == 0) {
-                C.poison = 0;
                 if (split) __threadfence();  // all the CTA's writes of the part: they came before the barrier
                 if (split && atomicAdd(&A.arrived[first_cta], 1) == members - 1) {
                     A.arrived[first_cta] = 0;  // as the next call wants it
