@@ -538,13 +538,16 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
             // loops run to their ends on whatever there is; the status tells.
             for (int t = sp.lo; t < sp.hi; ++t) {
                 const bool cut = partial<kWindow>(A, u, a, t);
-                if (cut) {
-                    // Masked keys must not reach O through 0 * infinity: a value
-                    // tile that some row does not see in full loses its NaN and
-                    // infinities; the rows that see them get them back at the
-                    // unit's end.  (The other block may read the tile before or
-                    // after: what it then gets back it already has, or lacks.)
-                    // The tile's scores are still being made.
+                // Masked keys must not reach O through 0 * infinity: a value
+                // tile that some row does not see in full loses its NaN and
+                // infinities; the rows that see them get them back at the
+                // unit's end.  Of a tile that both blocks walk, block 0 does it
+                // for both: its P comes before either block's products with
+                // that tile, so both read it clean, and both outputs come after
+                // the mark.  The tile's scores are still being made.
+                bool clean = cut;
+                if (kWindow && t >= other.lo && t < other.hi) clean = a == 0 && (cut || partial<kWindow>(A, u, 1, t));
+                if (clean) {
                     wait_or_give_up(&C.full[A.k_slots + rv.slot], rv.phase, A.wait_ns, gave_up);
                     __syncwarp();
                     const uint32_t at0 = v_ring + rv.slot * kSlotBytes + (half * kTile + row) * 16;
