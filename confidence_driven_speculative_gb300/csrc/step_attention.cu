@@ -1084,8 +1084,10 @@ cudaError_t launch(StepArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStrea
     A.slots = int(std::min<size_t>((room - fixed) / slot, kMaxSlots));
     A.k_slots = A.slots / 2;
     const size_t smem = 2048 + fixed + A.slots * slot;
-    cudaError_t e = cudaFuncSetAttribute(step_attention_kernel<D, kBox>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    // The limit is the process's: the same for every shape, so that calls of other shapes, from other
+    // threads or between a graph's capture and its instantiation, leave it alone.
+    cudaError_t e = cudaFuncSetAttribute(step_attention_kernel<D, kBox>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(kSmemBytes - sizeof(Ctrl)));
     if (e != cudaSuccess) return e;
     return launch_overlapped(step_attention_kernel<D, kBox>, ctas, kThreadsStep, smem, s, A, maps[0], maps[1], maps[2]);
 }
