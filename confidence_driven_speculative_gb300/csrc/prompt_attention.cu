@@ -109,6 +109,7 @@ struct Ctrl {
     int warp_sum[kScan / 32];
     float swap[2][2][2][kTile];  // between the two threads of a row (maxima, sums): by block and half
     uint32_t tmem;
+    int issued[2], q_issued[2];  // copies of K and V tiles, of the blocks' queries
     int gave_up;
 };
 
@@ -304,18 +305,11 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                 }
             }
         }
-        if (C.gave_up) {
-            // Let the copies in flight land before the CTA ends.
-            bool landed = true;
-            for (int kv = 0; kv < 2; ++kv) {
-                const int slots = kv ? v_slots : A.k_slots;
-                for (int k = max(issued[kv] - slots, 0); landed && k < issued[kv]; ++k)
-                    landed = mbar_wait_bounded(&C.full[(kv ? A.k_slots : 0) + k % slots], (k / slots) & 1, kDrainTimeoutNs);
-            }
-            for (int a = 0; a < 2; ++a)
-                if (landed && q_uses[a]) landed = mbar_wait_bounded(&C.q_full[a], (q_uses[a] - 1) & 1, kDrainTimeoutNs);
-        }
         if (lane == 0) {
+            for (int a = 0; a < 2; ++a) {  // for the CTA's end, should a wait have given up
+                C.issued[a] = issued[a];
+                C.q_issued[a] = int(q_uses[a]);
+            }
             // The last CTA leaves the counter as the next call wants it.
             __threadfence();
             if (atomicAdd(A.counter + 1, 1) == int(gridDim.x) - 1) {
@@ -453,11 +447,6 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
             }
             w = nx;
         }
-        if (C.gave_up) {
-            if (elect_one()) mma_commit(&C.drained);
-            __syncwarp();
-            mbar_wait_bounded(&C.drained, 0, kDrainTimeoutNs);
-        }
     } else if (warp == kWarpReady) {
         // ---- the last of P's arrivals: V of its tile and K of the next are there,
         // so that the MMA issuer has one barrier to test and not three ----------
@@ -467,6 +456,8 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
         uint32_t uses[2] = {0, 0};
         bool ok = true;
         Unit u = sched.next(C, A, gave_up, lane);
+        if (u.h >= 0) ok = poll_or_give_up(&C.full[A.k_slots], 0, A.wait_ns, gave_up);
+        ok = __all_sync(0xffffffffu, ok);
         while (ok && u.h >= 0) {
             const Span sp[2] = {span_of<kWindow>(A, u, 0), span_of<kWindow>(A, u, 1)};
             const int t_hi = max(sp[0].hi, sp[1].hi);
@@ -692,7 +683,26 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid == 0 && C.gave_up) atomicOr(A.status, kStatusWaitTimeout);
+    if (__builtin_expect(C.gave_up, 0)) {
+        // No warp issues any more.  What is in flight lands before the CTA ends: the products, each slot's
+        // latest copy, the queries.
+        if (warp == kWarpMma) {
+            if (elect_one()) mma_commit(&C.drained);
+            __syncwarp();
+            mbar_wait_bounded(&C.drained, 0, kDrainTimeoutNs);
+        } else if (warp == kWarpLoad) {
+            bool landed = true;
+            for (int kv = 0; kv < 2; ++kv) {
+                const int slots = kv ? A.slots - A.k_slots : A.k_slots, n = C.issued[kv];
+                for (int k = max(n - slots, 0); landed && k < n; ++k)
+                    landed = mbar_wait_bounded(&C.full[(kv ? A.k_slots : 0) + k % slots], (k / slots) & 1, kDrainTimeoutNs);
+            }
+            for (int a = 0; a < 2; ++a)
+                if (landed && C.q_issued[a]) landed = mbar_wait_bounded(&C.q_full[a], (C.q_issued[a] - 1) & 1, kDrainTimeoutNs);
+        }
+        if (tid == 0) atomicOr(A.status, kStatusWaitTimeout);
+        __syncthreads();
+    }
     if (warp == kWarpMma) tmem_free(tmem, 512);
 }
 

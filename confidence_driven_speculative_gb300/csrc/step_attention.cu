@@ -201,6 +201,7 @@ struct Ctrl {
     uint64_t q_full[2], q_empty[2], s_full[2];
     uint64_t p_full[2], pv_done[2], drained;
     uint32_t tmem;
+    int issued[2][2], q_issued;  // copies: (by K's and V's warps, by the third) of K and V tiles; units' queries
     int gave_up, joins;
     int poison;  // the CTA's last unit, counted from 1, that lost values (a tag: nobody has to clear it)
     Join join[2];
@@ -388,6 +389,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
     } else if (tid == 64) {
         mbar_init(&C.drained, 1);
         C.gave_up = C.poison = C.joins = 0;
+        C.issued[0][0] = C.issued[0][1] = C.issued[1][0] = C.issued[1][1] = C.q_issued = 0;
         C.start_b = C.start_unit = C.start_tile = 0;
         C.tiles_before[0] = C.tiles_before[1] = 0;
     } else if (tid == 96) {
@@ -702,17 +704,10 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
             t = tx;
             ids = ahead;
         }
-        if (C.gave_up) {
-            // Let the copies in flight land before the CTA ends: this warp's
-            // latest copy to each slot, and the queries'.  A phase that another
-            // warp leaves open ends the wait at its limit; by then all has landed.
-            bool landed = true;
-            for (int kv = 0; kv < 2; ++kv)
-                for (int k = max(issued[kv] - ring_slots[kv], 0); landed && k < issued[kv]; ++k)
-                    landed = mbar_wait_bounded(&C.full[ring_slot0[kv] + k % ring_slots[kv]], (k / ring_slots[kv]) & 1,
-                                               kDrainTimeoutNs);
-            for (int k = max(units - 1 - A.two_q, 0); landed && k < units; ++k)
-                landed = mbar_wait_bounded(&C.q_full[A.two_q ? k & 1 : 0], (A.two_q ? k >> 1 : k) & 1, kDrainTimeoutNs);
+        if (lane == 0) {  // for the CTA's end, should a wait have given up
+            if (warp != kWarpV) C.issued[part][0] = issued[0];
+            if (warp != kWarpK) C.issued[part][1] = issued[1];
+            if (warp == kWarpK) C.q_issued = units;
         }
     } else if (tiles > 0 && warp == kWarpMma) {
         // ---- MMA issuer: S of the next tile and O, L of this one, whichever's
@@ -801,11 +796,6 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 break;
             }
         }
-        if (C.gave_up) {
-            if (elect_one()) mma_commit(&C.drained);
-            __syncwarp();
-            mbar_wait_bounded(&C.drained, 0, kDrainTimeoutNs);
-        }
     } else if (tiles > 0) {
         // ---- softmax: thread = key of the tile -----------------------------------
         // Once a wait has given up, the others return at once and the loop
@@ -816,6 +806,10 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
         Ring rv;
         const int v_slots = A.slots - A.k_slots;
         int i = 0;  // tile of the CTA
+        if (warp == 0) {
+            poll_or_give_up(&C.s_full[0], 0, A.wait_ns, gave_up);
+            __syncwarp();
+        }
         for (int unit = 1; i < tiles; ++unit) {
             const int N = (u.ncols + 15) & ~15, t_first = t;
             const int here = min(u.q.nt - t, tiles - i);
@@ -879,6 +873,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                     if (__builtin_expect(move, 0)) {
                         if (!first && A.two_p)
                             wait_or_give_up(&C.pv_done[pb ^ 1], ((i - 1) >> 1) & 1, A.wait_ns, gave_up);
+                        __syncwarp();
                         tc_fence_after();
                         // the warps' maxima wait in P, which is about to be written
                         float *const colmax = reinterpret_cast<float *>(dyn + (p_smem + pb * p_bytes - smem_addr(dyn)));
@@ -944,6 +939,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
             // ---- the unit's end in this CTA --------------------------------------
             wait_or_give_up(&C.pv_done[A.two_p ? (i - 1) & 1 : 0], (A.two_p ? (i - 1) >> 1 : i - 1) & 1,
                             A.wait_ns, gave_up);
+            __syncwarp();
             tc_fence_after();
             const bool split = t_first > 0 || t < u.q.nt;
             const int d = key % D;
@@ -1041,7 +1037,27 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid == 0 && C.gave_up) atomicOr(A.status, kStatusWaitTimeout);
+    if (__builtin_expect(C.gave_up, 0)) {
+        // No warp issues any more.  What is in flight lands before the CTA ends: the products, each slot's
+        // latest copy, the queries.  A phase that a warp left open ends the wait at its limit; by then
+        // all has landed.
+        if (warp == kWarpMma) {
+            if (elect_one()) mma_commit(&C.drained);
+            __syncwarp();
+            mbar_wait_bounded(&C.drained, 0, kDrainTimeoutNs);
+        } else if (warp == kWarpK) {
+            bool landed = true;
+            for (int kv = 0; kv < 2; ++kv) {
+                const int slots = kv ? A.slots - A.k_slots : A.k_slots, n = max(C.issued[0][kv], C.issued[1][kv]);
+                for (int k = max(n - slots, 0); landed && k < n; ++k)
+                    landed = mbar_wait_bounded(&C.full[(kv ? A.k_slots : 0) + k % slots], (k / slots) & 1, kDrainTimeoutNs);
+            }
+            for (int k = max(C.q_issued - 1 - A.two_q, 0); landed && k < C.q_issued; ++k)
+                landed = mbar_wait_bounded(&C.q_full[A.two_q ? k & 1 : 0], (A.two_q ? k >> 1 : k) & 1, kDrainTimeoutNs);
+        }
+        if (tid == 0) atomicOr(A.status, kStatusWaitTimeout);
+        __syncthreads();
+    }
     if (warp == kWarpMma) tmem_free(tmem, kTmemCols);
     // The joins come last, when every warp has time and the loops above keep
     // their registers.

@@ -258,7 +258,9 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 // Wait for phase `parity` of `bar`; false after `limit_ns`, or once another
 // warp of the CTA has given up (*gave_up).  The timer is read only after some
-// polls: reading it takes longer than an ordinary wait.
+// polls: reading it takes longer than an ordinary wait.  A poll suspends for
+// 3.9 us, so a wait of less than 62 us keeps to no limit (polls told to be
+// shorter are not, and cost 2 %: packed 231 us against 236).
 __device__ __forceinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
                                                 volatile int *gave_up) {
     uint64_t t0 = 0;
@@ -274,6 +276,21 @@ __device__ __forceinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity, 
             return false;
         }
     }
+}
+
+// The same, by tests that do not suspend, against the clock from the start: keeps
+// to any limit, but takes issue slots from other warps.  A CTA's first wait.
+__device__ __forceinline__ bool poll_or_give_up(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
+                                                volatile int *gave_up) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_test_wait(bar, parity)) {
+        if (*gave_up) return false;
+        if (global_timer_ns() - t0 > limit_ns) {
+            *gave_up = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 // Host: a launch whose set-up may overlap the end of the kernel before it in
