@@ -539,6 +539,13 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                 bool clean = cut;
                 if (kWindow && t >= other.lo && t < other.hi) clean = a == 0 && (cut || partial<kWindow>(A, u, 1, t));
                 if (clean) {
+                    // The wait for V is good only once the slot's use before has landed: a parity tells two
+                    // phases apart, not three.  The block's waits so far say so (a tile's scores are issued
+                    // after the products of the tile two before) but in two places that a window makes: block
+                    // 1's first tile, since it skips units without a wait, and block 0's second one where V
+                    // has two slots.  There the tile's own scores say it.
+                    if (kWindow && (a ? t == sp.lo : t == sp.lo + 1 && v_slots < 3))
+                        wait_or_give_up(&C.s_full[a], s_uses & 1, A.wait_ns, gave_up);
                     wait_or_give_up(&C.full[A.k_slots + rv.slot], rv.phase, A.wait_ns, gave_up);
                     __syncwarp();
                     const uint32_t at0 = v_ring + rv.slot * kSlotBytes + (half * kTile + row) * 16;
@@ -711,6 +718,7 @@ cudaError_t launch(PromptArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStr
     const size_t slot = size_t(D) * 2 * kTile;
     A.slots = int(std::min<size_t>((kSmemBytes - sizeof(Ctrl) - 1024 - 2 * slot) / slot, kSlotsMax));
     A.k_slots = A.slots / 2;
+    static_assert((kSmemBytes - sizeof(Ctrl) - 1024) / (D * 2 * kTile) >= 2 + 4, "two slots each of K and V");
     const size_t smem = 1024 + (2 + A.slots) * slot;
     const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D, kWindow>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
