@@ -452,11 +452,13 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
         // so that the MMA issuer has one barrier to test and not three ----------
         SchedReader sched;
         Ring rk, rv;
-        rk.next(A.k_slots);  // the first K is waited for by the MMA issuer
         uint32_t uses[2] = {0, 0};
         bool ok = true;
         Unit u = sched.next(C, A, gave_up, lane);
-        if (u.h >= 0) ok = poll_or_give_up(&C.full[A.k_slots], 0, A.wait_ns, gave_up);
+        // The first K, which the MMA issuer waits for itself: a wait for a slot's next use is good only once
+        // the use before has landed.
+        if (u.h >= 0) ok = poll_or_give_up(&C.full[rk.slot], rk.phase, A.wait_ns, gave_up);
+        rk.next(A.k_slots);
         ok = __all_sync(0xffffffffu, ok);
         while (ok && u.h >= 0) {
             const Span sp[2] = {span_of<kWindow>(A, u, 0), span_of<kWindow>(A, u, 1)};
