@@ -419,7 +419,9 @@ def rope_freq(rot_dim: int, theta: float = 10000.0, inv_freq=None, device="cuda"
 
 class AttnBuffers:
     """The ``dspark_attn`` struct of one batch shape, with the outputs and the
-    workspace that it points at.  Inputs are attached with :meth:`bind`."""
+    workspace that it points at.  Inputs are attached with :meth:`bind`.  The
+    outputs start as zeros; the calls write the rows of the batch only, so
+    padding rows keep what an earlier, longer batch left there."""
 
     def __init__(self, B: int, rows: int, q_max: int, Hq: int, Hkv: int, D: int,
                  page_size: int = 64, num_pages: int = 0, max_pages: int = 0, rot_dim: int = 0,
@@ -456,7 +458,8 @@ class AttnBuffers:
         contiguous heads (views of one projection's output are fine).  q_rot,
         k_rot: contiguous, in place of the buffers' own.  k_cache, v_cache:
         [num_pages, page_size, Hkv, D] views of any strides, both alike.
-        What is left out stays NULL; the library checks what each call needs."""
+        q_rot and k_rot stay as they are where they are left out; the others
+        become NULL, and the library checks what each call needs."""
         import torch
         a = self.attn
         bf16 = torch.bfloat16

@@ -10,7 +10,12 @@
 // unchanged relative step.
 //
 // The weights are rounded to bfloat16 for the tensor core, by a relative 2^-8
-// at most; l sums them unrounded, in registers.
+// at most; l sums the rounded ones, in registers, so that the errors of numerator
+// and denominator partly cancel: 0.0020 of the output's norm against 0.0023 with
+// the unrounded ones, where the output's own rounding is 0.0017 (and values that are
+// all alike come out as they are).  Additions that take a bfloat16 operand
+// cost next to nothing for that; widening the weights first does (packed 238 us
+// against 234, after P has gone out 241).
 //
 // Bound: the tensor cores.  A unit is 256 rows of one head in two blocks of
 // 128, walked over tiles of 128 keys.  S and O of both blocks fill TMEM
@@ -18,8 +23,8 @@
 // P V.  While one block's softmax runs, the tensor cores work on the other
 // block: O_0 += P_0 V with S_0 of the next tile, then O_1 += P_1 V with S_1.
 // Two threads share a row, 64 keys each: one thread a row had twice the chain
-// of exponentials between two products (359 us against 346 for the long
-// prompts below).
+// of exponentials between two products (in an earlier version 359 us against 346
+// for the long prompt below).
 //
 // Units are handed out by a counter, the longest of a prompt first, so the
 // CTAs end together; a unit's result does not depend on who computes it.
@@ -30,8 +35,8 @@
 // 2000 rows and 40 heads 228 us, 113 at the library's rate.  A step's products
 // are 2048 clocks by the tensor cores' nominal rate and 2770 at the library's; a
 // step takes about 2900.  The softmax hides behind that: without the halves'
-// vote (240 clocks of a block's chain) the same prompts take 319 us against
-// 321.  A unit's border costs some 4000 clocks more (last product, outputs,
+// vote (240 clocks of a block's chain) an earlier version took 319 us against
+// 321 at 2070 MHz.  A unit's border costs some 4000 clocks more (last product, outputs,
 // diagonal masks), and short prompts have few steps to a unit.
 #include <algorithm>
 #include <cmath>
@@ -629,16 +634,15 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                     }
                 }
                 const float2 sc = make_float2(scale2, scale2), nr = make_float2(-ref, -ref);
+                float2 sums[2] = {l2, make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 32) {
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float2 x = fma2(make_float2(s[c + e], s[c + e + 1]), sc, nr);
-                        x.x = exp2_approx(x.x);
-                        x.y = exp2_approx(x.y);
-                        l2 = add2(l2, x);
-                        p[e / 2] = pack_bf16x2(x.x, x.y);
+                        const float2 x = fma2(make_float2(s[c + e], s[c + e + 1]), sc, nr);
+                        p[e / 2] = pack_bf16x2(exp2_approx(x.x), exp2_approx(x.y));
+                        add_bf16x2(sums[(e / 2) & 1], p[e / 2]);
                     }
                     tmem_st16u(s_tm + (half * kKeys + c) / 2, p);
                 }
@@ -647,6 +651,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&C.p_full[a]);
+                l2 = add2(sums[0], sums[1]);
             }
             for (int t = sp.hi; t < t_hi; ++t) rv.next(v_slots);
             const float mine = l2.x + l2.y, l = mine + exchange(1, mine), inv = l == 0.f ? 0.f : 1.f / l;

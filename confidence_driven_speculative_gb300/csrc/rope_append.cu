@@ -13,9 +13,9 @@
 // cosines are computed once per row, and the loads of up to four heads are in
 // flight before the angles are needed.
 //
-// Measured, Hq = 32, Hkv = 8, D = 128: 20 425 rows (32 768 slots, k_rot
-// written too) 84.8 us, 6.4 TB/s, 95 % of a copy's rate; 1024 rows of 256
-// requests 6.4 us; one request's 17 rows 3.8 us a call, the host's part and
+// Measured, Hq = 32, Hkv = 8, D = 128: 20 425 rows, no padding, k_rot written
+// too, 84.7 us, 6.4 TB/s, 95 % of a copy's rate; 1024 rows of 256 requests in
+// 4352 slots 6.7 us; one request's 17 rows 3.8 us a call, the host's part and
 // the launch.
 #include "attn.cuh"
 #include "dspark_internal.cuh"

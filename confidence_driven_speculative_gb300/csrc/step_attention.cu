@@ -14,7 +14,8 @@
 //     L   [D x N]        += 1 [D x 128] P^T          (sum of the rounded weights)
 // S, O and L live in TMEM.  A softmax thread owns one key and, of a tile's
 // columns, every fourth group of 16: four groups of 128 threads share a tile
-// (two groups: static 71 us against 66 below).
+// (with two groups, in an earlier version: 71 us against 66 for 32 requests of 17
+// rows).
 //
 // The reference lies 16 above the first tile's maximum and moves only when some
 // score passes it (with 8 in place of 16: window 85.4 us against 83.8).  So no weight passes 1,
@@ -31,12 +32,13 @@
 // tile ahead.  A page of 8 k positions goes in boxes of whole pages or parts of
 // them.  Other pages are gathered four keys a copy: 31 clocks per 512 bytes
 // whichever warp issues them, at most 70 % of a copy's rate; copies by the
-// lanes themselves were slower (123 us against 89 for the window below).
+// lanes themselves were slower (in an earlier version 123 us against 89 for the
+// windowed case below).
 //
 // Split.  The tiles of all (request, cached head, block of rows) units form
 // one list, cut evenly over the CTAs; a unit counts for two tiles more than it
-// has, what its start and end cost (without: 42 to 85 us a CTA where 49 to 61
-// are now).  The cut points come from a scan of the lengths in every CTA, on
+// has, what its start and end cost (when that came in, a CTA's time went from 42
+// to 85 us to 49 to 61).  The cut points come from a scan of the lengths in every CTA, on
 // the device.  A unit that is cut leaves partial (o, m, l) in the workspace,
 // in fp32, and the CTA that writes its last part adds them in the order of the
 // keys: the result does not depend on timing.

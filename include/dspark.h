@@ -338,9 +338,8 @@ dspark_status dspark_fit_sts_tau(int32_t N, int32_t gamma, const float *conf,
  *     (dtype = DSPARK_BF16; another code is DSPARK_EDTYPE).  Scores, softmax
  *     statistics and sums are fp32; each output is rounded once.  Softmax
  *     weights are rounded to bfloat16 before they multiply v; their sum is
- *     taken over the rounded weights in dspark_step_attention, over the
- *     unrounded ones in dspark_prompt_attention.  No weight passes 1 before
- *     the division: a sum overflows only where the seen values' own sum does.
+ *     taken over the rounded weights.  No weight passes 1 before the division:
+ *     a sum overflows only where the seen values' own sum does.
  *   - Packed rows: row r belongs to request row_req[r] (-1: padding) and sits
  *     at position packed_pos[r]; request b owns rows row_off[b] ..
  *     row_off[b+1], at consecutive positions.  These are the arrays that
