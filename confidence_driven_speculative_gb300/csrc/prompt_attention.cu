@@ -29,15 +29,15 @@
 // Units are handed out by a counter, the longest of a prompt first, so the
 // CTAs end together; a unit's result does not depend on who computes it.
 //
-// Measured, D = 128: one prompt of 8192 rows and 32 heads 316 us at 2070 MHz,
-// 1.74 PFLOP/s where a library product reaches 1.91; after some seconds the
-// power limit holds both back, 350 us = 1.57 against 1.72.  24 prompts of 20 to
-// 2000 rows and 40 heads 228 us, 113 at the library's rate.  A step's products
-// are 2048 clocks by the tensor cores' nominal rate and 2770 at the library's; a
-// step takes about 2900.  The softmax hides behind that: without the halves'
-// vote (240 clocks of a block's chain) an earlier version took 319 us against
-// 321 at 2070 MHz.  A unit's border costs some 4000 clocks more (last product, outputs,
-// diagonal masks), and short prompts have few steps to a unit.
+// Measured, D = 128: one prompt of 8192 rows and 32 heads 346 to 350 us in loops
+// of seconds, under the power limit, 1.58 PFLOP/s where a library product keeps up
+// 1.72; in a burst of 15 ms at 2070 MHz 316 us, 1.74 against 1.91.  24 prompts of
+// 20 to 2000 rows and 40 heads 233 to 236 us (228 in a burst), 113 at the library's
+// rate.  A step's products are 2048 clocks by the tensor cores' nominal rate and
+// 2770 at the library's; a step takes about 2900.  The softmax hides behind that:
+// without the halves' vote (240 clocks of a block's chain) an earlier version took
+// 319 us against 321 in a burst.  A unit's border costs some 4000 clocks more (last
+// product, outputs, diagonal masks), and short prompts have few steps to a unit.
 #include <algorithm>
 #include <cmath>
 

@@ -45,9 +45,9 @@
 //
 // Measured, 8 cached heads of 128, against the cache's bytes at a copy's 6.79
 // TB/s: 256 requests of 16 to 4095 keys with 1 to 7 rows of 32 heads 311 to
-// 318 us (floor 297); 2 of 131 000 keys with 9 rows of 64 heads 170 (158); 32
-// of 16 to 4095 keys with 17 rows 62 (42); one row over 4096 keys 13.4 (2.5);
-// 64 requests with a window of 1024 over single-position pages 84 (39).
+// 319 us (floor 297); 2 of 131 000 keys with 9 rows of 64 heads 171 (158); 32
+// of 16 to 4095 keys with 17 rows 62.5 (42); one row over 4096 keys 13.3 (2.5);
+// 64 requests with a window of 1024 over single-position pages 84.5 (39).
 // Long caches run at the memory's rate.  Otherwise a unit's end costs what two
 // to three tiles do (the wait for its last product, the outputs, the fences of
 // its parts), and one request alone is a chain of latencies: launch, cut, tile,
