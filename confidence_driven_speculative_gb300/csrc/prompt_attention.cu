@@ -4,10 +4,10 @@
 // P = 2^(scale log2(e) S - m) against a running reference m per row, l the
 // sum of P, O += P V; the output is O / l.  The reference lies 16 above the first
 // tile's maximum; a later tile moves it, and rescales O and l, only where a score
-// passes it, which is next to never (with 8 in place of 16: long 358 us against 353).  So no
-// weight passes 1, and O overflows only where the values' own sum does; a row's
-// largest weight is 2^-16 at least, which fp32 sums and bfloat16 hold with an
-// unchanged relative step.
+// passes it, which is next to never (with 8 in place of 16: long 358 us against
+// 353).  So no weight passes 1, and O overflows only where the values' own sum
+// does; a row's largest weight is 2^-16 or about that, which fp32 sums and
+// bfloat16 hold with an unchanged relative step.
 //
 // The weights are rounded to bfloat16 for the tensor core, by a relative 2^-8
 // at most; l sums the rounded ones, in registers, so that the errors of numerator

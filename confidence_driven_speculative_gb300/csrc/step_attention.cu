@@ -3,8 +3,8 @@
 // Mathematics.  One request and one cached head give a block of
 // cols = rows * G query vectors (G query heads share the cached head) over the
 // request's keys.  The keys are walked in tiles of 128 with a running
-// reference m and, per column, o = sum 2^(x - m) v and l = sum 2^(x - m),
-// x = scale * log2(e) * q.k; the output is o / l.
+// reference m and, per column, o = sum p v and l = sum p of the weights
+// p = 2^(scale * log2(e) * (q.k - m)); the output is o / l.
 //
 // Layout.  A step has few columns (4 to a few tens) and many keys, so the
 // products are taken transposed: the 128 keys of a tile are the M side of the
@@ -17,12 +17,12 @@
 // (with two groups, in an earlier version: 71 us against 66 for 32 requests of 17
 // rows).
 //
-// The reference lies 16 above the first tile's maximum and moves only when some
-// score passes it (with 8 in place of 16: window 85.4 us against 83.8).  So no weight passes 1,
-// and O overflows only where the values' own sum does; a column's largest weight
-// is 2^-16 at least, which fp32 sums and bfloat16 hold with an unchanged relative
-// step.  An ordinary tile needs no reduction over keys, only the
-// threads' vote that nothing passed.  Weights are rounded to bfloat16 for the
+// The reference lies 2^16 of a weight above the first tile's maximum and moves
+// only when some score passes it (with 2^8: window 85.4 us against 83.8).  So no
+// weight passes 1, and O overflows only where the values' own sum does; a column's
+// largest weight is 2^-16 or about that, which fp32 sums and bfloat16 hold with an
+// unchanged relative step.  An ordinary tile needs no reduction over keys, only
+// the threads' vote that nothing passed.  Weights are rounded to bfloat16 for the
 // tensor core, by a relative 2^-8 at most, and L sums the rounded ones, so
 // that the errors of numerator and denominator partly cancel.
 //
@@ -92,6 +92,7 @@ struct StepArgs {
     int page_rows, head_rows;  // gather: rows of the 2-D view per page and head
     int head_x;                // gather: entries of a row per head
     float scale2;              // scale * log2(e)
+    float headroom;            // kHeadroom in scores q.k
     int64_t page_stride, slot_stride, head_stride;
     const uint16_t *v_cache;
     const int32_t *row_off, *seq_lens, *block_table;
@@ -245,7 +246,7 @@ __device__ __forceinline__ void visible_columns(const StepArgs &A, const Unit &u
     if (bad || kpos < u.q.kbeg || kpos >= u.q.kend) hi = lo;
 }
 
-// 16 columns of a tile, on their way from TMEM: weights 2^(s * scale2 - ref), rounded, to P; returns
+// 16 columns of a tile, on their way from TMEM: weights 2^((s - ref) * scale2), rounded, to P; returns
 // the largest exponent.  Columns whose bit of `seen` is clear weigh nothing.
 template <bool kMasked>
 __device__ __forceinline__ float weigh16(float (&s)[16], const float *ref, float scale2,
@@ -259,10 +260,10 @@ __device__ __forceinline__ float weigh16(float (&s)[16], const float *ref, float
     float top = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
-        // The product is rounded as the reference's was: the maximum's exponent is then exactly 0 however
-        // far the scores lie from 0 (or what kHeadroom leaves).  Fused, it is off by half a step of the reference,
-        // by more than fp32's range from scores of 2^32 on (and 1 % faster: static 62.2 us against 62.8).
-        float x = __fmul_rn(s[e], scale2) - r[e], y = __fmul_rn(s[e + 1], scale2) - r[e + 1];
+        // The difference comes first.  It is exact for scores near the reference, however far both lie from
+        // 0; a fused s * scale2 - scaled reference is off by half a step of that reference, by more than
+        // fp32's range from scores of 2^32 on (and 1 % faster: static 62.2 us against 62.8).
+        float x = (s[e] - r[e]) * scale2, y = (s[e + 1] - r[e + 1]) * scale2;
         if (kMasked) {
             if (!((seen >> e) & 1)) x = -INFINITY;
             if (!((seen >> (e + 1)) & 1)) y = -INFINITY;
@@ -320,7 +321,7 @@ __device__ __forceinline__ void join_columns(const StepArgs &A, const Join &J, i
 #pragma unroll
             for (int o = kParts / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const float m_new = fmaxf(m, top);  // the lane's column's
-            const float w = exp2_approx(ref - m_new), f_old = exp2_approx(m - m_new);
+            const float w = exp2_approx((ref - m_new) * A.scale2), f_old = exp2_approx((m - m_new) * A.scale2);
             m = m_new;
 #pragma unroll
             for (int c = 0; c < kCols; ++c) {
@@ -887,7 +888,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                             float keep = -INFINITY;
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                float x = ((seen >> e) & 1) ? s[e] * A.scale2 : -INFINITY;
+                                float x = ((seen >> e) & 1) ? s[e] : -INFINITY;
                                 asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(x) : "f"(x));
                                 if (lane == e) keep = x;
                             }
@@ -898,10 +899,10 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                             const float old = first ? kRefMin : C.ref[n];
                             const float *const cm = colmax + n;
                             const float top = fmaxf(fmaxf(cm[0], cm[A.ncap]), fmaxf(cm[2 * A.ncap], cm[3 * A.ncap]));
-                            const float now = fmaxf(top + kHeadroom, old);
+                            const float now = fmaxf(top + A.headroom, old);
                             // the columns past the last weigh nothing
                             C.ref[n] = n < u.ncols ? now : INFINITY;
-                            C.fac[n] = exp2_approx(old - now);
+                            C.fac[n] = exp2_approx((old - now) * A.scale2);
                         }
                         soft_sync();
                         if (!first) {
@@ -1158,6 +1159,7 @@ cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_n
     A.ncap = step_columns(a.Hq, a.Hkv, a.q_max);
     A.rows_cap = step_rows(a.Hq, a.Hkv, a.q_max);
     A.scale2 = float(double(a.scale) * 1.4426950408889634);
+    A.headroom = std::min(kHeadroom / A.scale2, 1e38f);
     A.page_stride = a.page_stride; A.slot_stride = a.slot_stride; A.head_stride = a.head_stride;
     A.v_cache = static_cast<const uint16_t *>(a.v_cache);
     A.row_off = a.row_off; A.seq_lens = a.seq_lens; A.block_table = a.block_table;

@@ -120,3 +120,25 @@ def test_large_finite_values_under_a_late_maximum(cuda_lib, call, D, rise, power
     o, spread, ds = oa.attend(wide(q), wide(keys), wide(v), KEYS - n, 1.0)
     for out in got:
         assert_close(out, o, spread, ds, KEYS, (call, rise))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("power", [12, 16, 20])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_close_together_far_from_zero(cuda_lib, call, D, power, sign):
+    """Scores +-2^power + u with u of an eighth's steps in [-4, 4): exact in fp32, and a softmax of them
+    is a softmax of the u (ds is theirs)."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    n, Hq, Hkv = 3, 4, 2
+    u = torch.randint(-32, 32, (KEYS,), generator=gen, device="cuda") / 8.0
+    q = along([2.0 ** (power // 2)] * n, Hq, D)
+    k = along([sign * 2.0 ** (power - power // 2)] * KEYS, Hkv, D)
+    q[:, :, 5], k[:, :, 5] = 1.0, u[:, None].to(torch.bfloat16)
+    v = torch.randn((KEYS, Hkv, D), generator=gen, device="cuda").to(torch.bfloat16)
+    got = CALLS[call](q, k, v, 1.0)
+    only_u = torch.zeros_like(q)
+    only_u[:, :, 5] = 1.0
+    o, spread, ds = oa.attend(wide(only_u), wide(k), wide(v), KEYS - n, 1.0)
+    for out in got:
+        assert_close(out, o, spread, ds, KEYS, (call, power))
