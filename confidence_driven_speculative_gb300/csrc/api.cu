@@ -664,6 +664,14 @@ dspark_status check_row_stride(int64_t stride, int heads, int D, const char *wha
     return DSPARK_OK;
 }
 
+// Rows rotated in place lie where the contiguous output has them; others would be overwritten unread.
+dspark_status check_in_place(const dspark_attn *a, const void *x, const void *rot, int64_t stride, int heads,
+                             const char *what, const char *fn) {
+    if (x == rot && a->rows > 1 && stride != (int64_t)heads * a->D)
+        return fail(DSPARK_EINVAL, "%s: %s_rot is %s, whose rows are not contiguous", fn, what, what);
+    return DSPARK_OK;
+}
+
 dspark_status check_attn_softmax(const dspark_attn *a, const char *fn) {
     if (!(a->scale > 0.0f) || std::isinf(a->scale))
         return fail(DSPARK_EINVAL, "%s: scale must be finite and > 0", fn);
@@ -722,6 +730,8 @@ dspark_status dspark_rope_append(const dspark_attn *a, dspark_stream_t stream) {
         if ((st = check_row_stride(a->k_stride, a->Hkv, a->D, "k_stride", fn))) return st;
         if ((st = check_row_stride(a->v_stride, a->Hkv, a->D, "v_stride", fn))) return st;
     }
+    if (a->q && (st = check_in_place(a, a->q, a->q_rot, a->q_stride, a->Hq, "q", fn))) return st;
+    if (a->k && (st = check_in_place(a, a->k, a->k_rot, a->k_stride, a->Hkv, "k", fn))) return st;
     DeviceInfo *dev;
     if ((st = device_info(&dev))) return st;
     cudaError_t e = dspark::launch_rope_append(*a, dev->sms, reinterpret_cast<cudaStream_t>(stream));
