@@ -61,6 +61,35 @@ class DsparkAttn(ctypes.Structure):
         + [("workspace_bytes", ctypes.c_size_t)])
 
 
+class DsparkTree(ctypes.Structure):
+    """Mirror of ``struct dspark_tree`` (same field order and C types)."""
+    _fields_ = (
+        [(n, ctypes.c_int32) for n in ("B", "rows", "q_max", "V", "logit_dtype")]
+        + [(n, _P) for n in (
+            "target_logits", "row_off", "parent", "packed_ids", "accept_len", "num_emitted", "path",
+            "out_tokens", "seq_lens_commit", "workspace")]
+        + [("workspace_bytes", ctypes.c_size_t)])
+
+
+class DsparkCache(ctypes.Structure):
+    """Mirror of ``struct dspark_cache`` (same field order and C types)."""
+    _fields_ = (
+        [(n, ctypes.c_int32) for n in ("layers", "Hkv", "D", "dtype", "page_size", "num_pages")]
+        + [(n, ctypes.c_int64) for n in ("layer_stride", "page_stride", "slot_stride", "head_stride")]
+        + [(n, _P) for n in ("k_cache", "v_cache")])
+
+
+class DsparkPages(ctypes.Structure):
+    """Mirror of ``struct dspark_pages`` (same field order and C types)."""
+    _fields_ = (
+        [("cache", DsparkCache)]
+        + [(n, ctypes.c_int32) for n in ("B_in", "B", "max_pages", "sinks")]
+        + [(n, _P) for n in (
+            "table_in", "parent", "keep_len", "want_len", "first_pos", "held", "table_out",
+            "granted_len", "tail_src", "tail_dst", "totals", "workspace")]
+        + [("workspace_bytes", ctypes.c_size_t)])
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -97,10 +126,24 @@ def load():
         lib.dspark_verify_cap_accept.restype = ctypes.c_int
         lib.dspark_verify_noalloc.argtypes = [SP, ctypes.c_int32, _P, _P]
         lib.dspark_verify_noalloc.restype = ctypes.c_int
-        for name in ("dspark_rope_append", "dspark_step_attention", "dspark_prompt_attention"):
+        AP = ctypes.POINTER(DsparkAttn)
+        i32 = ctypes.c_int32
+        for name, args in (
+                ("dspark_rope_append", [AP, _P]), ("dspark_rope_append_tree", [AP, _P]),
+                ("dspark_step_attention", [AP, _P]), ("dspark_prompt_attention", [AP, _P]),
+                ("dspark_step_attention_sinks", [AP, i32, _P]),
+                ("dspark_prompt_attention_sinks", [AP, i32, _P]),
+                ("dspark_step_attention_tree", [AP, _P, i32, _P]),
+                ("dspark_verify_tree", [ctypes.POINTER(DsparkTree), _P]),
+                ("dspark_commit_path", [ctypes.POINTER(DsparkCache), i32, i32, i32, _P, _P, _P, _P]),
+                ("dspark_update_pages", [ctypes.POINTER(DsparkPages), _P])):
             fn = getattr(lib, name)
-            fn.argtypes = [ctypes.POINTER(DsparkAttn), _P]
+            fn.argtypes = args
             fn.restype = ctypes.c_int
+        for name, n in (("dspark_tree_workspace_size", 3), ("dspark_pages_workspace_size", 2)):
+            fn = getattr(lib, name)
+            fn.argtypes = [i32] * n
+            fn.restype = ctypes.c_size_t
         lib.dspark_attn_workspace_size.argtypes = [ctypes.c_int32] * 4
         lib.dspark_attn_workspace_size.restype = ctypes.c_size_t
         lib.dspark_workspace_size.argtypes = [ctypes.c_int32] * 4
@@ -227,6 +270,71 @@ def dspark_prompt_attention(attn: DsparkAttn, stream=None, check: bool = True) -
     return _call("dspark_prompt_attention", attn, stream, check)
 
 
+def dspark_step_attention_sinks(attn: DsparkAttn, sinks: int, stream=None, check: bool = True) -> int:
+    """dspark_step_attention with the first ``sinks`` positions visible beside the window."""
+    rc = load().dspark_step_attention_sinks(ctypes.byref(attn), sinks, _stream(stream))
+    if check and rc != DSPARK_OK:
+        raise DsparkError(rc, "dspark_step_attention_sinks")
+    return rc
+
+
+def dspark_prompt_attention_sinks(attn: DsparkAttn, sinks: int, stream=None, check: bool = True) -> int:
+    """dspark_prompt_attention with the first ``sinks`` positions visible beside the window."""
+    rc = load().dspark_prompt_attention_sinks(ctypes.byref(attn), sinks, _stream(stream))
+    if check and rc != DSPARK_OK:
+        raise DsparkError(rc, "dspark_prompt_attention_sinks")
+    return rc
+
+
+def dspark_rope_append_tree(attn: DsparkAttn, stream=None, check: bool = True) -> int:
+    """dspark_rope_append for the rows of trees: turned by their positions, stored at seq_lens + index."""
+    return _call("dspark_rope_append_tree", attn, stream, check)
+
+
+def dspark_step_attention_tree(attn: DsparkAttn, row_seen, sinks: int = 0, stream=None,
+                               check: bool = True) -> int:
+    """The rows of trees over the paged cache.  ``row_seen``: device int64 [rows], bit i of a row's
+    word set where it sees row i of its request (see :func:`tree_rows`)."""
+    _device_words(row_seen, "row_seen", attn.rows)
+    rc = load().dspark_step_attention_tree(ctypes.byref(attn), row_seen.data_ptr(), sinks, _stream(stream))
+    if check and rc != DSPARK_OK:
+        raise DsparkError(rc, "dspark_step_attention_tree")
+    return rc
+
+
+def dspark_verify_tree(tree: DsparkTree, stream=None, check: bool = True) -> int:
+    """The walk that the target goes down each request's drafted tree."""
+    return _call("dspark_verify_tree", tree, stream, check)
+
+
+def dspark_commit_path(cache: DsparkCache, block_table, seq_lens, path, stream=None,
+                       check: bool = True) -> int:
+    """The accepted rows' entries move to their places, in all layers.  Device int32 tensors:
+    ``block_table`` [B, max_pages], ``seq_lens`` [B] (the length before the verify) or None, ``path``
+    [B, q_max] as dspark_verify_tree writes it."""
+    B, q_max = _rows_of(path, "path")
+    max_pages = _rows_of(block_table, "block_table", B)[1]
+    _device_array(seq_lens, "seq_lens", "int32", B, optional=True)
+    rc = load().dspark_commit_path(ctypes.byref(cache), B, q_max, max_pages, block_table.data_ptr(),
+                                   _ptr(seq_lens), path.data_ptr(), _stream(stream))
+    if check and rc != DSPARK_OK:
+        raise DsparkError(rc, "dspark_commit_path")
+    return rc
+
+
+def dspark_update_pages(pages: DsparkPages, stream=None, check: bool = True) -> int:
+    """The pages of a batch's next step: kept, forked, copied where two would write one, given out, freed."""
+    return _call("dspark_update_pages", pages, stream, check)
+
+
+def dspark_tree_workspace_size(B: int, rows: int, V: int) -> int:
+    return int(load().dspark_tree_workspace_size(B, rows, V))
+
+
+def dspark_pages_workspace_size(B: int, num_pages: int) -> int:
+    return int(load().dspark_pages_workspace_size(B, num_pages))
+
+
 def dspark_attn_workspace_size(Hq: int, Hkv: int, D: int, q_max: int) -> int:
     return int(load().dspark_attn_workspace_size(Hq, Hkv, D, q_max))
 
@@ -315,6 +423,28 @@ def _device_array(t, name: str, dtype: str, numel: Optional[int] = None, optiona
         raise ValueError(f"{name} must be contiguous")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+
+
+def _device_words(t, name: str, numel: int) -> None:
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch tensor")
+    if t.dtype != torch.int64:
+        raise ValueError(f"{name} must be int64, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be CUDA device memory")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+
+
+def _rows_of(t, name: str, rows: Optional[int] = None) -> tuple:
+    """Shape of a contiguous device int32 matrix (of ``rows`` rows, when given)."""
+    _device_array(t, name, "int32")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be [{'B' if rows is None else rows}, n], got {tuple(t.shape)}")
+    return int(t.shape[0]), int(t.shape[1])
 
 
 class StepBuffers:
@@ -510,6 +640,157 @@ class AttnBuffers:
 
     def device_status(self, stream=None) -> int:
         return dspark_read_device_status(self.workspace.data_ptr(), stream)
+
+
+def tree_rows(parent, row_off, seq_lens=None):
+    """What the rows of trees see and where they sit, from ``parent`` and ``row_off`` (as in
+    :class:`DsparkTree`; int32 tensors of one device, row_off[B] rows at most DSPARK_MAX_TREE_ROWS a
+    request): (row_seen int64 [rows], packed_pos int32 [rows], row_req int32 [rows]), the rows past
+    row_off[B] as padding.  Set-up in torch operations without a host round trip: once where the
+    trees' shape is fixed, else once a step."""
+    import torch
+    rows, dev = parent.shape[0], parent.device
+    off = row_off.long()
+    r = torch.arange(rows, device=dev)
+    req = torch.searchsorted(off[1:].contiguous(), r, right=True)
+    pad = req >= off.shape[0] - 1
+    req = req.clamp(max=off.shape[0] - 2)
+    j = r - off[req]
+    p = parent.long()
+    p = torch.where((j > 0) & (p >= 0) & (p < j) & ~pad, p, -1)
+    one = torch.ones((), dtype=torch.int64, device=dev)
+    seen = torch.where(pad, 0, one << j.clamp(0, 63))
+    depth = (p >= 0).long()
+    up = torch.where(p >= 0, off[req] + p, r)
+    for _ in range(6):  # ancestors by doubling: 64 rows are at most 63 deep
+        seen = seen | seen[up]
+        depth = depth + torch.where(up != r, depth[up], 0)
+        up = up[up]
+    pos = depth if seq_lens is None else depth + seq_lens.long()[req]
+    return (seen, torch.where(pad, 0, pos).to(torch.int32), torch.where(pad, -1, req).to(torch.int32))
+
+
+class TreeBuffers:
+    """The ``dspark_tree`` struct of one batch shape, with the outputs and the workspace that it
+    points at.  Inputs are attached with :meth:`bind`."""
+
+    def __init__(self, B: int, rows: int, q_max: int, V: int, device="cuda", stream=None):
+        import torch
+        i32 = dict(dtype=torch.int32, device=device)
+        self.accept_len, self.num_emitted = torch.zeros(B, **i32), torch.zeros(B, **i32)
+        self.path, self.out_tokens = torch.zeros((B, q_max), **i32), torch.zeros((B, q_max), **i32)
+        self.ws_bytes = dspark_tree_workspace_size(B, rows, V)
+        if self.ws_bytes == 0:
+            raise ValueError("shape outside the library's limits")
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        dspark_workspace_init(self.workspace.data_ptr(), self.ws_bytes, stream)
+        self.tree = t = DsparkTree()
+        t.B, t.rows, t.q_max, t.V = B, rows, q_max, V
+        for name in ("accept_len", "num_emitted", "path", "out_tokens"):
+            setattr(t, name, getattr(self, name).data_ptr())
+        t.workspace, t.workspace_bytes = self.workspace.data_ptr(), self.ws_bytes
+        self._keep = {}
+
+    def bind(self, target_logits, row_off, parent, packed_ids, seq_lens_commit=None) -> "TreeBuffers":
+        """Point the struct at device tensors: target_logits [rows, V] float32 or bfloat16, row_off
+        [B+1], parent and packed_ids [rows], seq_lens_commit [B] or None."""
+        t = self.tree
+        t.logit_dtype = _dtype_code(target_logits)
+        _device_view(target_logits, "target_logits", target_logits.dtype, (t.rows, t.V))
+        if not target_logits.is_contiguous():
+            raise ValueError("target_logits must be contiguous")
+        for name, x, n in (("row_off", row_off, t.B + 1), ("parent", parent, t.rows),
+                           ("packed_ids", packed_ids, t.rows)):
+            _device_array(x, name, "int32", n)
+            setattr(t, name, _ptr(x))
+        _device_array(seq_lens_commit, "seq_lens_commit", "int32", t.B, optional=True)
+        t.target_logits, t.seq_lens_commit = _ptr(target_logits), _ptr(seq_lens_commit)
+        self._keep = dict(target_logits=target_logits, row_off=row_off, parent=parent,
+                          packed_ids=packed_ids, seq_lens_commit=seq_lens_commit)
+        return self
+
+    def device_status(self, stream=None) -> int:
+        return dspark_read_device_status(self.workspace.data_ptr(), stream)
+
+
+class CacheView:
+    """The ``dspark_cache`` struct over caches that the caller holds: views [layers, num_pages,
+    page_size, Hkv, D] of any strides with contiguous entries, both alike, or of four axes for one
+    layer."""
+
+    def __init__(self, k_cache, v_cache):
+        import torch
+        if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4:
+            k_cache, v_cache = k_cache.unsqueeze(0), v_cache.unsqueeze(0)
+        if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 5:
+            raise ValueError("k_cache must be [layers, num_pages, page_size, Hkv, D]")
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            _device_view(t, name, torch.bfloat16, k_cache.shape)
+        st = _layer_strides(k_cache)
+        if st != _layer_strides(v_cache):
+            raise ValueError("k_cache and v_cache must have the same strides")
+        if st[4] != 1:
+            raise ValueError("the entries of k_cache must be contiguous")
+        self.cache = c = DsparkCache()
+        c.layers, c.num_pages, c.page_size, c.Hkv, c.D = (int(n) for n in k_cache.shape)
+        c.dtype = DSPARK_BF16
+        c.layer_stride, c.page_stride, c.slot_stride, c.head_stride = st[:4]
+        c.k_cache, c.v_cache = _ptr(k_cache), _ptr(v_cache)
+        self._keep = (k_cache, v_cache)
+
+
+class PageBuffers:
+    """The ``dspark_pages`` struct of one batch shape, with the outputs and the workspace that it
+    points at.  Inputs are attached with :meth:`bind`.  ``cache``: a :class:`CacheView`, or None with
+    ``page_size`` and ``num_pages`` where the caller copies the tails (tail_src, tail_dst)."""
+
+    def __init__(self, cache: Optional[CacheView], B_in: int, B: int, max_pages: int, sinks: int = 0,
+                 page_size: int = 0, num_pages: int = 0, device="cuda", stream=None):
+        import torch
+        i32 = dict(dtype=torch.int32, device=device)
+        self.pages = p = DsparkPages()
+        if cache is None:
+            p.cache.page_size, p.cache.num_pages = page_size, num_pages
+        else:
+            p.cache = cache.cache
+        self.table_out = torch.full((B, max_pages), -1, **i32)
+        self.granted_len, self.totals = torch.zeros(B, **i32), torch.zeros(2, **i32)
+        self.tail_src, self.tail_dst = torch.full((B,), -1, **i32), torch.full((B,), -1, **i32)
+        self.ws_bytes = dspark_pages_workspace_size(B, p.cache.num_pages)
+        if self.ws_bytes == 0:
+            raise ValueError("shape outside the library's limits")
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        dspark_workspace_init(self.workspace.data_ptr(), self.ws_bytes, stream)
+        p.B_in, p.B, p.max_pages, p.sinks = B_in, B, max_pages, sinks
+        for name in ("table_out", "granted_len", "tail_src", "tail_dst", "totals"):
+            setattr(p, name, getattr(self, name).data_ptr())
+        p.workspace, p.workspace_bytes = self.workspace.data_ptr(), self.ws_bytes
+        self._keep = {"cache": cache}
+
+    def bind(self, table_in, keep_len, want_len, parent=None, first_pos=None, held=None) -> "PageBuffers":
+        """Point the struct at device int32 tensors: table_in [B_in, max_pages]; keep_len, want_len,
+        parent, first_pos [B]; held [num_pages]."""
+        p = self.pages
+        for name, t, n in (("table_in", table_in, p.B_in * p.max_pages), ("keep_len", keep_len, p.B),
+                           ("want_len", want_len, p.B)):
+            _device_array(t, name, "int32", n)
+            setattr(p, name, _ptr(t))
+        for name, t, n in (("parent", parent, p.B), ("first_pos", first_pos, p.B),
+                           ("held", held, p.cache.num_pages)):
+            _device_array(t, name, "int32", n, optional=True)
+            setattr(p, name, _ptr(t))
+        self._keep.update(table_in=table_in, keep_len=keep_len, want_len=want_len, parent=parent,
+                          first_pos=first_pos, held=held)
+        return self
+
+    def device_status(self, stream=None) -> int:
+        return dspark_read_device_status(self.workspace.data_ptr(), stream)
+
+
+def _layer_strides(t) -> tuple:
+    """Strides of a [layers, pages, slots, heads, D] view, as :func:`_cache_strides` has them."""
+    inner = _cache_strides(t[0])
+    return ((t.stride(0) if t.shape[0] > 1 else max(t.shape[1] * inner[0], 1)),) + inner
 
 
 def _device_view(t, name: str, dtype, shape) -> None:

@@ -11,6 +11,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "attn.cuh"
+#include "cache.cuh"
 #include "dspark_internal.cuh"
 #include "sts_fit.cuh"
 
@@ -690,20 +691,8 @@ dspark_status check_attn_softmax(const dspark_attn *a, const char *fn) {
     return DSPARK_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t dspark_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t D, int32_t q_max) {
-    if (Hq < 1 || Hq > DSPARK_MAX_HEADS || Hkv < 1 || Hkv > Hq || Hq % Hkv || (D != 64 && D != 128) ||
-        q_max < 1)
-        return 0;
-    return dspark::attn_workspace_bytes(Hq, Hkv, D, q_max);
-}
-
-dspark_status dspark_rope_append(const dspark_attn *a, dspark_stream_t stream) {
-    NvtxRange range("dspark_rope_append");
-    const char *fn = "dspark_rope_append";
+dspark_status rope_append(const dspark_attn *a, bool tree, const char *fn, dspark_stream_t stream) {
+    NvtxRange range(fn);
     dspark_status st = check_attn(a, fn);
     if (st) return st;
     if (a->rot_dim < 0 || a->rot_dim > a->D || a->rot_dim % 16)
@@ -714,6 +703,7 @@ dspark_status dspark_rope_append(const dspark_attn *a, dspark_stream_t stream) {
     if (!a->k != !a->v) return fail(DSPARK_EINVAL, "%s: one of k and v is NULL", fn);
     REQUIRE(a->row_req);
     REQUIRE(a->packed_pos);
+    if (tree) REQUIRE(a->row_off);
     if (a->rot_dim > 0) REQUIRE(a->rope_freq);
     if (a->rot_dim > 0) REQUIRE_ALIGNED(a->rope_freq, 8);
     if (a->q) {
@@ -734,18 +724,20 @@ dspark_status dspark_rope_append(const dspark_attn *a, dspark_stream_t stream) {
     if (a->k && (st = check_in_place(a, a->k, a->k_rot, a->k_stride, a->Hkv, "k", fn))) return st;
     DeviceInfo *dev;
     if ((st = device_info(&dev))) return st;
-    cudaError_t e = dspark::launch_rope_append(*a, dev->sms, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e = dspark::launch_rope_append(*a, tree, dev->sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rope_append_kernel launch");
     return DSPARK_OK;
 }
 
-dspark_status dspark_step_attention(const dspark_attn *a, dspark_stream_t stream) {
-    NvtxRange range("dspark_step_attention");
-    const char *fn = "dspark_step_attention";
+// The three calls over the paged cache.  tree: with row_seen.
+dspark_status step_attention(const dspark_attn *a, const uint64_t *row_seen, bool tree, int32_t sinks, const char *fn,
+                             dspark_stream_t stream) {
+    NvtxRange range(fn);
     dspark_status st = check_attn(a, fn);
     if (st) return st;
-    if (a->q_max > DSPARK_MAX_STEP_ROWS)
-        return fail(DSPARK_EINVAL, "%s: q_max=%d outside [1, %d]", fn, a->q_max, DSPARK_MAX_STEP_ROWS);
+    const int most = tree ? DSPARK_MAX_TREE_ROWS : DSPARK_MAX_STEP_ROWS;
+    if (a->q_max > most) return fail(DSPARK_EINVAL, "%s: q_max=%d outside [1, %d]", fn, a->q_max, most);
+    if (sinks < 0) return fail(DSPARK_EINVAL, "%s: sinks=%d < 0", fn, sinks);
     if (a->Hq / a->Hkv > DSPARK_MAX_STEP_GROUP)
         return fail(DSPARK_EINVAL, "%s: %d query heads per cached head, at most %d", fn,
                     a->Hq / a->Hkv, DSPARK_MAX_STEP_GROUP);
@@ -759,19 +751,26 @@ dspark_status dspark_step_attention(const dspark_attn *a, dspark_stream_t stream
     if (!dspark::step_list_fits(*a))
         return fail(DSPARK_EINVAL, "%s: B=%d Hkv=%d max_pages=%d is too large a batch", fn, a->B, a->Hkv,
                     a->max_pages);
+    if (tree) {
+        REQUIRE(row_seen);
+        REQUIRE_ALIGNED(row_seen, 8);
+        if (a->window > 0) REQUIRE(a->packed_pos);
+    }
     DeviceInfo *dev;
     if ((st = device_info(&dev))) return st;
-    cudaError_t e = dspark::launch_step_attention(*a, dev->sms, g_wait_ns.load(),
-                                                  reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e =
+        tree || (sinks > 0 && a->window > 0)
+            ? dspark::launch_seen_attention(*a, row_seen, sinks, true, reinterpret_cast<cudaStream_t>(stream))
+            : dspark::launch_step_attention(*a, dev->sms, g_wait_ns.load(), reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "step_attention_kernel launch");
     return DSPARK_OK;
 }
 
-dspark_status dspark_prompt_attention(const dspark_attn *a, dspark_stream_t stream) {
-    NvtxRange range("dspark_prompt_attention");
-    const char *fn = "dspark_prompt_attention";
+dspark_status prompt_attention(const dspark_attn *a, int32_t sinks, const char *fn, dspark_stream_t stream) {
+    NvtxRange range(fn);
     dspark_status st = check_attn(a, fn);
     if (st) return st;
+    if (sinks < 0) return fail(DSPARK_EINVAL, "%s: sinks=%d < 0", fn, sinks);
     if (a->B == 0 || a->rows == 0) return DSPARK_OK;
     if ((st = check_attn_softmax(a, fn))) return st;
     REQUIRE(a->k_rot);
@@ -781,9 +780,189 @@ dspark_status dspark_prompt_attention(const dspark_attn *a, dspark_stream_t stre
     if ((st = check_row_stride(a->v_stride, a->Hkv, a->D, "v_stride", fn))) return st;
     DeviceInfo *dev;
     if ((st = device_info(&dev))) return st;
-    cudaError_t e = dspark::launch_prompt_attention(*a, dev->sms, g_wait_ns.load(),
-                                                    reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e =
+        sinks > 0 && a->window > 0
+            ? dspark::launch_seen_attention(*a, nullptr, sinks, false, reinterpret_cast<cudaStream_t>(stream))
+            : dspark::launch_prompt_attention(*a, dev->sms, g_wait_ns.load(), reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "prompt_attention_kernel launch");
+    return DSPARK_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Drafted trees and the caches of all layers (verify_tree.cu, commit_path.cu,
+// update_pages.cu).
+// ---------------------------------------------------------------------------
+dspark_status check_batch(int32_t B, const char *what, const char *fn) {
+    if (B < 0 || B > DSPARK_MAX_B) return fail(DSPARK_EINVAL, "%s: %s=%d outside [0, %d]", fn, what, B, DSPARK_MAX_B);
+    return DSPARK_OK;
+}
+
+dspark_status check_scratch(const void *workspace, size_t bytes, size_t need, const char *fn) {
+    if (!workspace) return fail(DSPARK_EWORKSPACE, "%s: workspace is NULL", fn);
+    if (!aligned(workspace, 256)) return fail(DSPARK_EWORKSPACE, "%s: workspace is not 256-byte aligned", fn);
+    if (bytes < need) return fail(DSPARK_EWORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, bytes, need);
+    return DSPARK_OK;
+}
+
+dspark_status check_layers(const dspark_cache *c, int32_t max_pages, bool data, const char *fn) {
+    if (c->page_size < 1 || c->page_size > 65536)
+        return fail(DSPARK_EINVAL, "%s: page_size=%d outside [1, 65536]", fn, c->page_size);
+    if (c->num_pages < 1 || max_pages < 1)
+        return fail(DSPARK_EINVAL, "%s: num_pages=%d, max_pages=%d: each is >= 1", fn, c->num_pages, max_pages);
+    if ((long long)max_pages * c->page_size > INT32_MAX - 65536)
+        return fail(DSPARK_EINVAL, "%s: max_pages=%d pages of %d positions pass 32 bits", fn, max_pages, c->page_size);
+    if (!data) return DSPARK_OK;
+    if (c->layers < 1 || c->layers > DSPARK_MAX_LAYERS)
+        return fail(DSPARK_EINVAL, "%s: layers=%d outside [1, %d]", fn, c->layers, DSPARK_MAX_LAYERS);
+    if (c->Hkv < 1 || c->Hkv > DSPARK_MAX_HEADS)
+        return fail(DSPARK_EINVAL, "%s: Hkv=%d outside [1, %d]", fn, c->Hkv, DSPARK_MAX_HEADS);
+    if (c->D < 8 || c->D > DSPARK_MAX_HEAD_SIZE || c->D % 8)
+        return fail(DSPARK_EINVAL, "%s: D=%d is not a multiple of 8 in [8, %d]", fn, c->D, DSPARK_MAX_HEAD_SIZE);
+    if (c->dtype != DSPARK_BF16) return fail(DSPARK_EDTYPE, "%s: dtype=%d", fn, c->dtype);
+    REQUIRE(c->k_cache);
+    REQUIRE(c->v_cache);
+    REQUIRE_ALIGNED(c->k_cache, 16);
+    REQUIRE_ALIGNED(c->v_cache, 16);
+    if (c->layer_stride <= 0 || c->page_stride <= 0 || c->slot_stride <= 0 || c->head_stride <= 0)
+        return fail(DSPARK_EINVAL, "%s: cache strides must be > 0", fn);
+    if (c->layer_stride % 8 || c->page_stride % 8 || c->slot_stride % 8 || c->head_stride % 8)
+        return fail(DSPARK_EALIGN, "%s: a cache stride is not a multiple of 8 elements", fn);
+    return DSPARK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dspark_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t D, int32_t q_max) {
+    if (Hq < 1 || Hq > DSPARK_MAX_HEADS || Hkv < 1 || Hkv > Hq || Hq % Hkv || (D != 64 && D != 128) ||
+        q_max < 1)
+        return 0;
+    return dspark::attn_workspace_bytes(Hq, Hkv, D, q_max);
+}
+
+dspark_status dspark_rope_append(const dspark_attn *a, dspark_stream_t stream) {
+    return rope_append(a, false, "dspark_rope_append", stream);
+}
+
+dspark_status dspark_rope_append_tree(const dspark_attn *a, dspark_stream_t stream) {
+    return rope_append(a, true, "dspark_rope_append_tree", stream);
+}
+
+dspark_status dspark_step_attention(const dspark_attn *a, dspark_stream_t stream) {
+    return step_attention(a, nullptr, false, 0, "dspark_step_attention", stream);
+}
+
+dspark_status dspark_step_attention_sinks(const dspark_attn *a, int32_t sinks, dspark_stream_t stream) {
+    return step_attention(a, nullptr, false, sinks, "dspark_step_attention_sinks", stream);
+}
+
+dspark_status dspark_step_attention_tree(const dspark_attn *a, const uint64_t *row_seen, int32_t sinks,
+                                         dspark_stream_t stream) {
+    return step_attention(a, row_seen, true, sinks, "dspark_step_attention_tree", stream);
+}
+
+dspark_status dspark_prompt_attention(const dspark_attn *a, dspark_stream_t stream) {
+    return prompt_attention(a, 0, "dspark_prompt_attention", stream);
+}
+
+dspark_status dspark_prompt_attention_sinks(const dspark_attn *a, int32_t sinks, dspark_stream_t stream) {
+    return prompt_attention(a, sinks, "dspark_prompt_attention_sinks", stream);
+}
+
+size_t dspark_tree_workspace_size(int32_t B, int32_t rows, int32_t V) {
+    if (B < 0 || B > DSPARK_MAX_B || rows < 0 || rows > DSPARK_MAX_ROWS || V < 1 || V > DSPARK_MAX_V) return 0;
+    return dspark::tree_workspace_bytes(B, rows, V);
+}
+
+dspark_status dspark_verify_tree(const dspark_tree *t, dspark_stream_t stream) {
+    const char *fn = "dspark_verify_tree";
+    NvtxRange range(fn);
+    if (!t) return fail(DSPARK_EINVAL, "%s: tree is NULL", fn);
+    dspark_status st = check_batch(t->B, "B", fn);
+    if (st) return st;
+    if (t->rows < 0 || t->rows > DSPARK_MAX_ROWS)
+        return fail(DSPARK_EINVAL, "%s: rows=%d outside [0, %d]", fn, t->rows, DSPARK_MAX_ROWS);
+    if (t->q_max < 1 || t->q_max > DSPARK_MAX_TREE_ROWS)
+        return fail(DSPARK_EINVAL, "%s: q_max=%d outside [1, %d]", fn, t->q_max, DSPARK_MAX_TREE_ROWS);
+    if (t->V < 1 || t->V > DSPARK_MAX_V) return fail(DSPARK_EINVAL, "%s: V=%d outside [1, %d]", fn, t->V, DSPARK_MAX_V);
+    if (t->logit_dtype != DSPARK_F32 && t->logit_dtype != DSPARK_BF16)
+        return fail(DSPARK_EDTYPE, "%s: logit_dtype=%d", fn, t->logit_dtype);
+    if (t->B == 0) return DSPARK_OK;
+    REQUIRE(t->row_off);
+    REQUIRE(t->accept_len);
+    REQUIRE(t->num_emitted);
+    REQUIRE(t->path);
+    REQUIRE(t->out_tokens);
+    if (t->rows > 0) {
+        REQUIRE(t->target_logits);
+        REQUIRE(t->parent);
+        REQUIRE(t->packed_ids);
+    }
+    REQUIRE_ALIGNED(t->target_logits, 16);
+    if (t->V * dtype_size(t->logit_dtype) % 16)
+        return fail(DSPARK_EALIGN, "%s: rows of V=%d logits are not a multiple of 16 bytes", fn, t->V);
+    if ((st = check_scratch(t->workspace, t->workspace_bytes, dspark::tree_workspace_bytes(t->B, t->rows, t->V), fn)))
+        return st;
+    DeviceInfo *dev;
+    if ((st = device_info(&dev))) return st;
+    cudaError_t e = dspark::launch_verify_tree(*t, dev->sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "verify_tree_kernel launch");
+    return DSPARK_OK;
+}
+
+dspark_status dspark_commit_path(const dspark_cache *c, int32_t B, int32_t q_max, int32_t max_pages,
+                                 const int32_t *block_table, const int32_t *seq_lens, const int32_t *path,
+                                 dspark_stream_t stream) {
+    const char *fn = "dspark_commit_path";
+    NvtxRange range(fn);
+    if (!c) return fail(DSPARK_EINVAL, "%s: cache is NULL", fn);
+    dspark_status st = check_batch(B, "B", fn);
+    if (st) return st;
+    if (q_max < 1 || q_max > DSPARK_MAX_STEP_ROWS)
+        return fail(DSPARK_EINVAL, "%s: q_max=%d outside [1, %d]", fn, q_max, DSPARK_MAX_STEP_ROWS);
+    if ((st = check_layers(c, max_pages, true, fn))) return st;
+    if (B == 0) return DSPARK_OK;
+    REQUIRE(block_table);
+    REQUIRE(path);
+    DeviceInfo *dev;
+    if ((st = device_info(&dev))) return st;
+    cudaError_t e = dspark::launch_commit_path(*c, B, q_max, max_pages, block_table, seq_lens, path, dev->sms,
+                                               reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "commit_path_kernel launch");
+    return DSPARK_OK;
+}
+
+size_t dspark_pages_workspace_size(int32_t B, int32_t num_pages) {
+    if (B < 0 || B > DSPARK_MAX_B || num_pages < 1) return 0;
+    return dspark::pages_workspace_bytes(B, num_pages);
+}
+
+dspark_status dspark_update_pages(const dspark_pages *p, dspark_stream_t stream) {
+    const char *fn = "dspark_update_pages";
+    NvtxRange range(fn);
+    if (!p) return fail(DSPARK_EINVAL, "%s: pages is NULL", fn);
+    dspark_status st = check_batch(p->B, "B", fn);
+    if (st || (st = check_batch(p->B_in, "B_in", fn))) return st;
+    if (p->sinks < 0) return fail(DSPARK_EINVAL, "%s: sinks=%d < 0", fn, p->sinks);
+    if ((st = check_layers(&p->cache, p->max_pages, p->cache.k_cache || p->cache.v_cache, fn))) return st;
+    if (p->B == 0) return DSPARK_OK;
+    if (p->B_in > 0) REQUIRE(p->table_in);
+    REQUIRE(p->keep_len);
+    REQUIRE(p->want_len);
+    REQUIRE(p->table_out);
+    REQUIRE(p->granted_len);
+    REQUIRE(p->tail_src);
+    REQUIRE(p->tail_dst);
+    REQUIRE(p->totals);
+    if (p->table_in == p->table_out) return fail(DSPARK_EINVAL, "%s: table_out is table_in", fn);
+    if ((st = check_scratch(p->workspace, p->workspace_bytes,
+                            dspark::pages_workspace_bytes(p->B, p->cache.num_pages), fn)))
+        return st;
+    DeviceInfo *dev;
+    if ((st = device_info(&dev))) return st;
+    cudaError_t e = dspark::launch_update_pages(*p, dev->sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "update_pages_kernel launch");
     return DSPARK_OK;
 }
 

@@ -20,8 +20,12 @@ bool step_strides_ok(const dspark_attn &a);
 // Is the list of a step's tiles counted in 32 bits?
 bool step_list_fits(const dspark_attn &a);
 
-cudaError_t launch_rope_append(const dspark_attn &a, int sms, cudaStream_t s);
+// tree: entry j of a request goes to position seq_lens + j, whatever its own.
+cudaError_t launch_rope_append(const dspark_attn &a, bool tree, int sms, cudaStream_t s);
 cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_ns, cudaStream_t s);
+// A tree's rows (row_seen) or a window with sinks, over the cache or packed prompts.
+cudaError_t launch_seen_attention(const dspark_attn &a, const uint64_t *row_seen, int sinks, bool paged,
+                                  cudaStream_t s);
 cudaError_t launch_prompt_attention(const dspark_attn &a, int sms, uint64_t wait_ns, cudaStream_t s);
 
 }  // namespace dspark

@@ -1,0 +1,96 @@
+// commit_path.cu -- the entries of an accepted path move to their places, in
+// the caches of all layers.
+//
+// Position s + j receives what s + path[j] held, path[j] >= j.  So no entry is
+// written before the ones in front of it have been read, whichever order
+// the path has: place j is the source of places <= j only.  A thread that walks the
+// places in ascending order, a batch of loads before the batch's stores,
+// needs no barrier.
+//
+// Bound: bytes, each moved entry read and written once.
+#include "cache.cuh"
+#include "dspark_internal.cuh"
+#include "tcgen05.cuh"
+
+namespace dspark {
+namespace {
+
+constexpr int kThreadsCommit = 256;
+constexpr int kInFlight = 8;  // entries that a thread has asked for before it stores
+
+struct CommitArgs {
+    int B, q_max, max_pages, layers, heads, chunks, page_size, num_pages;
+    int64_t layer_stride, page_stride, slot_stride, head_stride;
+    uint16_t *cache[2];
+    const int32_t *block_table, *seq_lens, *path;
+};
+
+// A CTA takes one request in one layer.
+__global__ void __launch_bounds__(kThreadsCommit) commit_path_kernel(const CommitArgs A) {
+    __shared__ int64_t from[DSPARK_MAX_STEP_ROWS + 7], to[DSPARK_MAX_STEP_ROWS + 7];
+    __shared__ int moves;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int b = blockIdx.x / A.layers, layer = blockIdx.x - b * A.layers, tid = threadIdx.x;
+    if (tid < 32) {
+        // the moves, in ascending places
+        const int32_t *path = A.path + int64_t(b) * A.q_max, *table = A.block_table + int64_t(b) * A.max_pages;
+        const int64_t start = A.seq_lens ? max(A.seq_lens[b], 0) : 0;
+        auto entry = [&](int64_t pos) -> int64_t {
+            const int64_t i = pos / A.page_size;
+            if (i >= A.max_pages) return -1;
+            const int page = table[i];
+            if (page < 0 || page >= A.num_pages) return -1;
+            return page * A.page_stride + (pos - i * A.page_size) * A.slot_stride;
+        };
+        int n = 0;
+        bool ended = false;
+        for (int j0 = 0; j0 < A.q_max && !ended; j0 += 32) {
+            const int j = j0 + tid, x = j < A.q_max ? path[j] : -1;
+            const uint32_t stop = __ballot_sync(0xffffffffu, x < 0);
+            const bool before = !(stop & ((2u << tid) - 1u));  // no negative one up to here
+            int64_t src = -1, dst = -1;
+            if (before && x > j) {
+                src = entry(start + x);
+                dst = entry(start + j);
+            }
+            const uint32_t go = __ballot_sync(0xffffffffu, src >= 0 && dst >= 0);
+            if (src >= 0 && dst >= 0) {
+                const int at = n + __popc(go & ((1u << tid) - 1u));
+                from[at] = src;
+                to[at] = dst;
+            }
+            n += __popc(go);
+            ended = stop != 0;
+        }
+        if (tid == 0) moves = n;
+    }
+    __syncthreads();
+    const int n = moves, per = A.heads * A.chunks;
+    for (int x = tid; n > 0 && x < 2 * per; x += kThreadsCommit) {
+        const int kv = x >= per, in = x - kv * per, head = in / A.chunks;
+        uint16_t *const base = A.cache[kv] + layer * A.layer_stride + head * A.head_stride + (in - head * A.chunks) * 8;
+        for (int m0 = 0; m0 < n; m0 += kInFlight) {
+            uint4 v[kInFlight];
+#pragma unroll
+            for (int m = 0; m < kInFlight; ++m)
+                if (m0 + m < n) v[m] = *reinterpret_cast<const uint4 *>(base + from[m0 + m]);
+#pragma unroll
+            for (int m = 0; m < kInFlight; ++m)
+                if (m0 + m < n) *reinterpret_cast<uint4 *>(base + to[m0 + m]) = v[m];
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_commit_path(const dspark_cache &c, int B, int q_max, int max_pages, const int32_t *block_table,
+                               const int32_t *seq_lens, const int32_t *path, int sms, cudaStream_t s) {
+    const CommitArgs A{B, q_max, max_pages, c.layers, c.Hkv, c.D / 8, c.page_size, c.num_pages,
+                       c.layer_stride, c.page_stride, c.slot_stride, c.head_stride,
+                       {static_cast<uint16_t *>(c.k_cache), static_cast<uint16_t *>(c.v_cache)},
+                       block_table, seq_lens, path};
+    return launch_overlapped(commit_path_kernel, B * c.layers, kThreadsCommit, 0, s, A);
+}
+
+}  // namespace dspark

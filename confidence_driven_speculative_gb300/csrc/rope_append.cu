@@ -32,7 +32,7 @@ struct RopeArgs {
     int64_t q_stride, k_stride, v_stride, page_stride, slot_stride, head_stride;
     const uint16_t *q, *k, *v;
     uint16_t *q_rot, *k_rot, *k_cache, *v_cache;
-    const int32_t *row_req, *packed_pos, *block_table;
+    const int32_t *row_req, *packed_pos, *block_table, *row_off, *seq_lens;
     const uint64_t *freq;
 };
 
@@ -65,7 +65,8 @@ __device__ __forceinline__ void rotate(uint4 &a, uint4 &b, const float (&c)[8], 
     }
 }
 
-template <int D, bool kInterleaved>
+// kTree: the entry's place is seq_lens[b] + the row's index, and not its position.
+template <int D, bool kInterleaved, bool kTree>
 __device__ __forceinline__ void append_row(const RopeArgs &A, int r, int b, int pos) {
     constexpr int kLanes = D / 16;  // threads of a head, two 16-byte chunks each
     constexpr int kHeads = kRopeThreads / kLanes;
@@ -77,11 +78,17 @@ __device__ __forceinline__ void append_row(const RopeArgs &A, int r, int b, int 
     const bool turns = c < rc;
     int e0 = 16 * c, e1 = 16 * c + 8;
     if (turns && !kInterleaved) { e0 = 8 * c; e1 = 8 * c + A.rot_dim / 2; }
-    const int page_i = pos / A.page_size;
+    int place = pos;
+    if (kTree) {
+        // far past any table, where nothing is stored, stays in 32 bits
+        place = (A.seq_lens ? min(max(A.seq_lens[b], 0), INT32_MAX - DSPARK_MAX_ROWS) : 0) + r - A.row_off[b];
+        if (place < 0) return;
+    }
+    const int page_i = place / A.page_size;
     int page = -1;
     if (A.k && page_i < A.max_pages) page = A.block_table[(int64_t)b * A.max_pages + page_i];
     const bool stored = page >= 0 && page < A.num_pages;
-    const int64_t entry = stored ? page * A.page_stride + (pos % A.page_size) * A.slot_stride : 0;
+    const int64_t entry = stored ? page * A.page_stride + (place % A.page_size) * A.slot_stride : 0;
 
     const int q_heads = A.q ? A.Hq : 0, kv_heads = A.k ? A.Hkv : 0;
     const int slots = q_heads + 2 * kv_heads;
@@ -132,16 +139,16 @@ __device__ __forceinline__ void append_row(const RopeArgs &A, int r, int b, int 
 }
 
 // A CTA for each row slot.
-template <int D, bool kInterleaved>
+template <int D, bool kInterleaved, bool kTree>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs A) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    append_row<D, kInterleaved>(A, blockIdx.x, A.row_req[blockIdx.x], A.packed_pos[blockIdx.x]);
+    append_row<D, kInterleaved, kTree>(A, blockIdx.x, A.row_req[blockIdx.x], A.packed_pos[blockIdx.x]);
 }
 
 // The CTAs walk the row slots; the next one's place is asked for before this
 // one's work.
-template <int D, bool kInterleaved>
+template <int D, bool kInterleaved, bool kTree>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_walk_kernel(const RopeArgs A) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -153,23 +160,29 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_walk_kernel(const Ro
             b_next = A.row_req[next];
             pos_next = A.packed_pos[next];
         }
-        append_row<D, kInterleaved>(A, r, b, pos);
+        append_row<D, kInterleaved, kTree>(A, r, b, pos);
         r = next;
         b = b_next;
         pos = pos_next;
     }
 }
 
+template <int D, bool kInterleaved>
+auto *rope_kernel(bool walk, bool tree) {
+    return walk ? (tree ? rope_append_walk_kernel<D, kInterleaved, true> : rope_append_walk_kernel<D, kInterleaved, false>)
+                : (tree ? rope_append_kernel<D, kInterleaved, true> : rope_append_kernel<D, kInterleaved, false>);
+}
+
 }  // namespace
 
-cudaError_t launch_rope_append(const dspark_attn &a, int sms, cudaStream_t s) {
+cudaError_t launch_rope_append(const dspark_attn &a, bool tree, int sms, cudaStream_t s) {
     RopeArgs A{a.B, a.rows, a.Hq, a.Hkv, a.page_size, a.num_pages, a.max_pages, a.rot_dim,
                a.q_stride, a.k_stride, a.v_stride, a.page_stride, a.slot_stride, a.head_stride,
                static_cast<const uint16_t *>(a.q), static_cast<const uint16_t *>(a.k),
                static_cast<const uint16_t *>(a.v), static_cast<uint16_t *>(a.q_rot),
                static_cast<uint16_t *>(a.k_rot), static_cast<uint16_t *>(a.k_cache),
                static_cast<uint16_t *>(a.v_cache), a.row_req, a.packed_pos, a.block_table,
-               a.rope_freq};
+               a.row_off, a.seq_lens, a.rope_freq};
     if (!a.k) A.page_size = 1;  // not checked, not used
     // Walking pays where most slots are padding, as in a batch of steps: a CTA
     // that finds an empty slot costs a launch, a walker a load that is already
@@ -179,11 +192,8 @@ cudaError_t launch_rope_append(const dspark_attn &a, int sms, cudaStream_t s) {
     // longer the walk (32768: 134 against 150), so long lists keep a CTA a slot.
     const int walkers = 14 * sms;
     const bool walk = a.rows > walkers && a.rows <= 4 * walkers;
-    auto *kernel =
-        walk ? (a.D == 128 ? (a.interleaved ? rope_append_walk_kernel<128, true> : rope_append_walk_kernel<128, false>)
-                           : (a.interleaved ? rope_append_walk_kernel<64, true> : rope_append_walk_kernel<64, false>))
-             : (a.D == 128 ? (a.interleaved ? rope_append_kernel<128, true> : rope_append_kernel<128, false>)
-                           : (a.interleaved ? rope_append_kernel<64, true> : rope_append_kernel<64, false>));
+    auto *kernel = a.D == 128 ? (a.interleaved ? rope_kernel<128, true>(walk, tree) : rope_kernel<128, false>(walk, tree))
+                              : (a.interleaved ? rope_kernel<64, true>(walk, tree) : rope_kernel<64, false>(walk, tree));
     return launch_overlapped(kernel, walk ? walkers : a.rows, kRopeThreads, 0, s, A);
 }
 

@@ -16,6 +16,10 @@
  * dspark_score_compact is the first two calls in one kernel launch, with
  * the same outputs.
  *
+ * A tree of drafts in place of the block: dspark_verify_tree, with
+ * dspark_rope_append_tree, dspark_step_attention_tree and dspark_commit_path
+ * (further down).  dspark_update_pages keeps the paged cache's books.
+ *
  * Variants: dspark_score_entropy scores drafts by the entropy of their
  * distribution instead of the head; dspark_verify_cap_accept is the audit arm
  * that verifies the full block and commits the scheduled window;
@@ -444,6 +448,219 @@ dspark_status dspark_step_attention(const dspark_attn *attn, dspark_stream_t str
  * Reads q_rot, k_rot, v, row_off.  Writes out rows row_off[b] .. row_off[b+1].
  */
 dspark_status dspark_prompt_attention(const dspark_attn *attn, dspark_stream_t stream);
+
+/* ===========================================================================
+ * Windows with sinks.
+ *
+ * A layer with a sliding window whose first `sinks` positions stay visible:
+ * a row at position p sees key t <= p iff window = 0, or t > p - window, or
+ * t < sinks.  With sinks = 0 or window = 0 the calls are
+ * dspark_step_attention and dspark_prompt_attention.  Pages between the
+ * sinks and the window are not needed: their table entries may hold anything
+ * (dspark_update_pages leaves -1 there).  sinks < 0 is DSPARK_EINVAL;
+ * everything else, workspace included, as for the calls without sinks.
+ * =========================================================================== */
+dspark_status dspark_step_attention_sinks(const dspark_attn *attn, int32_t sinks,
+                                          dspark_stream_t stream);
+dspark_status dspark_prompt_attention_sinks(const dspark_attn *attn, int32_t sinks,
+                                            dspark_stream_t stream);
+
+/* ===========================================================================
+ * Drafted trees.
+ *
+ * A request's rows are a tree: row 0 is the root (the last committed token),
+ * every other row a draft that continues its parent's row.  Row j sits at
+ * position seq_lens[b] + depth(j) (its packed_pos; that turns it), but its
+ * cache entry is seq_lens[b] + j, a place of its own: siblings share a
+ * position.  One step on one stream, seq_lens being the cached length before
+ * it:
+ *
+ *   dspark_rope_append_tree     every layer: the rows into the cache;
+ *   dspark_step_attention_tree  every layer: the rows over the cache;
+ *   dspark_verify_tree          the path that the target goes;
+ *   dspark_commit_path          all layers: the path's entries to
+ *                               seq_lens[b] + 0, 1, 2, ..
+ * =========================================================================== */
+
+/* Rows of one request's tree. */
+#define DSPARK_MAX_TREE_ROWS 64
+
+/*
+ * dspark_rope_append for the rows of trees: row r = row_off[b] + j of request
+ * b turns by packed_pos[r], and its k and v go to position seq_lens[b] + j of
+ * the cache.  Reads row_off and seq_lens (NULL: 0) as well; otherwise as
+ * dspark_rope_append.
+ */
+dspark_status dspark_rope_append_tree(const dspark_attn *attn, dspark_stream_t stream);
+
+/*
+ * The rows of trees over the paged cache.  Row r = row_off[b] + j sees
+ *   - of the cached positions t < seq_lens[b]: all (window = 0), or those with
+ *     t > packed_pos[r] - window or t < sinks;
+ *   - of the rows' own entries seq_lens[b] + i, i < the request's rows: those
+ *     whose bit i of row_seen[r] is set, whatever the window.
+ * For a tree, row_seen[r] holds the row itself and its ancestors; any other
+ * set is as good, and a row that sees nothing gives zeros.
+ *
+ * row_seen: device uint64 [rows], 8-byte aligned.  packed_pos is read where
+ * window > 0 (values below seq_lens[b] count as seq_lens[b]).  q_max:
+ * 1..DSPARK_MAX_TREE_ROWS.  Everything else as dspark_step_attention.
+ */
+dspark_status dspark_step_attention_tree(const dspark_attn *attn, const uint64_t *row_seen,
+                                         int32_t sinks, dspark_stream_t stream);
+
+typedef struct dspark_tree {
+    /* ---- shapes ---------------------------------------------------------- */
+    int32_t B;           /* requests, 0..DSPARK_MAX_B (0: the call is a no-op) */
+    int32_t rows;        /* row slots of target_logits, parent and packed_ids, >= row_off[B];
+                            0..DSPARK_MAX_ROWS */
+    int32_t q_max;       /* bound of one request's rows, 1..DSPARK_MAX_TREE_ROWS; rows of a
+                            request past it are not there */
+    int32_t V;           /* vocabulary size, 1..DSPARK_MAX_V */
+    int32_t logit_dtype; /* dspark_dtype of target_logits */
+
+    /* ---- inputs (device, read only) -------------------------------------- */
+    const void *target_logits;  /* [rows, V]; rows as in the alignment convention.  -inf
+                                   marks masked ids */
+    const int32_t *row_off;     /* [B+1] request b owns rows row_off[b] .. row_off[b+1] */
+    const int32_t *parent;      /* [rows] index of the parent in the request, below the row's
+                                   own; another value: no parent, never reached.  Row 0's is
+                                   not read */
+    const int32_t *packed_ids;  /* [rows] token of each row; the root's is not read.  An id
+                                   outside [0, V) is always rejected */
+
+    /* ---- outputs (device, caller-allocated) ------------------------------ */
+    int32_t *accept_len;      /* [B] accepted drafts a_b */
+    int32_t *num_emitted;     /* [B] a_b + 1; 0 for a request without rows */
+    int32_t *path;            /* [B, q_max] accepted rows from the root (0) on, then -1 */
+    int32_t *out_tokens;      /* [B, q_max] tokens of the accepted drafts, then the target's
+                                 own after the last, then -1 */
+    int32_t *seq_lens_commit; /* [B] incremented by num_emitted in place, or NULL */
+
+    /* ---- scratch --------------------------------------------------------- */
+    void *workspace;        /* dspark_tree_workspace_size() bytes, under the workspace
+                               convention */
+    size_t workspace_bytes;
+} dspark_tree;
+
+/* Bytes of workspace that dspark_verify_tree needs.  0 outside the limits. */
+size_t dspark_tree_workspace_size(int32_t B, int32_t rows, int32_t V);
+
+/*
+ * The walk that the target goes down each tree: y_j = argmax of the target row
+ * at row j (the lowest id on ties); from the root on, the lowest child of the
+ * present row whose token is y of that row is accepted and becomes the present
+ * row; the walk ends where there is none, and emits y of its last row.
+ *
+ * This is the greedy rule.  For sampling at a temperature Tm, hand in
+ * logits / Tm plus independent standard Gumbel noise: y_j is then a draw from
+ * softmax(logits / Tm), and the tokens of the walk are those of sampling one
+ * by one.
+ *
+ * Rows that no walk comes to may be left unread.
+ */
+dspark_status dspark_verify_tree(const dspark_tree *tree, dspark_stream_t stream);
+
+/* ===========================================================================
+ * The paged caches of all layers.
+ * =========================================================================== */
+typedef struct dspark_cache {
+    int32_t layers;     /* 1..DSPARK_MAX_LAYERS */
+    int32_t Hkv;        /* heads, 1..DSPARK_MAX_HEADS */
+    int32_t D;          /* head size, a multiple of 8, 8..DSPARK_MAX_HEAD_SIZE */
+    int32_t dtype;      /* DSPARK_BF16 */
+    int32_t page_size;  /* positions per page, 1..65536 */
+    int32_t num_pages;  /* pages of each layer, >= 1 */
+    /* strides in elements, of both caches; multiples of 8.  Entry (layer, page,
+       slot, head) lies as in dspark_attn, with layer * layer_stride in front */
+    int64_t layer_stride, page_stride, slot_stride, head_stride;
+    void *k_cache, *v_cache; /* 16-byte aligned device memory */
+} dspark_cache;
+
+#define DSPARK_MAX_LAYERS 1024
+#define DSPARK_MAX_HEAD_SIZE 512
+
+/*
+ * An accepted path's entries move to their places: in all layers, k and v,
+ * position seq_lens[b] + j receives what position seq_lens[b] + path[b][j]
+ * held before the call, for the j in front of the first negative
+ * path[b][j].  An accepted row never lies in front of its place: where
+ * path[b][j] < j, the entry stays as it is.  An entry whose old or new position has no page
+ * stays as well.  Entries that no path names keep what they hold.
+ *
+ * block_table [B, max_pages], seq_lens [B] (the length before the verify; NULL:
+ * 0), path [B, q_max] (as dspark_verify_tree writes it): device memory, read
+ * only.  q_max: 1..DSPARK_MAX_STEP_ROWS.  A page that an entry moves to belongs
+ * to one request.  path may name rows past the request's own; the caller's
+ * pages say how far.
+ */
+dspark_status dspark_commit_path(const dspark_cache *cache, int32_t B, int32_t q_max,
+                                 int32_t max_pages, const int32_t *block_table,
+                                 const int32_t *seq_lens, const int32_t *path,
+                                 dspark_stream_t stream);
+
+typedef struct dspark_pages {
+    dspark_cache cache;  /* k_cache and v_cache NULL together: no entry is copied, the caller
+                            does it by tail_src and tail_dst */
+
+    /* ---- shapes ---------------------------------------------------------- */
+    int32_t B_in;        /* rows of table_in, 0..DSPARK_MAX_B */
+    int32_t B;           /* requests of the next step, 0..DSPARK_MAX_B */
+    int32_t max_pages;   /* columns of both tables, >= 1 */
+    int32_t sinks;       /* positions that first_pos does not drop, >= 0 */
+
+    /* ---- inputs (device, read only) -------------------------------------- */
+    const int32_t *table_in;  /* [B_in, max_pages] pages of the requests so far; an entry
+                                 outside [0, num_pages) is none */
+    const int32_t *parent;    /* [B] row of table_in that request b continues; outside
+                                 [0, B_in): it starts from nothing.  NULL: b itself */
+    const int32_t *keep_len;  /* [B] positions taken over from the parent */
+    const int32_t *want_len;  /* [B] positions that have memory afterwards; those from
+                                 keep_len[b] on are about to be written.  Less than keep_len
+                                 counts as keep_len */
+    const int32_t *first_pos; /* [B] or NULL (0): pages that lie in front of it in full and
+                                 begin at `sinks` or later are dropped */
+    const int32_t *held;      /* [num_pages] or NULL: pages with a nonzero word are not given
+                                 out and not written, whoever else names them */
+
+    /* ---- outputs (device, caller-allocated) ------------------------------ */
+    int32_t *table_out;   /* [B, max_pages], apart from table_in; -1 where there is no page */
+    int32_t *granted_len; /* [B] want_len, or where pages ran out the first position that
+                             has no memory to be written */
+    int32_t *tail_src;    /* [B] page whose first keep_len % page_size entries were copied */
+    int32_t *tail_dst;    /* [B] to this one, in all layers; -1 and -1 for none */
+    int32_t *totals;      /* [2] pages left free, and pages that were wanted but missing */
+
+    /* ---- scratch --------------------------------------------------------- */
+    void *workspace;        /* dspark_pages_workspace_size() bytes, under the workspace
+                               convention */
+    size_t workspace_bytes;
+} dspark_pages;
+
+/* Bytes of workspace that dspark_update_pages needs.  0 outside the limits. */
+size_t dspark_pages_workspace_size(int32_t B, int32_t num_pages);
+
+/*
+ * The pages of a batch's next step, in one call: requests go on, fork, start
+ * or end; pages are kept and shared, copied where two would write one, dropped
+ * where a window has left them, given out for growth, and freed.  No list of
+ * free pages is kept anywhere: a page is free when no row of table_out names
+ * it and it is not held.  So every request that is to live on is in the call.
+ *
+ * Request b takes over its parent's pages of the positions below keep_len[b],
+ * except dropped ones.  Where want_len[b] > keep_len[b] and keep_len[b] lies
+ * inside a page, that tail is about to be written: of the requests that would
+ * write one page, the lowest keeps it, unless it is held or some request
+ * names it without writing it, and the others get a page of their own with the
+ * tail's entries copied.  Then come the pages up to want_len[b], except those
+ * that first_pos drops.  The n-th page wanted, by request and by position, is
+ * the n-th lowest free one: the result does not depend on timing.  What
+ * runs out is missing from the end of that order; a tail that finds no page
+ * stays shared, and granted_len then is keep_len: it must not be written.
+ *
+ * A parent's row of table_in names each of its pages once.
+ */
+dspark_status dspark_update_pages(const dspark_pages *pages, dspark_stream_t stream);
 
 /*
  * Blocking read of the workspace's device status word (0 = healthy).  A

@@ -102,3 +102,44 @@ def attend(q, k, v, first_pos: int, scale: float, window: int = 0, valid=None):
             spread[j, h] = p @ np.abs(vv) / total
             ds[j, h] = scale * (np.abs(kk) @ np.abs(q[j, h])).max()
     return o, spread, ds
+
+
+def seen_step(first_pos: int, n: int, m: int, window: int = 0, sinks: int = 0, valid=None) -> np.ndarray:
+    """[n, m]: does row j, at position first_pos + j, see key t of 0..m-1?"""
+    pos, t = first_pos + np.arange(n)[:, None], np.arange(m)[None, :]
+    seen = t <= pos
+    if window > 0:
+        seen &= (t > pos - window) | (t < sinks)
+    return seen if valid is None else seen & valid[None, :]
+
+
+def seen_tree(start: int, words, pos, m: int, window: int = 0, sinks: int = 0, valid=None) -> np.ndarray:
+    """[n, m]: does row j of a tree (its word of seen rows, its position) see entry t of 0..m-1?  The
+    rows' own entries begin at ``start``."""
+    n, seen = len(words), np.zeros((len(words), m), bool)
+    for j in range(n):
+        for t in range(m):
+            if t < start:
+                seen[j, t] = window == 0 or t > max(int(pos[j]), start) - window or t < sinks
+            elif t - start < n:
+                seen[j, t] = int(words[j]) >> (t - start) & 1
+    return seen if valid is None else seen & valid[None, :]
+
+
+def attend_seen(q, k, v, seen, scale: float):
+    """:func:`attend` for rows that see the keys of ``seen`` [n, m]."""
+    n, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    o, spread, ds = np.zeros((n, Hq, D)), np.zeros((n, Hq, D)), np.zeros((n, Hq))
+    for j in range(n):
+        s = np.nonzero(seen[j])[0]
+        if len(s) == 0:
+            continue
+        for h in range(Hq):
+            kk, vv = k[s, h // G], v[s, h // G]
+            x = scale * (kk @ q[j, h])
+            p = np.exp(x - x.max())
+            o[j, h] = p @ vv / p.sum()
+            spread[j, h] = p @ np.abs(vv) / p.sum()
+            ds[j, h] = scale * (np.abs(kk) @ np.abs(q[j, h])).max()
+    return o, spread, ds
