@@ -758,10 +758,11 @@ dspark_status step_attention(const dspark_attn *a, const uint64_t *row_seen, boo
     }
     DeviceInfo *dev;
     if ((st = device_info(&dev))) return st;
-    cudaError_t e =
-        tree || (sinks > 0 && a->window > 0)
-            ? dspark::launch_seen_attention(*a, row_seen, sinks, true, reinterpret_cast<cudaStream_t>(stream))
-            : dspark::launch_step_attention(*a, dev->sms, g_wait_ns.load(), reinterpret_cast<cudaStream_t>(stream));
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const uint64_t ns = g_wait_ns.load();
+    cudaError_t e = tree ? dspark::launch_step_attention_tree(*a, row_seen, sinks, dev->sms, ns, cs)
+                    : sinks > 0 && a->window > 0 ? dspark::launch_step_attention_sinks(*a, sinks, dev->sms, ns, cs)
+                                                 : dspark::launch_step_attention(*a, dev->sms, ns, cs);
     if (e != cudaSuccess) return cuda_fail(e, "step_attention_kernel launch");
     return DSPARK_OK;
 }

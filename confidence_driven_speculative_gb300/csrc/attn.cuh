@@ -23,6 +23,10 @@ bool step_list_fits(const dspark_attn &a);
 // tree: entry j of a request goes to position seq_lens + j, whatever its own.
 cudaError_t launch_rope_append(const dspark_attn &a, bool tree, int sms, cudaStream_t s);
 cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_ns, cudaStream_t s);
+cudaError_t launch_step_attention_sinks(const dspark_attn &a, int sinks, int sms, uint64_t wait_ns, cudaStream_t s);
+cudaError_t launch_step_attention_tree(const dspark_attn &a, const uint64_t *row_seen, int sinks, int sms,
+                                       uint64_t wait_ns, cudaStream_t s);
+
 // A tree's rows (row_seen) or a window with sinks, over the cache or packed prompts.
 cudaError_t launch_seen_attention(const dspark_attn &a, const uint64_t *row_seen, int sinks, bool paged,
                                   cudaStream_t s);
