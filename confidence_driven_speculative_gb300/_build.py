@@ -21,7 +21,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "score_budget.cu", "compact.cu", "verify.cu", "verify_small.cu", "sts_fit.cu",
            "tensor_map.cu", "rope_append.cu", "step_attention.cu", "prompt_attention.cu",
            "step_attention_sinks.cu", "step_attention_tree.cu",
-           "seen_attention.cu", "verify_tree.cu", "commit_path.cu", "update_pages.cu"]
+           "prompt_attention_sinks.cu", "verify_tree.cu", "commit_path.cu", "update_pages.cu"]
 
 
 def nvcc() -> str:

@@ -781,10 +781,10 @@ dspark_status prompt_attention(const dspark_attn *a, int32_t sinks, const char *
     if ((st = check_row_stride(a->v_stride, a->Hkv, a->D, "v_stride", fn))) return st;
     DeviceInfo *dev;
     if ((st = device_info(&dev))) return st;
-    cudaError_t e =
-        sinks > 0 && a->window > 0
-            ? dspark::launch_seen_attention(*a, nullptr, sinks, false, reinterpret_cast<cudaStream_t>(stream))
-            : dspark::launch_prompt_attention(*a, dev->sms, g_wait_ns.load(), reinterpret_cast<cudaStream_t>(stream));
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const uint64_t ns = g_wait_ns.load();
+    cudaError_t e = sinks > 0 && a->window > 0 ? dspark::launch_prompt_attention_sinks(*a, sinks, dev->sms, ns, cs)
+                                               : dspark::launch_prompt_attention(*a, dev->sms, ns, cs);
     if (e != cudaSuccess) return cuda_fail(e, "prompt_attention_kernel launch");
     return DSPARK_OK;
 }

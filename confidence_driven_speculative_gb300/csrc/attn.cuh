@@ -27,9 +27,7 @@ cudaError_t launch_step_attention_sinks(const dspark_attn &a, int sinks, int sms
 cudaError_t launch_step_attention_tree(const dspark_attn &a, const uint64_t *row_seen, int sinks, int sms,
                                        uint64_t wait_ns, cudaStream_t s);
 
-// A tree's rows (row_seen) or a window with sinks, over the cache or packed prompts.
-cudaError_t launch_seen_attention(const dspark_attn &a, const uint64_t *row_seen, int sinks, bool paged,
-                                  cudaStream_t s);
 cudaError_t launch_prompt_attention(const dspark_attn &a, int sms, uint64_t wait_ns, cudaStream_t s);
+cudaError_t launch_prompt_attention_sinks(const dspark_attn &a, int sinks, int sms, uint64_t wait_ns, cudaStream_t s);
 
 }  // namespace dspark
