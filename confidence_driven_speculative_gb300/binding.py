@@ -312,11 +312,15 @@ def dspark_commit_path(cache: DsparkCache, block_table, seq_lens, path, stream=N
     """The accepted rows' entries move to their places, in all layers.  Device int32 tensors:
     ``block_table`` [B, max_pages], ``seq_lens`` [B] (the length before the verify) or None, ``path``
     [B, q_max] as dspark_verify_tree writes it."""
-    B, q_max = _rows_of(path, "path")
-    max_pages = _rows_of(block_table, "block_table", B)[1]
-    _device_array(seq_lens, "seq_lens", "int32", B, optional=True)
+    B, q_max = _matrix(path, "path")
+    rows, max_pages = _matrix(block_table, "block_table")
+    if rows != B:
+        raise ValueError(f"block_table must be [{B}, n], got {tuple(block_table.shape)}")
+    if seq_lens is not None:
+        _device_array(seq_lens, "seq_lens", "int32", B)
     rc = load().dspark_commit_path(ctypes.byref(cache), B, q_max, max_pages, block_table.data_ptr(),
-                                   _ptr(seq_lens), path.data_ptr(), _stream(stream))
+                                   None if seq_lens is None else seq_lens.data_ptr(), path.data_ptr(),
+                                   _stream(stream))
     if check and rc != DSPARK_OK:
         raise DsparkError(rc, "dspark_commit_path")
     return rc
@@ -412,7 +416,7 @@ def _device_array(t, name: str, dtype: str, numel: Optional[int] = None, optiona
             return
         raise ValueError(f"{name} is required")
     import torch
-    want = {"int32": torch.int32, "float32": torch.float32}[dtype]
+    want = torch.int32 if dtype == "int32" else torch.float32
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch tensor")
     if t.dtype != want:
@@ -439,12 +443,12 @@ def _device_words(t, name: str, numel: int) -> None:
         raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
 
 
-def _rows_of(t, name: str, rows: Optional[int] = None) -> tuple:
-    """Shape of a contiguous device int32 matrix (of ``rows`` rows, when given)."""
+def _matrix(t, name: str):
+    """Shape of a contiguous device int32 matrix."""
     _device_array(t, name, "int32")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} must be [{'B' if rows is None else rows}, n], got {tuple(t.shape)}")
-    return int(t.shape[0]), int(t.shape[1])
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {tuple(t.shape)}")
+    return t.shape
 
 
 class StepBuffers:

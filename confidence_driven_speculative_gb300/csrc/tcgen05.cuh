@@ -316,6 +316,24 @@ cudaError_t launch_overlapped(void (*kernel)(P...), int grid, int block, size_t 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The same in clusters of `cluster` CTAs.
+template <typename... P, typename... T>
+cudaError_t launch_clusters(void (*kernel)(P...), int grid, int block, int cluster, cudaStream_t s, const T &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Host: cuTensorMapEncodeTiled for bfloat16 with the 128-byte swizzle.
 cudaError_t encode_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
                        const uint64_t *strides_bytes, const uint32_t *box);

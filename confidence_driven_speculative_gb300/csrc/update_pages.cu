@@ -20,10 +20,9 @@
 namespace dspark {
 namespace {
 
-constexpr int kCluster = 8;
 constexpr int kThreadsPages = 1024;
-constexpr int kAll = kCluster * kThreadsPages;
-constexpr int kSeg = 128;               // entries of a table that a warp takes at once
+constexpr int kSeg = 256;               // entries of a table that a warp takes at once
+constexpr int kPages = 8;               // pages in a row that a thread looks at
 constexpr int kFull = 0x7fffffff;       // claim of a request that only reads
 constexpr int kWriters = 1 << 17;       // kWriters - b: claim of request b that writes
 
@@ -33,7 +32,7 @@ struct PagesArgs {
     int32_t *table_out, *granted_len, *tail_src, *tail_dst, *totals;
     int32_t *claim;   // [num_pages], 0 between calls
     int32_t *free_list;  // [num_pages]
-    int32_t *start;   // [B] rank of the request's first wanted page
+    int2 *start;      // [B] rank of the request's first wanted page, does its tail need one?
     int4 *copies;     // [B] source, destination, entries
     int32_t *n_copies;
 };
@@ -92,12 +91,13 @@ __device__ __forceinline__ int remote(const int *p, int rank) {
     return v;
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreadsPages, 1)
-update_pages_kernel(const PagesArgs A) {
+template <int kCtas>
+__global__ void __launch_bounds__(kThreadsPages, 1) update_pages_kernel(const PagesArgs A) {
+    constexpr int kAll = kCtas * kThreadsPages, kAllWarps = kAll / 32;
     __shared__ int warp_sum[2][32], cta_sum[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster_rank();
-    const int g = rank * kThreadsPages + tid, gw = g >> 5;
-    constexpr int kAllWarps = kAll / 32;
+    // Warps of one number lie in different CTAs, so that few requests keep all CTAs busy.
+    const int g = rank * kThreadsPages + tid, gw = warp * kCtas + rank;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -128,66 +128,103 @@ update_pages_kernel(const PagesArgs A) {
     cluster_sync();
 
     // ---- ranks of the wanted pages and of the free ones ---------------------
-    const int per = (A.B + kAll - 1) / kAll, per_page = (A.num_pages - 1) / kAll + 1;
-    const int b_lo = min(int64_t(g) * per, int64_t(A.B)), b_hi = min(b_lo + per, A.B);
-    const int p_lo = min(int64_t(g) * per_page, int64_t(A.num_pages));
-    const int p_hi = min(int64_t(p_lo) + per_page, int64_t(A.num_pages));
-    auto is_free = [&](int p) { return __ldcg(A.claim + p) == 0 && !(A.held && A.held[p]); };
+    // A thread counts the pages of `per` requests, and of every kAll * kPages
+    // pages kPages in a row.
+    const int per = (A.B + kAll - 1) / kAll;
+    const int b_lo = min(g * per, A.B), b_hi = min(b_lo + per, A.B);
     // Does request b's tail need a page of its own?
     auto shares = [&](int b, const Want &w) {
         if (w.tail < 0) return false;
         const int page = __ldcg(A.table_out + int64_t(b) * A.max_pages + w.tail);
         return page >= 0 && (__ldcg(A.claim + page) != kWriters - b || (A.held && A.held[page]));
     };
-    int sum[2] = {0, 0};
+    const int64_t chunk = int64_t(kAll) * kPages;
+    // Bits of the free ones of a thread's pages p .. p + kPages - 1; their claims go back to zero in `clear`.
+    auto free_bits = [&](int64_t p) {
+        uint32_t bits = 0;
+        if (p + kPages <= A.num_pages) {
+            int4 c[kPages / 4], h[kPages / 4];
+#pragma unroll
+            for (int k = 0; k < kPages / 4; ++k) {
+                c[k] = __ldcg(reinterpret_cast<const int4 *>(A.claim + p) + k);
+                h[k] = make_int4(0, 0, 0, 0);
+            }
+            if (A.held) {
+#pragma unroll
+                for (int k = 0; k < kPages; ++k) reinterpret_cast<int *>(h)[k] = A.held[p + k];
+            }
+#pragma unroll
+            for (int k = 0; k < kPages / 4; ++k) {
+                bits |= uint32_t((c[k].x | h[k].x) == 0) << (4 * k) | uint32_t((c[k].y | h[k].y) == 0) << (4 * k + 1) |
+                        uint32_t((c[k].z | h[k].z) == 0) << (4 * k + 2) | uint32_t((c[k].w | h[k].w) == 0) << (4 * k + 3);
+            }
+        } else {
+            for (int k = 0; k < kPages; ++k)
+                if (p + k < A.num_pages && __ldcg(A.claim + p + k) == 0 && !(A.held && A.held[p + k])) bits |= 1u << k;
+        }
+        return bits;
+    };
+    // Exclusive sums over the cluster's threads, and the totals.
+    auto scan = [&](const int (&mine)[2], int (&before)[2], int (&total)[2]) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            int x = mine[k];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) warp_sum[k][warp] = x;
+            before[k] = x - mine[k];
+        }
+        __syncthreads();
+        if (warp < 2) {
+            int x = warp_sum[warp][lane];
+            const int own = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            warp_sum[warp][lane] = x - own;
+            if (lane == 31) cta_sum[warp] = x;
+        }
+        cluster_sync();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int x = lane < kCtas ? remote(&cta_sum[k], lane) : 0;
+            before[k] += warp_sum[k][warp] + __reduce_add_sync(0xffffffffu, lane < rank ? x : 0);
+            total[k] = __reduce_add_sync(0xffffffffu, x);
+        }
+    };
+    int count[2] = {0, 0}, at[2], total[2];
     for (int b = b_lo; b < b_hi; ++b) {
         const Want w = load_want(A, b);
-        sum[0] += Fresh(A, w).count + shares(b, w);
+        count[0] += Fresh(A, w).count + shares(b, w);
     }
-    for (int p = p_lo; p < p_hi; ++p) sum[1] += is_free(p);
-    int at[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        int x = sum[k];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) warp_sum[k][warp] = x;
-        at[k] = x - sum[k];
-    }
-    __syncthreads();
-    if (warp < 2) {
-        int x = warp_sum[warp][lane];
-        const int mine = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        warp_sum[warp][lane] = x - mine;
-        if (lane == 31) cta_sum[warp] = x;
-    }
-    cluster_sync();
-    int total[2] = {0, 0};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        at[k] += warp_sum[k][warp];
-        for (int r = 0; r < kCluster; ++r) {
-            const int x = remote(&cta_sum[k], r);
-            if (r < rank) at[k] += x;
-            total[k] += x;
-        }
-    }
-    const int wanted = total[0], there = total[1];
+    uint32_t bits = free_bits(int64_t(g) * kPages);
+    count[1] = __popc(bits);
+    scan(count, at, total);
+    const int wanted = total[0];
     for (int b = b_lo; b < b_hi; ++b) {
         const Want w = load_want(A, b);
-        A.start[b] = at[0];
-        at[0] += Fresh(A, w).count + shares(b, w);
+        const int share = shares(b, w);
+        A.start[b] = make_int2(at[0], share);
+        at[0] += Fresh(A, w).count + share;
     }
-    for (int p = p_lo; p < p_hi && at[1] < wanted; ++p)
-        if (is_free(p)) A.free_list[at[1]++] = p;
+    int there = 0;
+    for (int64_t p0 = 0;;) {
+        for (int left = bits, n = there + at[1]; left && n < wanted; left &= left - 1)
+            A.free_list[n++] = int(p0 + int64_t(g) * kPages) + __ffs(left) - 1;
+        there += total[1];
+        if ((p0 += chunk) >= A.num_pages) break;
+        bits = free_bits(p0 + int64_t(g) * kPages);
+        count[0] = 0;
+        count[1] = __popc(bits);
+        cluster_sync();  // the sums are read
+        scan(count, at, total);
+    }
     if (g == 0) {
         A.totals[0] = max(there - wanted, 0);
         A.totals[1] = max(wanted - there, 0);
@@ -195,19 +232,27 @@ update_pages_kernel(const PagesArgs A) {
     cluster_sync();
 
     // ---- the wanted pages, and the claims back to zero ----------------------
+    for (int64_t p = int64_t(g) * kPages; p < A.num_pages; p += chunk) {
+        if (p + kPages <= A.num_pages) {
+#pragma unroll
+            for (int k = 0; k < kPages / 4; ++k) reinterpret_cast<int4 *>(A.claim + p)[k] = make_int4(0, 0, 0, 0);
+        } else {
+            for (int k = 0; p + k < A.num_pages; ++k) A.claim[p + k] = 0;
+        }
+    }
     for (int b = gw; b < A.B; b += kAllWarps) {
+        const int2 s = __ldcg(A.start + b);
         const Want w = load_want(A, b);
         const Fresh f(A, w);
-        const int32_t start = __ldcg(A.start + b);
-        const int share = shares(b, w), count = f.count + share, given = min(max(there - start, 0), count);
+        const int share = s.y, count = f.count + share, given = min(max(there - s.x, 0), count);
         int32_t *out = A.table_out + int64_t(b) * A.max_pages;
         for (int i = lane; i < f.count; i += 32)
-            if (i + share < given) out[f.place(w, i)] = __ldcg(A.free_list + start + share + i);
+            if (i + share < given) out[f.place(w, i)] = __ldcg(A.free_list + s.x + share + i);
         if (lane == 0) {
             int src = -1, dst = -1;
             if (share && given > 0) {
                 src = __ldcg(out + w.tail);
-                dst = __ldcg(A.free_list + start);
+                dst = __ldcg(A.free_list + s.x);
                 out[w.tail] = dst;
                 A.copies[atomicAdd(A.n_copies, 1)] = make_int4(src, dst, w.keep % A.page_size, 0);
             }
@@ -218,36 +263,46 @@ update_pages_kernel(const PagesArgs A) {
                                                : max(f.place(w, given - share) * A.page_size, w.keep);
         }
     }
-    cluster_sync();
-    for (int p = p_lo; p < p_hi; ++p) A.claim[p] = 0;
 }
 
 struct CopyArgs {
     int layers, heads, chunks;  // chunks: 16-byte parts of an entry
     int64_t layer_stride, page_stride, slot_stride, head_stride;
-    uint16_t *cache[2];
+    uint16_t *k, *v;
     const int4 *copies;
     const int32_t *n_copies;
 };
 
 constexpr int kThreadsCopy = 256;
+constexpr int kCopies = 8;  // 16-byte parts that a thread has asked for before it stores
 
 // A CTA takes one tail of one layer, of k or v, at a time.
 __global__ void __launch_bounds__(kThreadsCopy) copy_tails_kernel(const CopyArgs A) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int n = *A.n_copies;
+    const int n = *A.n_copies, tid = threadIdx.x;
     const int64_t units = int64_t(n) * A.layers * 2;
-    const int per_slot = A.heads * A.chunks;
+    // A thread keeps its place in an entry and walks the slots, `step` at a time.
+    const int per_slot = A.heads * A.chunks, step = max(kThreadsCopy / per_slot, 1), slot0 = tid / per_slot;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int4 c = A.copies[u % n];
         const int lk = int(u / n);
-        uint16_t *const base = A.cache[lk & 1] + (lk >> 1) * A.layer_stride;
-        for (int x = threadIdx.x; x < c.z * per_slot; x += kThreadsCopy) {
-            const int slot = x / per_slot, in = x - slot * per_slot, head = in / A.chunks;
-            const int64_t at = slot * A.slot_stride + head * A.head_stride + (in - head * A.chunks) * 8;
-            *reinterpret_cast<uint4 *>(base + c.y * A.page_stride + at) =
-                *reinterpret_cast<const uint4 *>(base + c.x * A.page_stride + at);
+        const int4 c = A.copies[u - int64_t(lk) * n];
+        uint16_t *const base = (lk & 1 ? A.v : A.k) + (lk >> 1) * A.layer_stride;
+        if (slot0 >= step) continue;
+        for (int in = tid - slot0 * per_slot; in < per_slot; in += kThreadsCopy) {
+            const int head = in / A.chunks;
+            uint16_t *const at = base + head * A.head_stride + (in - head * A.chunks) * 8;
+            const uint16_t *const from = at + c.x * A.page_stride;
+            uint16_t *const to = at + c.y * A.page_stride;
+            for (int s = slot0; s < c.z; s += step * kCopies) {
+                uint4 x[kCopies];
+#pragma unroll
+                for (int k = 0; k < kCopies; ++k)
+                    if (s + k * step < c.z) x[k] = __ldcs(reinterpret_cast<const uint4 *>(from + (s + k * step) * A.slot_stride));
+#pragma unroll
+                for (int k = 0; k < kCopies; ++k)
+                    if (s + k * step < c.z) *reinterpret_cast<uint4 *>(to + (s + k * step) * A.slot_stride) = x[k];
+            }
         }
     }
 }
@@ -258,7 +313,7 @@ PagesLayout pages_layout(int B, int num_pages) {
     PagesLayout l;
     l.copies = 256;
     l.start = l.copies + align256(sizeof(int4) * size_t(B));
-    l.claim = l.start + align256(sizeof(int32_t) * size_t(B));
+    l.claim = l.start + align256(sizeof(int2) * size_t(B));
     l.free_list = l.claim + align256(sizeof(int32_t) * size_t(num_pages));
     l.total = l.free_list + align256(sizeof(int32_t) * size_t(num_pages));
     return l;
@@ -276,12 +331,15 @@ cudaError_t launch_update_pages(const dspark_pages &p, int sms, cudaStream_t s) 
                 int((int64_t(p.sinks) + c.page_size - 1) / c.page_size), p.table_in, p.parent, p.keep_len,
                 p.want_len, p.first_pos, p.held, p.table_out, p.granted_len, p.tail_src, p.tail_dst, p.totals,
                 reinterpret_cast<int32_t *>(ws + l.claim), reinterpret_cast<int32_t *>(ws + l.free_list),
-                reinterpret_cast<int32_t *>(ws + l.start), reinterpret_cast<int4 *>(ws + l.copies),
+                reinterpret_cast<int2 *>(ws + l.start), reinterpret_cast<int4 *>(ws + l.copies),
                 reinterpret_cast<int32_t *>(ws) + 1};
-    cudaError_t e = launch_overlapped(update_pages_kernel, kCluster, kThreadsPages, 0, s, A);
+    constexpr int kCtas = 16;
+    cudaError_t e = cudaFuncSetAttribute(update_pages_kernel<kCtas>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    e = launch_clusters(update_pages_kernel<kCtas>, kCtas, kThreadsPages, kCtas, s, A);
     if (e != cudaSuccess || !c.k_cache) return e;
     const CopyArgs C{c.layers, c.Hkv, c.D / 8, c.layer_stride, c.page_stride, c.slot_stride, c.head_stride,
-                     {static_cast<uint16_t *>(c.k_cache), static_cast<uint16_t *>(c.v_cache)}, A.copies, A.n_copies};
+                     static_cast<uint16_t *>(c.k_cache), static_cast<uint16_t *>(c.v_cache), A.copies, A.n_copies};
     return launch_overlapped(copy_tails_kernel, 8 * sms, kThreadsCopy, 0, s, C);
 }
 

@@ -1,11 +1,24 @@
 // verify_tree.cu -- the walk that the target goes down a drafted tree.
 //
 // y_j = argmax of the target's row j, the lowest id on ties; the walk goes on
-// to the lowest child whose token is y of the present row.  Only the rows of the
-// walk are needed, so they are read one after the other, as the walk comes to
-// them.
+// to the lowest child whose token is y of the present row.  Maxima are taken
+// over 64-bit keys, the logit in an order-preserving form above the
+// complement of its id, so that the largest key is the lowest id of the
+// largest logit, whatever the order of the comparisons.
 //
-// Bound: bytes of the walks' rows, or the latency of one row after the other.
+// Only the walk's own rows are needed, and a walk seldom goes far, so
+// verify_tree_kernel reads one row after the other: a cluster of CTAs shares the
+// present row, each warp hands its key to every CTA of the cluster, and one
+// cluster barrier later all know the next row.  Bound: bytes of the walks'
+// rows while many walk, later the latency of a level (a load, a reduction, a
+// barrier).  Clusters are as large as still lets all requests walk at once.
+//
+// Few rows are read all at once (verify_tree_all_kernel): every CTA
+// takes a part of a row and merges its key by atomicMax, and the one that
+// finishes a request's last part walks in registers.  Reading more than needed
+// costs less than waiting once per level.
+#include <algorithm>
+
 #include "cache.cuh"
 #include "dspark_internal.cuh"
 #include "tcgen05.cuh"
@@ -13,83 +26,257 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreadsTree = 1024;
+constexpr int kThreadsTree = 256;
+constexpr int kMaxCluster = 16;
+// Bytes of all rows up to which they are read at once.
+constexpr size_t kAllBytes = size_t(24) << 20;
+constexpr int kAllRequests = 1024;  // and requests
+constexpr int kTreeLoads = 8;       // 16-byte loads of a thread in flight
 
 struct TreeArgs {
     int B, rows, q_max, V;
     const void *logits;
     const int32_t *row_off, *parent, *ids;
     int32_t *accept_len, *num_emitted, *path, *out_tokens, *commit;
+    unsigned long long *key;  // [rows]: verify_tree_all_kernel, 0 between calls
+    int32_t *done;            // [B]: parts read, 0 between calls
+    int parts;                // of a row
 };
 
-// A CTA walks one request's tree.
-template <typename T>
-__global__ void __launch_bounds__(kThreadsTree) verify_tree_kernel(const TreeArgs A) {
-    constexpr int E = Vec<T>::kElems;
-    __shared__ float best_v[32];
-    __shared__ int best_i[32], next, token;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row0 = min(max(A.row_off[b], 0), A.rows);
-    const int n = min(min(max(A.row_off[b + 1], row0), A.rows) - row0, A.q_max);
-    int32_t *const path = A.path + int64_t(b) * A.q_max, *const out = A.out_tokens + int64_t(b) * A.q_max;
-    int at = n > 0 ? 0 : -1, len = 0;
-    while (at >= 0) {
-        const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const T *>(A.logits) + int64_t(row0 + at) * A.V);
-        float v = -INFINITY;
-        int i = 0x7fffffff;
-        for (int c = tid; c < A.V / E; c += kThreadsTree) {
-            float x[E];
-            Vec<T>::unpack(row[c], x);
+struct Rows { int row0, n; };
+__device__ __forceinline__ Rows rows_of(const TreeArgs &A, int b) {
+    const int a0 = A.row_off[b], a1 = A.row_off[b + 1];
+    const int row0 = min(max(a0, 0), A.rows);
+    return {row0, min(min(max(a1, row0), A.rows) - row0, A.q_max)};
+}
+
+using Key = unsigned long long;
+__device__ __forceinline__ Key make_key(float v, int i) {
+    const uint32_t x = __float_as_uint(v + 0.f);  // -0 is 0
+    return (Key(x ^ (x >> 31 ? 0xffffffffu : 0x80000000u)) << 32) | uint32_t(~i);
+}
+__device__ __forceinline__ int id_of(Key k) { return int(~uint32_t(k)); }
+__device__ __forceinline__ Key warp_max(Key k) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) am_combine(v, i, x[e], c * E + e);
-        }
-        warp_am_reduce(v, i);
-        if (lane == 0) {
-            best_v[warp] = v;
-            best_i[warp] = i;
-        }
-        __syncthreads();
-        if (warp == 0) {
-            v = best_v[lane];
-            i = best_i[lane];
-            warp_am_reduce(v, i);
-            // the lowest child with that token
-            int child = -1;
-            for (int j0 = at + 1; j0 < n && child < 0; j0 += 32) {
-                const int j = j0 + lane;
-                const uint32_t hit = __ballot_sync(
-                    0xffffffffu, j < n && A.parent[row0 + j] == at && A.ids[row0 + j] == i);
-                if (hit) child = j0 + __ffs(hit) - 1;
+    for (int o = 16; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, o));
+    return k;
+}
+
+// The largest key of the 16-byte vectors first, first + stride, .. below end of a row, for this thread.
+template <typename T>
+__device__ __forceinline__ Key best_of(const uint4 *row, int first, int end, int stride) {
+    constexpr int E = Vec<T>::kElems;
+    float v = -INFINITY;
+    int at = -1;
+    for (int c0 = first; c0 < end; c0 += kTreeLoads * stride) {
+        uint4 x[kTreeLoads];
+#pragma unroll
+        for (int k = 0; k < kTreeLoads; ++k)
+            if (c0 + k * stride < end) x[k] = __ldcs(row + c0 + k * stride);
+#pragma unroll
+        for (int k = 0; k < kTreeLoads; ++k) {
+            if (c0 + k * stride >= end) break;
+            float z[E];
+            Vec<T>::unpack(x[k], z);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                // ids ascend, so the first of equals stays
+                if (z[e] > v || at < 0) {
+                    v = z[e];
+                    at = (c0 + k * stride) * E + e;
+                }
             }
-            if (lane == 0) {
-                path[len] = at;
-                out[len] = i;
-                next = child;
-            }
         }
-        __syncthreads();
-        at = next;
+    }
+    return at < 0 ? 0 : make_key(v, at);
+}
+
+// The lowest child of row `at` whose token is y; -1: none.  Lane j holds rows j and 32 + j.
+__device__ __forceinline__ int child_of(int at, int y, const int (&parent)[2], const int (&id)[2], int lane) {
+    const uint32_t lo = __ballot_sync(0xffffffffu, parent[0] == at && id[0] == y);
+    const uint32_t hi = __ballot_sync(0xffffffffu, parent[1] == at && id[1] == y);
+    return lo ? __ffs(lo) - 1 : hi ? 31 + __ffs(hi) : -1;
+}
+// Those rows of a request; a parent that is not below its row is none.
+__device__ __forceinline__ void load_tree(const TreeArgs &A, const Rows &r, int lane, int (&parent)[2], int (&id)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int j = 32 * h + lane;
+        parent[h] = -1;
+        id[h] = -1;
+        if (j > 0 && j < r.n) {
+            parent[h] = A.parent[r.row0 + j];
+            id[h] = A.ids[r.row0 + j];
+            if (parent[h] >= j) parent[h] = -1;
+        }
+    }
+}
+
+// A walk on its way out: lane j keeps entries j and 32 + j.
+struct Walk {
+    int len = 0, path[2] = {-1, -1}, token[2] = {-1, -1};
+    __device__ __forceinline__ void add(int at, int y, int lane) {
+        if (len == lane) {
+            path[0] = at;
+            token[0] = y;
+        } else if (len == 32 + lane) {
+            path[1] = at;
+            token[1] = y;
+        }
         ++len;
     }
-    for (int j = len + tid; j < A.q_max; j += kThreadsTree) path[j] = out[j] = -1;
-    if (tid == 0) {
-        A.accept_len[b] = max(len - 1, 0);
-        A.num_emitted[b] = len;
-        if (A.commit) A.commit[b] += len;
+    __device__ __forceinline__ void write(const TreeArgs &A, int b, int lane) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = 32 * h + lane;
+            if (j < A.q_max) {
+                A.path[int64_t(b) * A.q_max + j] = path[h];
+                A.out_tokens[int64_t(b) * A.q_max + j] = token[h];
+            }
+        }
+        if (lane == 0) {
+            A.accept_len[b] = max(len - 1, 0);
+            A.num_emitted[b] = len;
+            if (A.commit) A.commit[b] += len;
+        }
     }
+};
+
+// A cluster walks one request's tree, row by row.
+template <typename T>
+__global__ void __launch_bounds__(kThreadsTree) verify_tree_kernel(const TreeArgs A) {
+    constexpr int kWarpsTree = kThreadsTree / 32;
+    __shared__ Key keys[2][kMaxCluster * kWarpsTree];  // by level % 2: of all warps of the cluster
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int rank, size;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+    // all CTAs of the cluster are there before one writes to another's memory (waited for below)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int b = blockIdx.x / size, vecs = A.V / Vec<T>::kElems;
+    const Rows r = rows_of(A, b);
+    int parent[2], id[2];
+    load_tree(A, r, lane, parent, id);
+    Walk walk;
+    int at = r.n > 0 ? 0 : -1;
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    while (at >= 0) {
+        const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const T *>(A.logits) + int64_t(r.row0 + at) * A.V);
+        Key k = warp_max(best_of<T>(row, rank * kThreadsTree + tid, vecs, size * kThreadsTree));
+        Key *const mine = &keys[walk.len & 1][rank * kWarpsTree + warp];
+        if (lane < size)
+            asm volatile(
+                "{\n\t.reg .b32 a;\n\t"
+                "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+                "st.shared::cluster.b64 [a], %2;\n\t}"
+                ::"r"(smem_addr(mine)), "r"(lane), "l"(k) : "memory");
+        // One barrier a level: the other buffer is written only by warps that have passed the next one.
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        k = 0;
+        for (int w = lane; w < size * kWarpsTree; w += 32) k = max(k, keys[walk.len & 1][w]);
+        const int y = id_of(warp_max(k));
+        const int next = child_of(at, y, parent, id, lane);
+        walk.add(at, y, lane);
+        at = next;
+    }
+    if (rank == 0 && warp == 0) walk.write(A, b, lane);
+    // no CTA ends while others may still write to it: the last barrier came after the last write
+}
+
+// All rows at once.
+template <typename T>
+__global__ void __launch_bounds__(kThreadsTree) verify_tree_all_kernel(const TreeArgs A) {
+    __shared__ Key keys[kThreadsTree / 32];
+    __shared__ int last;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int item = blockIdx.x / A.parts, part = blockIdx.x - item * A.parts;
+    const int b = item / A.q_max, j = item - b * A.q_max;
+    const Rows r = rows_of(A, b);
+    if (j >= r.n) {
+        if (r.n == 0 && j == 0 && part == 0 && warp == 0) Walk().write(A, b, lane);
+        return;
+    }
+    const int vecs = A.V / Vec<T>::kElems, each = (vecs + A.parts - 1) / A.parts;
+    const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const T *>(A.logits) + int64_t(r.row0 + j) * A.V);
+    Key k = warp_max(best_of<T>(row, part * each + tid, min((part + 1) * each, vecs), kThreadsTree));
+    if (lane == 0) keys[warp] = k;
+    __syncthreads();
+    if (warp > 0) return;
+    k = warp_max(lane < kThreadsTree / 32 ? keys[lane] : 0);
+    if (lane == 0) {
+        atomicMax(A.key + r.row0 + j, k);
+        __threadfence();
+        last = atomicAdd(A.done + b, 1) == r.n * A.parts - 1;
+    }
+    __syncwarp();
+    if (!last) return;
+    __threadfence();
+    int parent[2], id[2], best[2] = {0, 0};
+    load_tree(A, r, lane, parent, id);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (32 * h + lane < r.n) {
+            best[h] = id_of(__ldcg(A.key + r.row0 + 32 * h + lane));
+            A.key[r.row0 + 32 * h + lane] = 0;  // as the next call wants it
+        }
+    }
+    if (lane == 0) A.done[b] = 0;
+    Walk walk;
+    for (int at = 0; at >= 0;) {
+        const int lo = __shfl_sync(0xffffffffu, best[0], at & 31), hi = __shfl_sync(0xffffffffu, best[1], at & 31);
+        const int y = at < 32 ? lo : hi;
+        walk.add(at, y, lane);
+        at = child_of(at, y, parent, id, lane);
+    }
+    walk.write(A, b, lane);
+}
+
+// Rows that are read at once, at most: what the workspace has room for.
+size_t all_rows(int B, int rows, int V) {
+    const size_t most = B <= kAllRequests ? kAllBytes / (size_t(V) * 2) : 0;
+    return size_t(rows) <= most ? size_t(rows) : 0;
+}
+
+template <typename T>
+cudaError_t launch(TreeArgs A, size_t together, int sms, cudaStream_t s) {
+    // all in one wave of CTAs
+    if (together && A.B * A.q_max <= 8 * sms) {
+        A.parts = std::max(1, std::min(4 * sms / (A.B * A.q_max), A.V / 2048));
+        return launch_overlapped(verify_tree_all_kernel<T>, A.B * A.q_max * A.parts, kThreadsTree, 0, s, A);
+    }
+    int size = kMaxCluster;
+    // one wave too, and no thread without a vector of the row
+    while (size > 1 && (A.B * size > 8 * sms || size / 2 * kThreadsTree >= A.V / Vec<T>::kElems)) size /= 2;
+    if (size > 8) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(verify_tree_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_clusters(verify_tree_kernel<T>, A.B * size, kThreadsTree, size, s, A);
 }
 
 }  // namespace
 
-size_t tree_workspace_bytes(int, int, int) { return 256; }
+// The workspace: status; parts done by request; keys by row.
+size_t tree_workspace_bytes(int B, int rows, int V) {
+    const size_t n = all_rows(B, rows, V);
+    return n ? 256 + align256(sizeof(int32_t) * size_t(B)) + align256(sizeof(Key) * n) : 256;
+}
 
-cudaError_t launch_verify_tree(const dspark_tree &t, int, cudaStream_t s) {
+cudaError_t launch_verify_tree(const dspark_tree &t, int sms, cudaStream_t s) {
+    char *ws = static_cast<char *>(t.workspace);
+    const bool bf16 = t.logit_dtype == DSPARK_BF16;
+    const size_t n = all_rows(t.B, t.rows, t.V), bytes = size_t(t.rows) * t.V * (bf16 ? 2 : 4);
     const TreeArgs A{t.B, t.rows, t.q_max, t.V, t.target_logits, t.row_off, t.parent, t.packed_ids,
-                     t.accept_len, t.num_emitted, t.path, t.out_tokens, t.seq_lens_commit};
-    return t.logit_dtype == DSPARK_BF16 ? launch_overlapped(verify_tree_kernel<uint16_t>, t.B, kThreadsTree, 0, s, A)
-                                        : launch_overlapped(verify_tree_kernel<float>, t.B, kThreadsTree, 0, s, A);
+                     t.accept_len, t.num_emitted, t.path, t.out_tokens, t.seq_lens_commit,
+                     reinterpret_cast<Key *>(ws + 256 + align256(sizeof(int32_t) * size_t(t.B))),
+                     reinterpret_cast<int32_t *>(ws + 256), 1};
+    const size_t together = bytes <= kAllBytes ? n : 0;
+    return bf16 ? launch<uint16_t>(A, together, sms, s) : launch<float>(A, together, sms, s);
 }
 
 }  // namespace dspark

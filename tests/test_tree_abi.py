@@ -224,7 +224,7 @@ def test_binding_checks_what_it_is_given(lib):
         with pytest.raises(ValueError, match=what):
             binding.dspark_step_attention_tree(a, bad)
     c = cache()
-    with pytest.raises(ValueError, match="path must be"):
+    with pytest.raises(ValueError, match="path must be a matrix"):
         binding.dspark_commit_path(c, fake(4, 8, dtype=torch.int32), None, fake(36, dtype=torch.int32))
     with pytest.raises(ValueError, match="block_table must be"):
         binding.dspark_commit_path(c, fake(3, 8, dtype=torch.int32), None, fake(4, 9, dtype=torch.int32))
