@@ -138,18 +138,6 @@ struct Ctrl {
     int gave_up;
 };
 
-// 16 bfloat16 of one row: a whole sector where the alignment allows.
-__device__ __forceinline__ void st_global32(uint16_t *p, const uint32_t (&y)[8], bool wide) {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                     ::"l"(p), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4 *>(p)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-        reinterpret_cast<uint4 *>(p)[1] = make_uint4(y[4], y[5], y[6], y[7]);
-    }
-}
-
 // Reads the next unit off the ring.
 struct SchedReader {
     Ring r;

@@ -1248,9 +1248,10 @@ inline bool step_gather_rows(const dspark_attn &a, int64_t *row, int64_t *page_r
     return *row >= a.D && last <= INT32_MAX;
 }
 
-template <Seen kSeen>
-cudaError_t launch_rows(const dspark_attn &a, const uint64_t *row_seen, int sinks, int sms, uint64_t wait_ns, cudaStream_t s) {
-    StepArgs A{};
+// The arguments and tensor maps of a call: units of up to `rows_cap` rows, whose columns' parts have room for
+// `ncap`; a copy of queries takes q_rows rows.
+inline cudaError_t step_args(const dspark_attn &a, const uint64_t *row_seen, int sinks, int rows_cap, int ncap, int q_rows,
+                             uint64_t wait_ns, StepArgs &A, CUtensorMap (&maps)[3]) {
     A.B = a.B; A.rows = a.rows; A.q_max = a.q_max; A.Hq = a.Hq; A.Hkv = a.Hkv; A.G = a.Hq / a.Hkv;
     A.page_size = a.page_size; A.num_pages = a.num_pages; A.max_pages = a.max_pages;
     A.window = a.window;
@@ -1260,8 +1261,8 @@ cudaError_t launch_rows(const dspark_attn &a, const uint64_t *row_seen, int sink
     A.page_shift = 31;  // exact below 2^31: page_mul = ceil(2^shift / page_size) < 2^32
     while ((1u << (A.page_shift - 31)) < unsigned(a.page_size)) ++A.page_shift;
     A.page_mul = uint32_t(((1ull << A.page_shift) + a.page_size - 1) / a.page_size);
-    A.ncap = step_columns(a.Hq, a.Hkv, a.q_max);
-    A.rows_cap = step_rows(a.Hq, a.Hkv, a.q_max);
+    A.ncap = ncap;
+    A.rows_cap = rows_cap;
     A.scale2 = float(double(a.scale) * 1.4426950408889634);
     A.headroom = std::min(kHeadroom / A.scale2, 1e38f);
     A.page_stride = a.page_stride; A.slot_stride = a.slot_stride; A.head_stride = a.head_stride;
@@ -1279,11 +1280,10 @@ cudaError_t launch_rows(const dspark_attn &a, const uint64_t *row_seen, int sink
 
     // A page of 8 k positions is copied in boxes of whole pages or parts of
     // them; other pages key by key (four keys a copy).
-    CUtensorMap maps[3];
     {
         const uint64_t dims[3] = {uint64_t(a.D), uint64_t(a.Hq), uint64_t(a.rows)};
         const uint64_t st[2] = {uint64_t(a.D) * 2, uint64_t(a.D) * a.Hq * 2};
-        const uint32_t bx[3] = {64, uint32_t(A.G), 1};
+        const uint32_t bx[3] = {64, uint32_t(A.G), uint32_t(q_rows)};
         const cudaError_t e = encode_map(&maps[0], a.q_rot, 3, dims, st, bx);
         if (e != cudaSuccess) return e;
     }
@@ -1313,6 +1313,16 @@ cudaError_t launch_rows(const dspark_attn &a, const uint64_t *row_seen, int sink
             if (e != cudaSuccess) return e;
         }
     }
+    return cudaSuccess;
+}
+
+template <Seen kSeen>
+cudaError_t launch_rows(const dspark_attn &a, const uint64_t *row_seen, int sinks, int sms, uint64_t wait_ns, cudaStream_t s) {
+    StepArgs A{};
+    CUtensorMap maps[3];
+    const cudaError_t e = step_args(a, row_seen, sinks, step_rows(a.Hq, a.Hkv, a.q_max),
+                                    step_columns(a.Hq, a.Hkv, a.q_max), 1, wait_ns, A, maps);
+    if (e != cudaSuccess) return e;
     const int ctas = std::min(sms, kAttnMaxCtas);
     if (A.box) return a.D == 128 ? launch<128, true, kSeen>(A, maps, ctas, s) : launch<64, true, kSeen>(A, maps, ctas, s);
     return a.D == 128 ? launch<128, false, kSeen>(A, maps, ctas, s) : launch<64, false, kSeen>(A, maps, ctas, s);
