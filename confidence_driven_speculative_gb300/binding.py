@@ -316,7 +316,8 @@ def dspark_commit_path(cache: DsparkCache, block_table, seq_lens, path, stream=N
     rows, max_pages = _matrix(block_table, "block_table")
     if rows != B:
         raise ValueError(f"block_table must be [{B}, n], got {tuple(block_table.shape)}")
-    if seq_lens is not None:
+    if seq_lens is not None and (seq_lens.dtype is not _INT32 or seq_lens.numel() != B or not seq_lens.is_cuda
+                                 or not seq_lens.is_contiguous()):
         _device_array(seq_lens, "seq_lens", "int32", B)
     rc = load().dspark_commit_path(ctypes.byref(cache), B, q_max, max_pages, block_table.data_ptr(),
                                    None if seq_lens is None else seq_lens.data_ptr(), path.data_ptr(),
@@ -443,12 +444,22 @@ def _device_words(t, name: str, numel: int) -> None:
         raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
 
 
-def _matrix(t, name: str):
-    """Shape of a contiguous device int32 matrix."""
-    _device_array(t, name, "int32")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix, got {tuple(t.shape)}")
-    return t.shape
+_INT32 = None  # torch.int32, once asked for
+
+
+def _matrix(t, name: str) -> tuple:
+    """Shape of a contiguous device int32 matrix.  The checks that a good one passes come first: this is
+    on the way of every call."""
+    global _INT32
+    if _INT32 is None:
+        import torch
+        _INT32 = torch.int32
+    if getattr(t, "dtype", None) is not _INT32 or not t.is_cuda or not t.is_contiguous():
+        _device_array(t, name, "int32")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix, got {tuple(shape)}")
+    return shape
 
 
 class StepBuffers:

@@ -18,22 +18,23 @@ namespace dspark {
 namespace {
 
 constexpr int kThreadsCommit = 256;
-constexpr int kInFlight = 8;  // entries that a thread has asked for before it stores
+constexpr int kMoves = 4;  // of each layer, that a thread has asked for before it stores
 
 struct CommitArgs {
-    int B, q_max, max_pages, layers, group, groups, heads, chunks, page_size, num_pages;
+    int B, q_max, max_pages, layers, groups, heads, chunks, page_size, num_pages;
     int64_t layer_stride, page_stride, slot_stride, head_stride;
     uint16_t *k, *v;
     const int32_t *block_table, *seq_lens, *path;
 };
 
-// A CTA takes one request in a group of layers.
-__global__ void __launch_bounds__(kThreadsCommit) commit_path_kernel(const CommitArgs A) {
+// A CTA takes one request in kLayers layers.
+template <int kLayers>
+__global__ void __launch_bounds__(kThreadsCommit, kLayers == 2 ? 5 : 6) commit_path_kernel(const CommitArgs A) {
     __shared__ int64_t from[DSPARK_MAX_STEP_ROWS], to[DSPARK_MAX_STEP_ROWS];
     __shared__ int moves;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int b = blockIdx.x / A.groups, layer0 = (blockIdx.x - b * A.groups) * A.group, tid = threadIdx.x;
+    const int b = blockIdx.x / A.groups, layer0 = (blockIdx.x - b * A.groups) * kLayers, tid = threadIdx.x;
     if (tid < 32) {
         // the moves, in ascending places
         const int32_t *path = A.path + int64_t(b) * A.q_max, *table = A.block_table + int64_t(b) * A.max_pages;
@@ -68,32 +69,26 @@ __global__ void __launch_bounds__(kThreadsCommit) commit_path_kernel(const Commi
         if (tid == 0) moves = n;
     }
     __syncthreads();
-    const int n = moves, per = A.heads * A.chunks, all = n * min(A.group, A.layers - layer0);
-    if (n == 0) return;
-    for (int x = tid; x < 2 * per; x += kThreadsCommit) {
+    const int n = moves, per = A.heads * A.chunks;
+    const bool both = kLayers == 2 && layer0 + 1 < A.layers;
+    for (int x = tid; n > 0 && x < 2 * per; x += kThreadsCommit) {
         const int kv = x >= per, in = x - kv * per, head = in / A.chunks;
         uint16_t *const base = (kv ? A.v : A.k) + layer0 * A.layer_stride + head * A.head_stride + (in - head * A.chunks) * 8;
-        // all moves of all layers of the group, layer by layer
-        int64_t next = 0;  // the layer of the next move, and the move
-        for (int m0 = 0, i = 0; m0 < all; m0 += kInFlight) {
-            uint4 v[kInFlight];
-            int64_t layer = next;
-            int at = i;
+        for (int m0 = 0; m0 < n; m0 += kMoves) {
+            uint4 v[kLayers][kMoves];
 #pragma unroll
-            for (int m = 0; m < kInFlight; ++m) {
-                if (m0 + m < all) v[m] = *reinterpret_cast<const uint4 *>(base + next + from[i]);
-                if (++i == n) {
-                    i = 0;
-                    next += A.layer_stride;
-                }
+            for (int m = 0; m < kMoves; ++m) {
+                if (m0 + m >= n) break;
+                const uint16_t *src = base + from[m0 + m];
+                v[0][m] = *reinterpret_cast<const uint4 *>(src);
+                if (kLayers == 2 && both) v[kLayers - 1][m] = *reinterpret_cast<const uint4 *>(src + A.layer_stride);
             }
 #pragma unroll
-            for (int m = 0; m < kInFlight; ++m) {
-                if (m0 + m < all) *reinterpret_cast<uint4 *>(base + layer + to[at]) = v[m];
-                if (++at == n) {
-                    at = 0;
-                    layer += A.layer_stride;
-                }
+            for (int m = 0; m < kMoves; ++m) {
+                if (m0 + m >= n) break;
+                uint16_t *dst = base + to[m0 + m];
+                *reinterpret_cast<uint4 *>(dst) = v[0][m];
+                if (kLayers == 2 && both) *reinterpret_cast<uint4 *>(dst + A.layer_stride) = v[kLayers - 1][m];
             }
         }
     }
@@ -103,14 +98,14 @@ __global__ void __launch_bounds__(kThreadsCommit) commit_path_kernel(const Commi
 
 cudaError_t launch_commit_path(const dspark_cache &c, int B, int q_max, int max_pages, const int32_t *block_table,
                                const int32_t *seq_lens, const int32_t *path, int sms, cudaStream_t s) {
-    // As many layers to a CTA as let all CTAs run at once: their path and pages are looked up once.
-    const int group = std::max(1, std::min<int>(c.layers, int64_t(B) * c.layers / (8 * sms)));
-    const int groups = (c.layers + group - 1) / group;
-    const CommitArgs A{B, q_max, max_pages, c.layers, group, groups, c.Hkv, c.D / 8, c.page_size, c.num_pages,
+    // Two layers to a CTA, whose path and pages are looked up once, where there are CTAs enough.
+    const bool two = int64_t(B) * c.layers > 4 * sms;
+    const int groups = two ? (c.layers + 1) / 2 : c.layers;
+    const CommitArgs A{B, q_max, max_pages, c.layers, groups, c.Hkv, c.D / 8, c.page_size, c.num_pages,
                        c.layer_stride, c.page_stride, c.slot_stride, c.head_stride,
                        static_cast<uint16_t *>(c.k_cache), static_cast<uint16_t *>(c.v_cache),
                        block_table, seq_lens, path};
-    return launch_overlapped(commit_path_kernel, B * groups, kThreadsCommit, 0, s, A);
+    return launch_overlapped(two ? commit_path_kernel<2> : commit_path_kernel<1>, B * groups, kThreadsCommit, 0, s, A);
 }
 
 }  // namespace dspark

@@ -21,19 +21,21 @@ namespace dspark {
 namespace {
 
 constexpr int kThreadsPages = 1024;
+static_assert(kThreadsPages == 32 * 32, "the scan takes a warp's sums from a lane each");
 constexpr int kSeg = 256;               // entries of a table that a warp takes at once
 constexpr int kPages = 8;               // pages in a row that a thread looks at
+constexpr int kFewPages = 4;            // new pages that a thread writes by itself
 constexpr int kFull = 0x7fffffff;       // claim of a request that only reads
 constexpr int kWriters = 1 << 17;       // kWriters - b: claim of request b that writes
 
 struct PagesArgs {
     int B_in, B, max_pages, num_pages, page_size, sink_pages;
+    uint32_t page_mul, page_shift;  // position / page_size = position * mul >> shift
     const int32_t *table_in, *parent, *keep_len, *want_len, *first_pos, *held;
     int32_t *table_out, *granted_len, *tail_src, *tail_dst, *totals;
     int32_t *claim;   // [num_pages], 0 between calls
     int32_t *free_list;  // [num_pages]
-    int2 *start;      // [B] rank of the request's first wanted page, does its tail need one?
-    int4 *copies;     // [B] source, destination, entries
+    int4 *copies;        // [B] source, destination, entries
     int32_t *n_copies;
 };
 
@@ -46,16 +48,18 @@ struct Want {
 };
 
 __device__ __forceinline__ Want load_want(const PagesArgs &A, int b) {
+    auto page_of = [&](int pos) { return int((uint64_t(uint32_t(pos)) * A.page_mul) >> A.page_shift); };
     Want w;
     const int cap = A.max_pages * A.page_size;
     w.parent = A.parent ? A.parent[b] : b;
     if (w.parent >= A.B_in) w.parent = -1;
     w.keep = min(max(A.keep_len[b], 0), cap);
     w.want = min(max(A.want_len[b], w.keep), cap);
-    w.first = A.first_pos ? max(A.first_pos[b], 0) / A.page_size : 0;
-    w.keep_pages = (w.keep + A.page_size - 1) / A.page_size;
-    w.want_pages = (w.want + A.page_size - 1) / A.page_size;
-    w.tail = w.want > w.keep && w.keep % A.page_size ? w.keep_pages - 1 : -1;
+    w.first = A.first_pos ? page_of(max(A.first_pos[b], 0)) : 0;
+    w.keep_pages = page_of(w.keep + A.page_size - 1);
+    w.want_pages = page_of(w.want + A.page_size - 1);
+    const int last = page_of(w.keep);
+    w.tail = w.want > w.keep && last < w.keep_pages ? last : -1;
     return w;
 }
 
@@ -94,18 +98,33 @@ __device__ __forceinline__ int remote(const int *p, int rank) {
 template <int kCtas>
 __global__ void __launch_bounds__(kThreadsPages, 1) update_pages_kernel(const PagesArgs A) {
     constexpr int kAll = kCtas * kThreadsPages, kAllWarps = kAll / 32;
-    __shared__ int warp_sum[2][32], cta_sum[2];
+    __shared__ int warp_sum[2][32], cta_sum[2], cta_before[2], cluster_sum[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster_rank();
     // Warps of one number lie in different CTAs, so that few requests keep all CTAs busy.
     const int g = rank * kThreadsPages + tid, gw = warp * kCtas + rank;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- what is kept, and the claims on it --------------------------------
+    // A thread looks after `per` requests; of the first it keeps what it knows.
     if (g == 0) *A.n_copies = 0;
+    const int per = (A.B + kAll - 1) / kAll;
+    const int b_lo = min(g * per, A.B), b_hi = min(b_lo + per, A.B);
+    auto tail_page = [&](const Want &w) {  // that the tail lies in, or -1
+        if (w.tail < 0 || w.parent < 0 || !(w.tail >= w.first || w.tail < A.sink_pages)) return -1;
+        const int page = A.table_in[int64_t(w.parent) * A.max_pages + w.tail];
+        return page < A.num_pages ? page : -1;
+    };
+    Want w0{};
+    int tail0 = -1;
+    if (b_lo < b_hi) {
+        w0 = load_want(A, b_lo);
+        tail0 = tail_page(w0);
+    }
+
+    // ---- what is kept, and the claims on it --------------------------------
     const int segs = (A.max_pages + kSeg - 1) / kSeg;
-    for (int64_t s = gw; s < int64_t(A.B) * segs; s += kAllWarps) {
-        const int b = int(s / segs), i0 = int(s - int64_t(b) * segs) * kSeg + lane;
+    for (int b = gw / segs, seg = gw % segs; b < A.B;) {
+        const int i0 = seg * kSeg + lane;
         const Want w = load_want(A, b);
         const int32_t *in = A.table_in + int64_t(max(w.parent, 0)) * A.max_pages;
         int32_t *out = A.table_out + int64_t(b) * A.max_pages;
@@ -124,20 +143,22 @@ __global__ void __launch_bounds__(kThreadsPages, 1) update_pages_kernel(const Pa
             if (page[k] >= 0) atomicMax(A.claim + page[k], i == w.tail ? kWriters - b : kFull);
             out[i] = max(page[k], -1);
         }
+        b += kAllWarps / segs;
+        seg += kAllWarps % segs;
+        if (seg >= segs) {
+            seg -= segs;
+            ++b;
+        }
     }
     cluster_sync();
 
     // ---- ranks of the wanted pages and of the free ones ---------------------
-    // A thread counts the pages of `per` requests, and of every kAll * kPages
-    // pages kPages in a row.
-    const int per = (A.B + kAll - 1) / kAll;
-    const int b_lo = min(g * per, A.B), b_hi = min(b_lo + per, A.B);
-    // Does request b's tail need a page of its own?
-    auto shares = [&](int b, const Want &w) {
-        if (w.tail < 0) return false;
-        const int page = __ldcg(A.table_out + int64_t(b) * A.max_pages + w.tail);
+    // Does request b's tail, in `page`, need a page of its own?
+    auto shares = [&](int b, int page) {
         return page >= 0 && (__ldcg(A.claim + page) != kWriters - b || (A.held && A.held[page]));
     };
+    const int claim0 = tail0 >= 0 ? __ldcg(A.claim + tail0) : 0, held0 = tail0 >= 0 && A.held ? A.held[tail0] : 0;
+    // Of every kAll * kPages pages a thread looks at kPages in a row.
     const int64_t chunk = int64_t(kAll) * kPages;
     // Bits of the free ones of a thread's pages p .. p + kPages - 1; their claims go back to zero in `clear`.
     auto free_bits = [&](int64_t p) {
@@ -191,28 +212,33 @@ __global__ void __launch_bounds__(kThreadsPages, 1) update_pages_kernel(const Pa
             if (lane == 31) cta_sum[warp] = x;
         }
         cluster_sync();
+        if (warp < 2) {  // one reader a CTA: all warps at once take 5 us
+            const int x = lane < kCtas ? remote(&cta_sum[warp], lane) : 0;
+            const int below = __reduce_add_sync(0xffffffffu, lane < rank ? x : 0);
+            const int all = __reduce_add_sync(0xffffffffu, x);
+            if (lane == 0) {
+                cta_before[warp] = below;
+                cluster_sum[warp] = all;
+            }
+        }
+        __syncthreads();
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int x = lane < kCtas ? remote(&cta_sum[k], lane) : 0;
-            before[k] += warp_sum[k][warp] + __reduce_add_sync(0xffffffffu, lane < rank ? x : 0);
-            total[k] = __reduce_add_sync(0xffffffffu, x);
+            before[k] += warp_sum[k][warp] + cta_before[k];
+            total[k] = cluster_sum[k];
         }
     };
     int count[2] = {0, 0}, at[2], total[2];
-    for (int b = b_lo; b < b_hi; ++b) {
+    for (int b = b_lo + 1; b < b_hi; ++b) {
         const Want w = load_want(A, b);
-        count[0] += Fresh(A, w).count + shares(b, w);
+        count[0] += Fresh(A, w).count + shares(b, tail_page(w));
     }
     uint32_t bits = free_bits(int64_t(g) * kPages);
     count[1] = __popc(bits);
+    const int share0 = tail0 >= 0 && (claim0 != kWriters - b_lo || held0);
+    if (b_lo < b_hi) count[0] += Fresh(A, w0).count + share0;
     scan(count, at, total);
-    const int wanted = total[0];
-    for (int b = b_lo; b < b_hi; ++b) {
-        const Want w = load_want(A, b);
-        const int share = shares(b, w);
-        A.start[b] = make_int2(at[0], share);
-        at[0] += Fresh(A, w).count + share;
-    }
+    const int wanted = total[0], start0 = at[0];  // rank of the thread's first wanted page
     int there = 0;
     for (int64_t p0 = 0;;) {
         for (int left = bits, n = there + at[1]; left && n < wanted; left &= left - 1)
@@ -232,35 +258,59 @@ __global__ void __launch_bounds__(kThreadsPages, 1) update_pages_kernel(const Pa
     cluster_sync();
 
     // ---- the wanted pages, and the claims back to zero ----------------------
+    auto finish = [&](int b, const Want &w, const Fresh &f, int start, int share, int page) {
+        const int all = f.count + share, given = min(max(there - start, 0), all);
+        int src = -1, dst = -1;
+        if (share && given > 0) {
+            src = page;
+            dst = __ldcg(A.free_list + start);
+            A.table_out[int64_t(b) * A.max_pages + w.tail] = dst;
+            A.copies[atomicAdd(A.n_copies, 1)] = make_int4(src, dst, w.keep - w.tail * A.page_size, 0);
+        }
+        A.tail_src[b] = src;
+        A.tail_dst[b] = dst;
+        A.granted_len[b] = given == all ? w.want
+                           : given < share ? w.keep
+                                           : max(f.place(w, given - share) * A.page_size, w.keep);
+    };
+    // New pages first, first + step, ..; `start` is the rank of the first new one.
+    auto give = [&](int b, const Want &w, const Fresh &f, int start, int first, int step) {
+        const int given = min(max(there - start, 0), f.count);
+        for (int i = first; i < given; i += step)
+            A.table_out[int64_t(b) * A.max_pages + f.place(w, i)] = __ldcg(A.free_list + start + i);
+    };
+    int start = start0;
+    for (int k = 0; k < per; ++k) {
+        const int b = b_lo + k;
+        const bool mine = b < b_hi;
+        Want w = w0;
+        int page = tail0, share = share0;
+        if (k > 0 && mine) {
+            w = load_want(A, b);
+            page = tail_page(w);
+            share = shares(b, page);
+        }
+        const Fresh f(A, w);
+        if (mine) {
+            finish(b, w, f, start, share, page);
+            if (f.count <= kFewPages) give(b, w, f, start + share, 0, 1);
+        }
+        // a request that wants many: all lanes
+        for (uint32_t many = __ballot_sync(0xffffffffu, mine && f.count > kFewPages); many; many &= many - 1) {
+            const int src = __ffs(many) - 1, bs = __shfl_sync(0xffffffffu, b, src);
+            const int at0 = __shfl_sync(0xffffffffu, start + share, src);
+            const Want ws = load_want(A, bs);
+            give(bs, ws, Fresh(A, ws), at0, lane, 32);
+        }
+        if (mine) start += f.count + share;
+    }
+    if (per > 1) cluster_sync();  // claims are read up to here
     for (int64_t p = int64_t(g) * kPages; p < A.num_pages; p += chunk) {
         if (p + kPages <= A.num_pages) {
 #pragma unroll
             for (int k = 0; k < kPages / 4; ++k) reinterpret_cast<int4 *>(A.claim + p)[k] = make_int4(0, 0, 0, 0);
         } else {
             for (int k = 0; p + k < A.num_pages; ++k) A.claim[p + k] = 0;
-        }
-    }
-    for (int b = gw; b < A.B; b += kAllWarps) {
-        const int2 s = __ldcg(A.start + b);
-        const Want w = load_want(A, b);
-        const Fresh f(A, w);
-        const int share = s.y, count = f.count + share, given = min(max(there - s.x, 0), count);
-        int32_t *out = A.table_out + int64_t(b) * A.max_pages;
-        for (int i = lane; i < f.count; i += 32)
-            if (i + share < given) out[f.place(w, i)] = __ldcg(A.free_list + s.x + share + i);
-        if (lane == 0) {
-            int src = -1, dst = -1;
-            if (share && given > 0) {
-                src = __ldcg(out + w.tail);
-                dst = __ldcg(A.free_list + s.x);
-                out[w.tail] = dst;
-                A.copies[atomicAdd(A.n_copies, 1)] = make_int4(src, dst, w.keep % A.page_size, 0);
-            }
-            A.tail_src[b] = src;
-            A.tail_dst[b] = dst;
-            A.granted_len[b] = given == count ? w.want
-                               : given < share ? w.keep
-                                               : max(f.place(w, given - share) * A.page_size, w.keep);
         }
     }
 }
@@ -308,12 +358,11 @@ __global__ void __launch_bounds__(kThreadsCopy) copy_tails_kernel(const CopyArgs
 }
 
 // The workspace: status word, number of copies; copies; ranks; claims; free pages.
-struct PagesLayout { size_t copies, start, claim, free_list, total; };
+struct PagesLayout { size_t copies, claim, free_list, total; };
 PagesLayout pages_layout(int B, int num_pages) {
     PagesLayout l;
     l.copies = 256;
-    l.start = l.copies + align256(sizeof(int4) * size_t(B));
-    l.claim = l.start + align256(sizeof(int2) * size_t(B));
+    l.claim = l.copies + align256(sizeof(int4) * size_t(B));
     l.free_list = l.claim + align256(sizeof(int32_t) * size_t(num_pages));
     l.total = l.free_list + align256(sizeof(int32_t) * size_t(num_pages));
     return l;
@@ -327,11 +376,14 @@ cudaError_t launch_update_pages(const dspark_pages &p, int sms, cudaStream_t s) 
     const dspark_cache &c = p.cache;
     char *ws = static_cast<char *>(p.workspace);
     const PagesLayout l = pages_layout(p.B, c.num_pages);
+    uint32_t shift = 31;  // exact below 2^31: mul = ceil(2^shift / page_size) < 2^32
+    while ((1u << (shift - 31)) < unsigned(c.page_size)) ++shift;
+    const uint32_t mul = uint32_t(((1ull << shift) + c.page_size - 1) / c.page_size);
     PagesArgs A{p.B_in, p.B, p.max_pages, c.num_pages, c.page_size,
-                int((int64_t(p.sinks) + c.page_size - 1) / c.page_size), p.table_in, p.parent, p.keep_len,
+                int((int64_t(p.sinks) + c.page_size - 1) / c.page_size), mul, shift, p.table_in, p.parent, p.keep_len,
                 p.want_len, p.first_pos, p.held, p.table_out, p.granted_len, p.tail_src, p.tail_dst, p.totals,
                 reinterpret_cast<int32_t *>(ws + l.claim), reinterpret_cast<int32_t *>(ws + l.free_list),
-                reinterpret_cast<int2 *>(ws + l.start), reinterpret_cast<int4 *>(ws + l.copies),
+                reinterpret_cast<int4 *>(ws + l.copies),
                 reinterpret_cast<int32_t *>(ws) + 1};
     constexpr int kCtas = 16;
     cudaError_t e = cudaFuncSetAttribute(update_pages_kernel<kCtas>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -340,7 +392,7 @@ cudaError_t launch_update_pages(const dspark_pages &p, int sms, cudaStream_t s) 
     if (e != cudaSuccess || !c.k_cache) return e;
     const CopyArgs C{c.layers, c.Hkv, c.D / 8, c.layer_stride, c.page_stride, c.slot_stride, c.head_stride,
                      static_cast<uint16_t *>(c.k_cache), static_cast<uint16_t *>(c.v_cache), A.copies, A.n_copies};
-    return launch_overlapped(copy_tails_kernel, 8 * sms, kThreadsCopy, 0, s, C);
+    return launch_overlapped(copy_tails_kernel, 12 * sms, kThreadsCopy, 0, s, C);
 }
 
 }  // namespace dspark
