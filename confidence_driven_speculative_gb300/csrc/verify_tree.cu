@@ -26,12 +26,14 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreadsTree = 256;
+constexpr int kThreadsAll = 256;    // verify_tree_all_kernel
+constexpr int kThreadsWalk = 128;   // verify_tree_kernel
+constexpr int kResident = 4;        // its CTAs of an SM
 constexpr int kMaxCluster = 16;
 // Bytes of all rows up to which they are read at once.
 constexpr size_t kAllBytes = size_t(24) << 20;
 constexpr int kAllRequests = 1024;  // and requests
-constexpr int kTreeLoads = 8;       // 16-byte loads of a thread in flight
+constexpr int kLoadsAll = 8, kLoadsWalk = 16;  // 16-byte loads of a thread in flight
 
 struct TreeArgs {
     int B, rows, q_max, V;
@@ -62,12 +64,27 @@ __device__ __forceinline__ Key warp_max(Key k) {
     return k;
 }
 
-// The largest key of the 16-byte vectors first, first + stride, .. below end of a row, for this thread.
-template <typename T>
+// The largest of a 16-byte vector's elements.
+template <typename T> __device__ __forceinline__ float vector_max(const uint4 &x);
+template <> __device__ __forceinline__ float vector_max<uint16_t>(const uint4 &x) {
+    uint32_t m;
+    asm("{\n\t.reg .b32 a, b;\n\t"
+        "max.bf16x2 a, %1, %2;\n\tmax.bf16x2 b, %3, %4;\n\tmax.bf16x2 %0, a, b;\n\t}"
+        : "=r"(m) : "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w));
+    return fmaxf(bf16_lo(m), bf16_hi(m));
+}
+template <> __device__ __forceinline__ float vector_max<float>(const uint4 &x) {
+    return fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)), fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
+}
+
+// The largest key of the 16-byte vectors first, first + stride, .. below end of a row, for this thread.  A
+// vector is taken apart only at the end, the one that holds the maximum.
+template <typename T, int kTreeLoads>
 __device__ __forceinline__ Key best_of(const uint4 *row, int first, int end, int stride) {
     constexpr int E = Vec<T>::kElems;
     float v = -INFINITY;
     int at = -1;
+    uint4 best = make_uint4(0, 0, 0, 0);
     for (int c0 = first; c0 < end; c0 += kTreeLoads * stride) {
         uint4 x[kTreeLoads];
 #pragma unroll
@@ -76,19 +93,22 @@ __device__ __forceinline__ Key best_of(const uint4 *row, int first, int end, int
 #pragma unroll
         for (int k = 0; k < kTreeLoads; ++k) {
             if (c0 + k * stride >= end) break;
-            float z[E];
-            Vec<T>::unpack(x[k], z);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                // ids ascend, so the first of equals stays
-                if (z[e] > v || at < 0) {
-                    v = z[e];
-                    at = (c0 + k * stride) * E + e;
-                }
+            const float m = vector_max<T>(x[k]);
+            if (m > v || at < 0) {  // vectors ascend, so the first of equals stays
+                v = m;
+                at = c0 + k * stride;
+                best = x[k];
             }
         }
     }
-    return at < 0 ? 0 : make_key(v, at);
+    if (at < 0) return 0;
+    float z[E];
+    Vec<T>::unpack(best, z);
+    int e = 0;
+#pragma unroll
+    for (int k = E - 1; k >= 0; --k)
+        if (z[k] == v) e = k;
+    return make_key(v, at * E + e);
 }
 
 // The lowest child of row `at` whose token is y; -1: none.  Lane j holds rows j and 32 + j.
@@ -144,8 +164,8 @@ struct Walk {
 
 // A cluster walks one request's tree, row by row.
 template <typename T>
-__global__ void __launch_bounds__(kThreadsTree) verify_tree_kernel(const TreeArgs A) {
-    constexpr int kWarpsTree = kThreadsTree / 32;
+__global__ void __launch_bounds__(kThreadsWalk, kResident) verify_tree_kernel(const TreeArgs A) {
+    constexpr int kWarpsTree = kThreadsWalk / 32;
     __shared__ Key keys[2][kMaxCluster * kWarpsTree];  // by level % 2: of all warps of the cluster
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int rank, size;
@@ -164,7 +184,7 @@ __global__ void __launch_bounds__(kThreadsTree) verify_tree_kernel(const TreeArg
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     while (at >= 0) {
         const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const T *>(A.logits) + int64_t(r.row0 + at) * A.V);
-        Key k = warp_max(best_of<T>(row, rank * kThreadsTree + tid, vecs, size * kThreadsTree));
+        Key k = warp_max(best_of<T, kLoadsWalk>(row, rank * kThreadsWalk + tid, vecs, size * kThreadsWalk));
         Key *const mine = &keys[walk.len & 1][rank * kWarpsTree + warp];
         if (lane < size)
             asm volatile(
@@ -187,8 +207,8 @@ __global__ void __launch_bounds__(kThreadsTree) verify_tree_kernel(const TreeArg
 
 // All rows at once.
 template <typename T>
-__global__ void __launch_bounds__(kThreadsTree) verify_tree_all_kernel(const TreeArgs A) {
-    __shared__ Key keys[kThreadsTree / 32];
+__global__ void __launch_bounds__(kThreadsAll) verify_tree_all_kernel(const TreeArgs A) {
+    __shared__ Key keys[kThreadsAll / 32];
     __shared__ int last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -202,11 +222,11 @@ __global__ void __launch_bounds__(kThreadsTree) verify_tree_all_kernel(const Tre
     }
     const int vecs = A.V / Vec<T>::kElems, each = (vecs + A.parts - 1) / A.parts;
     const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const T *>(A.logits) + int64_t(r.row0 + j) * A.V);
-    Key k = warp_max(best_of<T>(row, part * each + tid, min((part + 1) * each, vecs), kThreadsTree));
+    Key k = warp_max(best_of<T, kLoadsAll>(row, part * each + tid, min((part + 1) * each, vecs), kThreadsAll));
     if (lane == 0) keys[warp] = k;
     __syncthreads();
     if (warp > 0) return;
-    k = warp_max(lane < kThreadsTree / 32 ? keys[lane] : 0);
+    k = warp_max(lane < kThreadsAll / 32 ? keys[lane] : 0);
     if (lane == 0) {
         atomicMax(A.key + r.row0 + j, k);
         __threadfence();
@@ -246,17 +266,17 @@ cudaError_t launch(TreeArgs A, size_t together, int sms, cudaStream_t s) {
     // all in one wave of CTAs
     if (together && A.B * A.q_max <= 8 * sms) {
         A.parts = std::max(1, std::min(4 * sms / (A.B * A.q_max), A.V / 2048));
-        return launch_overlapped(verify_tree_all_kernel<T>, A.B * A.q_max * A.parts, kThreadsTree, 0, s, A);
+        return launch_overlapped(verify_tree_all_kernel<T>, A.B * A.q_max * A.parts, kThreadsAll, 0, s, A);
     }
     int size = kMaxCluster;
     // one wave too, and no thread without a vector of the row
-    while (size > 1 && (A.B * size > 8 * sms || size / 2 * kThreadsTree >= A.V / Vec<T>::kElems)) size /= 2;
+    while (size > 1 && (A.B * size > kResident * sms || size / 2 * kThreadsWalk >= A.V / Vec<T>::kElems)) size /= 2;
     if (size > 8) {
         const cudaError_t e =
             cudaFuncSetAttribute(verify_tree_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
-    return launch_clusters(verify_tree_kernel<T>, A.B * size, kThreadsTree, size, s, A);
+    return launch_clusters(verify_tree_kernel<T>, A.B * size, kThreadsWalk, size, s, A);
 }
 
 }  // namespace
