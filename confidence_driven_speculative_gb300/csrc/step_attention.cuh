@@ -287,7 +287,8 @@ struct TreeRow {
     int pos;
     __device__ __forceinline__ TreeRow(const StepArgs &A, const Req &q, int j, bool there) : seen(0), pos(q.pos0) {
         if (!there) return;
-        seen = A.row_seen[q.row0 + j];
+        // (asked for here, and not where it is used first)
+        asm volatile("ld.global.b64 %0, [%1];" : "=l"(seen) : "l"(A.row_seen + q.row0 + j));
         if (A.window > 0) pos = max(A.packed_pos[q.row0 + j], q.pos0);
     }
     // Which of the 32 keys from k0 on it sees.

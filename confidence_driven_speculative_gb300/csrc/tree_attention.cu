@@ -35,7 +35,8 @@ constexpr int kSlotsT = 10;      // ring slots at most
 constexpr int kParts = 4;        // parts on their way to the warps
 constexpr int kPartReaders = 19; // warps that read them
 constexpr int kBad = 8;          // ring of the tiles' bad-key words
-constexpr int kUnitCostT = 2;    // what a unit costs beside its tiles, in tiles
+// Places of the list: of a tile of one block, of one of two, and what a unit costs beside its tiles.
+constexpr int kTileOne = 2, kTileTwo = 3, kUnitPlaces = 10;
 
 // A unit that was cut, for the second kernel.
 struct Cut {
@@ -257,9 +258,10 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
 
     if (warp == kWarpTK) {
         // ---- the CTA's parts, their queries and keys ---------------------------
-        constexpr int U = kUnitCostT;
+        constexpr int U = kUnitPlaces;
         const int me = blockIdx.x, per = (A.B + 31) / 32, b_lo = min(lane * per, A.B), b_hi = min(b_lo + per, A.B);
-        auto cost_of = [&](const Req &r) { return r.blocks * A.Hkv * (r.nt + U); };
+        auto places_of = [&](const Req &r) { return r.per > A.rb ? kTileTwo : kTileOne; };  // of a tile
+        auto cost_of = [&](const Req &r) { return r.blocks * A.Hkv * (r.nt * places_of(r) + U); };
         int mine = 0;
 #pragma unroll 4
         for (int b = b_lo; b < b_hi; ++b) mine += cost_of(load_req<kTree>(A, b));
@@ -270,7 +272,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
             if (lane >= o) sum += x;
         }
         const int total = __shfl_sync(0xffffffffu, sum, 31);
-        const Cuts cuts(total, gridDim.x);
+        // (no CTA's share is shorter than a tile, so that a cut unit has a tile in each CTA from its first to its last)
+        const Cuts cuts(total, min(int(gridDim.x), max(total / kTileTwo, 1)));
         const int start = cuts.start(me), end = cuts.start(me + 1);
         const uint32_t who = __ballot_sync(0xffffffffu, start >= sum - mine && start < sum);
         int b = A.B, place = sum - mine;  // the request that holds `start`, and where it begins
@@ -292,13 +295,13 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
         bool ok = true;
         for (; b < A.B && place < end && ok; ++b) {
             const Req q = load_req<kTree>(A, b);
-            const int each = q.nt + U, units = q.blocks * A.Hkv;
+            const int w = places_of(q), each = q.nt * w + U, units = q.blocks * A.Hkv;
             int i = max(start - place, 0) / each;
             for (; i < units && place + i * each < end && ok; ++i) {
                 const int tile0 = place + i * each + U;  // the place of the unit's first tile
                 Part p;
-                p.t_beg = max(start - tile0, 0);
-                p.n = min(end - tile0, q.nt) - p.t_beg;
+                p.t_beg = (max(start - tile0, 0) + w - 1) / w;
+                p.n = min((max(end - tile0, 0) + w - 1) / w, q.nt) - p.t_beg;
                 if (p.n <= 0) continue;  // only its cost lies here
                 p.b = b;
                 p.h = i / q.blocks;
@@ -315,7 +318,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
                     // A unit that begins here and goes on is the CTA's last, one that goes on here its first.
                     p.slot = 2 * me + (p.t_beg == 0);
                     if (p.t_beg == 0 && lane == 0)
-                        A.cuts[me] = Cut{p.row0, p.h * A.G, p.nrows * A.G, cuts.of(tile0 + q.nt - 1) - me + 1};
+                        A.cuts[me] = Cut{p.row0, p.h * A.G, p.nrows * A.G, cuts.of(tile0 + (q.nt - 1) * w) - me + 1};
                 }
                 int last_pos = q.pos0;
                 if (A.window > 0) {
@@ -838,11 +841,61 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
 }
 
 constexpr int kThreadsJoin = 256;
-constexpr int kJoinEntries = 4;  // that a thread adds, of its column
-constexpr int kJoinParts = 8;    // parts whose entries it has asked for at once
 
-// Adds the parts of the units that were cut, in the order of the keys.  A warp takes 32 columns, a lane each, and
-// kJoinEntries of their entries.
+// Adds the parts of a cut unit in the order of the keys: for column n, entries d .. d + kEntries - 1.  The loads of
+// kParts parts are in flight at once.
+template <int D, int kEntries, int kParts>
+__device__ __forceinline__ void join_entries(const TreeArgs &A, const Cut &cut, int first_cta, int n, int d) {
+    float top = kRefMin, l = 0.f, acc[kEntries] = {};
+    for (int k0 = 0; k0 < cut.members; k0 += kParts) {
+        float ref[kParts], sum[kParts], o[kParts][kEntries];
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+            ref[k] = kRefMin;
+            sum[k] = 0.f;
+#pragma unroll
+            for (int e = 0; e < kEntries; ++e) o[k][e] = 0.f;
+            if (k0 + k < cut.members) {
+                // (2 * kAttnMaxCtas * 128 * 256 floats at most: 32 bits)
+                const uint32_t slot = k0 + k == 0 ? 2 * first_cta + 1 : 2 * (first_cta + k0 + k);
+                const float *stat = A.stat + slot * 2 * A.ncap + n, *part = A.part + (slot * D + d) * A.ncap + n;
+                ref[k] = __ldcg(stat);
+                sum[k] = __ldcg(stat + A.ncap);
+#pragma unroll
+                for (int e = 0; e < kEntries; ++e) {
+                    o[k][e] = __ldcg(part);
+                    part += A.ncap;
+                }
+            }
+        }
+        float now = top;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) now = fmaxf(now, ref[k]);
+        const float f = exp2_approx((top - now) * A.scale2);
+        top = now;
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) acc[e] *= f;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+            const float w = exp2_approx((ref[k] - now) * A.scale2);
+            l = fmaf(w, sum[k], l);
+#pragma unroll
+            for (int e = 0; e < kEntries; ++e) acc[e] = fmaf(w, o[k][e], acc[e]);
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t *out = reinterpret_cast<uint32_t *>(
+        A.out + ((int64_t)(cut.row0 + n / A.G) * A.Hq + cut.head0 + n % A.G) * D + d);
+#pragma unroll
+    for (int e = 0; e < kEntries; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+}
+
+// A warp takes 32 columns of a unit, a lane each, and some of their entries: 16 where there are up to three parts,
+// 4 where there are more, so that some 50 loads are in flight either way.  (For one request's 19 parts of 240 columns
+// 2, 4 and 8 entries: 27.3, 25.1 and 29.1 us for the call; 2 entries are bound by their instructions.)
+constexpr int kFewParts = 3, kEntriesFew = 16, kManyParts = 10, kEntriesMany = 4;
+
 template <int D>
 __global__ void __launch_bounds__(kThreadsJoin) join_parts_kernel(const TreeArgs A, int ctas) {
     static_assert(kAttnMaxCtas <= kThreadsJoin, "a thread for each CTA's unit");
@@ -852,7 +905,8 @@ __global__ void __launch_bounds__(kThreadsJoin) join_parts_kernel(const TreeArgs
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Cut mine{0, 0, 0, 0};
     if (tid < ctas) mine = A.cuts[tid];
-    const int groups = mine.members > 1 ? (mine.ncols + 31) / 32 * (D / kJoinEntries) : 0;
+    auto each = [](int members) { return D / (members <= kFewParts ? kEntriesFew : kEntriesMany); };
+    const int groups = mine.members > 1 ? (mine.ncols + 31) / 32 * each(mine.members) : 0;
     int x = groups;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -872,45 +926,10 @@ __global__ void __launch_bounds__(kThreadsJoin) join_parts_kernel(const TreeArgs
         for (int o = kThreadsJoin / 2; o > 0; o >>= 1)
             if (before[u + o] <= i) u += o;
         const Cut cut = A.cuts[u];
-        const int g = i - before[u], n = g / (D / kJoinEntries) * 32 + lane, d = g % (D / kJoinEntries) * kJoinEntries;
+        const int g = i - before[u], parts = each(cut.members), n = g / parts * 32 + lane, d = g % parts;
         if (n >= cut.ncols) continue;
-        auto slot_of = [&](int k) { return int64_t(k == 0 ? 2 * u + 1 : 2 * (u + k)); };
-        float top = kRefMin, l = 0.f, acc[kJoinEntries] = {};
-        for (int k0 = 0; k0 < cut.members; k0 += kJoinParts) {
-            float ref[kJoinParts], sum[kJoinParts], o[kJoinParts][kJoinEntries];
-#pragma unroll
-            for (int k = 0; k < kJoinParts; ++k) {
-                ref[k] = kRefMin;
-                sum[k] = 0.f;
-#pragma unroll
-                for (int e = 0; e < kJoinEntries; ++e) o[k][e] = 0.f;
-                if (k0 + k < cut.members) {
-                    const int64_t slot = slot_of(k0 + k);
-                    ref[k] = __ldcg(A.stat + slot * 2 * A.ncap + n);
-                    sum[k] = __ldcg(A.stat + (slot * 2 + 1) * A.ncap + n);
-#pragma unroll
-                    for (int e = 0; e < kJoinEntries; ++e) o[k][e] = __ldcg(A.part + (slot * D + d + e) * A.ncap + n);
-                }
-            }
-            float now = top;
-#pragma unroll
-            for (int k = 0; k < kJoinParts; ++k) now = fmaxf(now, ref[k]);
-            const float f = exp2_approx((top - now) * A.scale2);
-            top = now;
-            l *= f;
-#pragma unroll
-            for (int e = 0; e < kJoinEntries; ++e) acc[e] *= f;
-#pragma unroll
-            for (int k = 0; k < kJoinParts; ++k) {
-                const float w = exp2_approx((ref[k] - now) * A.scale2);
-                l = fmaf(w, sum[k], l);
-#pragma unroll
-                for (int e = 0; e < kJoinEntries; ++e) acc[e] = fmaf(w, o[k][e], acc[e]);
-            }
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        *reinterpret_cast<uint2 *>(A.out + ((int64_t)(cut.row0 + n / A.G) * A.Hq + cut.head0 + n % A.G) * D + d) =
-            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+        if (cut.members <= kFewParts) join_entries<D, kEntriesFew, kFewParts>(A, cut, u, n, d * kEntriesFew);
+        else join_entries<D, kEntriesMany, kManyParts>(A, cut, u, n, d * kEntriesMany);
     }
 }
 
@@ -941,6 +960,13 @@ size_t cuts_at(int Hq, int Hkv, int D, int q_max) {
 }
 
 }  // namespace
+
+bool tree_list_fits(const dspark_attn &a) {
+    const int rows = unit_rows(a.Hq, a.Hkv, a.q_max);
+    const long long units = (a.q_max + rows - 1) / rows + 1;
+    const long long places = ((long long)a.max_pages * a.page_size / kTile + 2) * kTileTwo + kUnitPlaces;
+    return places * units * a.Hkv <= INT32_MAX / a.B;
+}
 
 size_t tree_attn_workspace_bytes(int Hq, int Hkv, int D, int q_max) {
     return cuts_at(Hq, Hkv, D, q_max) + sizeof(Cut) * kAttnMaxCtas;
