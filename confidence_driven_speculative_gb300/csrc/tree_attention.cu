@@ -340,19 +340,6 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
                 ++published;
                 typename Tiles<D, kBox>::Ids ids, ahead;
                 tiles.look_up(A, b, q, p.t_beg, lane, ids);
-                for (int x = 0; x < p.blocks && ok; ++x, ++q_use) {
-                    const int s = q_use & 1;
-                    if (q_use >= 2) ok = wait_or_give_up(&C.q_empty[s], ((q_use >> 1) - 1) & 1, A.wait_ns, gave_up);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&C.q_full[s], uint32_t(A.rb * A.G) * D * 2);
-                        for (int hf = 0; hf < kHalves; ++hf)
-                            tma_load_3d(q_smem + s * kSlotBytes + hf * kHalfBytes, &q_map, &C.q_full[s], hf * 64, p.h * A.G,
-                                        p.row0 + x * A.rb);
-                    }
-                    __syncwarp();
-                }
                 for (int t = 0; t < p.n && ok; ++t) {
                     if (t + 1 < p.n) tiles.look_up(A, b, q, p.t_beg + t + 1, lane, ahead);
                     if (issued >= A.k_slots) ok = wait_or_give_up(&C.empty[rk.slot], rk.phase ^ 1, A.wait_ns, gave_up);
@@ -363,6 +350,20 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
                     rk.next(A.k_slots);
                     ++issued;
                     ids = ahead;
+                    // the queries behind the first keys: they wait until the part before has no use for theirs
+                    for (int x = 0; t == 0 && x < p.blocks && ok; ++x, ++q_use) {
+                        const int s = q_use & 1;
+                        if (q_use >= 2) ok = wait_or_give_up(&C.q_empty[s], ((q_use >> 1) - 1) & 1, A.wait_ns, gave_up);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&C.q_full[s], uint32_t(A.rb * A.G) * D * 2);
+                            for (int hf = 0; hf < kHalves; ++hf)
+                                tma_load_3d(q_smem + s * kSlotBytes + hf * kHalfBytes, &q_map, &C.q_full[s], hf * 64, p.h * A.G,
+                                            p.row0 + x * A.rb);
+                        }
+                        __syncwarp();
+                    }
                 }
             }
             place += units * each;
@@ -412,40 +413,25 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
         if (lane == 0) C.issued[1] = issued;
     } else if (warp == kWarpTMma) {
         // ---- MMA issuer: O of a job, then S of the stream's next one -----------------
+        // A part's first two S come when all products of the part before are on their way: whoever
+        // computes its outputs waits for those, and not for the next part's queries and keys.
         const uint64_t qd0 = smem_desc(q_smem, 16, 1024), kd0 = smem_desc(ring, 16, 1024);
         const uint64_t vd0 = smem_desc(v_ring, kHalfBytes, 1024);
         constexpr uint32_t id_s = mma_idesc(128, kTile, false, false), id_o = mma_idesc(128, D, false, true);
-        enum : int { kFirst = 1, kLast = 2, kTileDone = 4 };  // of a stream's jobs in a part; of a tile's jobs
         PartReader parts;
         Ring rk, rv;
-        bool ok = true, more = true;
-        int n = 0, blocks = 1, k = 0, q_use = 0;  // the part of the next S, its job, its first query block
-        int flags[2] = {0, 0};                    // of each stream's job whose O is next
         uint32_t p_phase[2] = {0, 0};
+        bool ok = true;
+        int n = 0, blocks = 1, job0 = 0, q_use = 0;  // the part: its jobs, ..., its first query block
         auto wait = [&](uint64_t *bar, uint32_t phase) {
             ok = ok && wait_or_give_up(bar, phase, A.wait_ns, gave_up);
             ok = __all_sync(0xffffffffu, ok);
         };
-        // S of the next job on stream a, if there is one.  k_wait: its K may not be there yet.
-        auto next_s = [&](auto stream, bool k_wait) {
+        // S of job k, on stream a.
+        auto issue_s = [&](auto stream, int k) {
             constexpr int a = decltype(stream)::value;
-            if (more && k == n) {
-                ok = ok && parts.next(C, A, gave_up, lane, [&](const Part &p) {
-                    n = __shfl_sync(0xffffffffu, p.jobs, 0);
-                    blocks = __shfl_sync(0xffffffffu, p.blocks, 0);
-                    q_use = __shfl_sync(0xffffffffu, p.q_use, 0);
-                    more = __shfl_sync(0xffffffffu, p.n, 0) > 0;
-                });
-                k = 0;
-            }
-            flags[a] = 0;
-            if (!more || !ok) return false;
             const int x = blocks == 2 ? k & 1 : 0, u = q_use + x;  // the query block
-            if (k < blocks) wait(&C.q_full[u & 1], (u >> 1) & 1);
-            if (k_wait) wait(&C.full[rk.slot], rk.phase);
-            if (!ok) return false;
             const bool tile_done = blocks == 1 || x == 1;
-            flags[a] = (k < 2 ? kFirst : 0) | (k + 2 >= n ? kLast : 0) | (tile_done ? kTileDone : 0);
             tc_fence_after();
             if (elect_one()) {
                 mbar_arrive(&C.s_full[a]);  // passes the producer's words on
@@ -462,86 +448,94 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
             }
             __syncwarp();
             if (tile_done) rk.next(A.k_slots);
-            ++k;
-            return true;
         };
-        // O of the stream's pending job, and its next S; false: there is none.
-        bool pending[2] = {false, false};
-        auto step = [&](auto stream) {
+        // One of a part's first two jobs: its queries and keys are waited for here.
+        auto first_s = [&](auto stream, int k) {
+            const int u = q_use + (blocks == 2 ? k & 1 : 0);
+            if (k < blocks) wait(&C.q_full[u & 1], (u >> 1) & 1);
+            wait(&C.full[rk.slot], rk.phase);
+            if (ok) issue_s(stream, k);
+        };
+        // O of job k on stream a, and S of job k + 2.
+        auto step = [&](auto stream, int k) {
             constexpr int a = decltype(stream)::value;
-            if (!pending[a]) return false;
             wait(&C.p_full[a], p_phase[a]);
-            if (!ok) return false;
+            if (!ok) return;
             p_phase[a] ^= 1;
+            const bool tile_done = blocks == 1 || (k & 1), more = k + 2 < n;
             tc_fence_after();
-            const int f = flags[a];
             if (elect_one()) {
                 const uint64_t vd = vd0 + uint32_t(rv.slot) * (kSlotBytes >> 4);
 #pragma unroll
                 for (int i = 0; i < kTile / 16; ++i)
-                    mma_ts(tmem + kColO + a * D, tmem + a * kTile + i * 8, vd + i * (2048 >> 4), id_o, !((f & kFirst) && i == 0));
-                if (f & kTileDone) mma_commit(&C.empty[A.k_slots + rv.slot]);
-                if (f & kLast) {
+                    mma_ts(tmem + kColO + a * D, tmem + a * kTile + i * 8, vd + i * (2048 >> 4), id_o, !(k < 2 && i == 0));
+                if (tile_done) mma_commit(&C.empty[A.k_slots + rv.slot]);
+                if (!more) {
                     mbar_arrive(&C.o_full[a]);  // passes on what was lost of V
                     mma_commit(&C.o_full[a]);
                 }
             }
             __syncwarp();
-            if (f & kTileDone) rv.next(A.v_slots);
-            pending[a] = next_s(stream, false);
-            return true;
+            if (tile_done) rv.next(A.v_slots);
+            if (more) issue_s(stream, k + 2);
         };
-        pending[0] = next_s(Stream<0>{}, true);
-        pending[1] = pending[0] && next_s(Stream<1>{}, true);
-        while (step(Stream<0>{}) && step(Stream<1>{})) {}
+        auto whole_part = [&](auto even, auto odd) {  // the streams of its even and odd jobs
+            first_s(even, 0);
+            if (ok && n > 1) first_s(odd, 1);
+            for (int k = 0; ok && k < n; k += 2) {
+                step(even, k);
+                if (ok && k + 1 < n) step(odd, k + 1);
+            }
+        };
+        while (ok) {
+            ok = parts.next(C, A, gave_up, lane, [&](const Part &p) {
+                n = __shfl_sync(0xffffffffu, p.jobs, 0);
+                blocks = __shfl_sync(0xffffffffu, p.blocks, 0);
+                job0 = __shfl_sync(0xffffffffu, p.job0, 0);
+                q_use = __shfl_sync(0xffffffffu, p.q_use, 0);
+                if (__shfl_sync(0xffffffffu, p.n, 0) == 0) n = 0;
+            });
+            if (!ok || n == 0) break;
+            if (job0 & 1) whole_part(Stream<1>{}, Stream<0>{});
+            else whole_part(Stream<0>{}, Stream<1>{});
+        }
     } else if (warp == kWarpTReady) {
-        // ---- the last of P's arrivals: V of its tile and K of the stream's next job are
-        // there, so that the MMA issuer has one barrier to test and not three ----------
+        // ---- the last of P's arrivals: V of its tile and K of the stream's next job in the part
+        // are there, so that the MMA issuer has one barrier to test and not three ----------
         PartReader parts;
         Ring rk, rv;
         uint32_t uses[2] = {0, 0};
-        bool ok = true, more = true, first = true;
-        int n = 0, blocks = 1, k = 0;
-        bool done[2] = {false, false}, pending[2] = {false, false};  // of the two jobs whose V is next: the tile's last? are there any?
-        auto next_k = [&](auto stream) {
-            constexpr int a = decltype(stream)::value;
-            if (more && k == n) {
-                ok = ok && parts.next(C, A, gave_up, lane, [&](const Part &p) {
-                    n = p.jobs;
-                    blocks = p.blocks;
-                    more = p.n > 0;
-                });
-                k = 0;
+        bool ok = true;
+        int keys = 0, tiles_before = 0;  // tiles whose K was waited for (each in turn: a parity tells two uses apart)
+        while (ok) {
+            int n = 0, blocks = 1, job0 = 0;
+            ok = parts.next(C, A, gave_up, lane, [&](const Part &p) {
+                n = p.n ? p.jobs : 0;
+                blocks = p.blocks;
+                job0 = p.job0;
+            });
+            if (!ok || n == 0) break;
+            for (int k = 0; ok && k < n; ++k) {
+                const int a = (job0 + k) & 1, want = min(k + 2, n - 1);
+                for (const int last = tiles_before + (blocks == 2 ? want >> 1 : want); ok && keys <= last; ++keys) {
+                    ok = keys == 0 ? poll_or_give_up(&C.full[rk.slot], rk.phase, A.wait_ns, gave_up)
+                                   : wait_or_give_up(&C.full[rk.slot], rk.phase, A.wait_ns, gave_up);
+                    ok = __all_sync(0xffffffffu, ok);
+                    rk.next(A.k_slots);
+                }
+                ok = ok && wait_or_give_up(&C.full[A.k_slots + rv.slot], rv.phase, A.wait_ns, gave_up);
+                if (blocks == 1 || (k & 1)) rv.next(A.v_slots);
+                // not before the stream's job before is through
+                if ((a ? uses[1] : uses[0]) > 0)
+                    ok = ok && wait_or_give_up(&C.p_full[a], ((a ? uses[1] : uses[0]) - 1) & 1, A.wait_ns, gave_up);
+                uses[0] += a == 0;
+                uses[1] += a == 1;
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok && lane == 0) mbar_arrive(&C.p_full[a]);
+                __syncwarp();
             }
-            if (!more || !ok) return false;
-            ok = first ? poll_or_give_up(&C.full[rk.slot], rk.phase, A.wait_ns, gave_up)
-                       : wait_or_give_up(&C.full[rk.slot], rk.phase, A.wait_ns, gave_up);
-            ok = __all_sync(0xffffffffu, ok);
-            first = false;
-            done[a] = blocks == 1 || (k & 1);
-            if (done[a]) rk.next(A.k_slots);
-            ++k;
-            return ok;
-        };
-        auto step = [&](auto stream) {
-            constexpr int a = decltype(stream)::value;
-            if (!pending[a]) return false;
-            ok = wait_or_give_up(&C.full[A.k_slots + rv.slot], rv.phase, A.wait_ns, gave_up);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return false;
-            if (done[a]) rv.next(A.v_slots);
-            pending[a] = next_k(stream);
-            // not before the stream's job before is through
-            if (uses[a] > 0) ok = ok && wait_or_give_up(&C.p_full[a], (uses[a] - 1) & 1, A.wait_ns, gave_up);
-            ++uses[a];
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok && lane == 0) mbar_arrive(&C.p_full[a]);
-            __syncwarp();
-            return ok;
-        };
-        pending[0] = next_k(Stream<0>{});
-        pending[1] = pending[0] && next_k(Stream<1>{});
-        while (step(Stream<0>{}) && step(Stream<1>{})) {}
+            tiles_before += blocks == 2 ? n / 2 : n;
+        }
     } else {
         // ---- softmax and output --------------------------------------------------
         // Two threads share a vector of stream a: thread `half` takes 64 keys of
@@ -609,38 +603,27 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
                 __syncwarp();
                 ++s_uses;
                 tc_fence_after();
-                float s[kKeys];
-#pragma unroll
-                for (int c = 0; c < kKeys; c += 32) tmem_ld32(s + c, s_tm + half * kKeys + c);
                 const uint4 bw = *reinterpret_cast<const uint4 *>(C.bad[(tiles_before + t) % kBad]);
                 const bool edge = tile >= whole_hi || !(tile >= whole_lo || (tile + 1) * kTile <= A.sinks);
                 const bool cut = edge || (bw.x | bw.y | bw.z | bw.w) != 0;
-                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                for (int c = 0; c < kKeys; c += 32) tmem_use32(s + c);
-                if (__builtin_expect(cut, 0)) {
-#pragma unroll
-                    for (int c = 0; c < kKeys; c += 32) {
-                        const uint32_t bad = half ? (c ? bw.w : bw.z) : (c ? bw.y : bw.x);
-                        const uint32_t seen = valid ? mine.word(A, q, tile * kTile + half * kKeys + c) & ~bad : 0u;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(seen >> e & 1)) s[c + e] = -INFINITY;
-                    }
+                if (__builtin_expect(cut, 0) && (blocks == 1 || k0 == 0)) {
                     // Masked keys must not reach O through 0 * infinity: the tile's values lose their NaN
                     // and infinities; the rows that see them get them back at the part's end.  Where both
                     // streams use the tile, the one with its first job does it for both: its P comes
                     // before either's products.  (S of this job says that the products of V's use of this
                     // slot before are through, so that the parity tells whether V is there.)
-                    if (blocks == 1 || k0 == 0) {
-                        const int use = tiles_before + t, vs = use % A.v_slots;
-                        wait_or_give_up(&C.full[A.k_slots + vs], (use / A.v_slots) & 1, A.wait_ns, gave_up);
-                        __syncwarp();
-                        const uint32_t at0 = v_ring + vs * kSlotBytes + (half * kTile + row) * 16;
+                    const int use = tiles_before + t, vs = use % A.v_slots;
+                    wait_or_give_up(&C.full[A.k_slots + vs], (use / A.v_slots) & 1, A.wait_ns, gave_up);
+                    __syncwarp();
+                    const uint32_t at0 = v_ring + vs * kSlotBytes + (half * kTile + row) * 16;
+                    bool odd = false;
+#pragma unroll
+                    for (uint32_t c = 0; c < kSlotBytes; c += 2 * kTile * 16) odd |= nonfinite_any(ld_shared16(at0 + c));
+                    if (__builtin_expect(odd, 0)) {
 #pragma unroll 1
                         for (uint32_t c = 0; c < kSlotBytes; c += 2 * kTile * 16) {
                             const uint4 v = ld_shared16(at0 + c);
-                            if (__builtin_expect(!nonfinite_any(v), 1)) continue;
+                            if (!nonfinite_any(v)) continue;
                             st_shared16(at0 + c, v.x & ~nonfinite_mask(v.x), v.y & ~nonfinite_mask(v.y),
                                         v.z & ~nonfinite_mask(v.z), v.w & ~nonfinite_mask(v.w));
                             // what no copy has brought, or lies outside the sequence, is not missed
@@ -651,6 +634,23 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
                             }
                         }
                         fence_async_shared();
+                    }
+                }
+                float s[kKeys];
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) tmem_ld32(s + c, s_tm + half * kKeys + c);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) tmem_use32(s + c);
+                if (__builtin_expect(cut, 0)) {
+#pragma unroll
+                    for (int c = 0; c < kKeys; c += 32) {
+                        const uint32_t bad = half ? (c ? bw.w : bw.z) : (c ? bw.y : bw.x);
+                        const uint32_t seen = valid ? mine.word(A, q, tile * kTile + half * kKeys + c) & ~bad : 0u;
+                        if (__all_sync(0xffffffffu, seen == 0xffffffffu || !valid)) continue;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(seen >> e & 1)) s[c + e] = -INFINITY;
                     }
                 }
                 float m0 = max3(s[0], s[1], s[2]), m1 = max3(s[3], s[4], s[5]);
