@@ -108,8 +108,9 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 template <int D, bool kBox>
 struct Tiles {
     int span, boxes;
+    uint64_t policy;  // the cache's lines make way for the parts of cut units, which are read again
     struct Ids { int page[4]; };
-    __device__ __forceinline__ Tiles(const TreeArgs &A) : span(kBox ? A.box : 4), boxes(kTile / span) {}
+    __device__ __forceinline__ Tiles(const TreeArgs &A) : span(kBox ? A.box : 4), boxes(kTile / span), policy(evict_first()) {}
 
     __device__ __forceinline__ void look_up(const TreeArgs &A, int b, const Req &q, int t, int lane, Ids &ids) const {
         const int key0 = tile_at<kTree>(q, t) * kTile + lane * span;
@@ -173,8 +174,8 @@ struct Tiles {
             for (int j = box_lo; j < box_lo + box_n; ++j) {
                 const int page = __shfl_sync(0xffffffffu, row[0], j);
                 if (leader) {
-                    tma_load_4d(dst, map, full, 0, in_page, h, page);
-                    if (kHalves == 2) tma_load_4d(dst + kHalfBytes, map, full, 64, in_page, h, page);
+                    tma_load_4d(dst, map, full, 0, in_page, h, page, policy);
+                    if (kHalves == 2) tma_load_4d(dst + kHalfBytes, map, full, 64, in_page, h, page, policy);
                 }
                 dst += span * 128;
                 in_page += span;
@@ -187,8 +188,8 @@ struct Tiles {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) k[i] = __shfl_sync(0xffffffffu, row[i], j);
                 if (leader) {
-                    tma_gather4(dst, map, full, x0, k[0], k[1], k[2], k[3]);
-                    if (kHalves == 2) tma_gather4(dst + kHalfBytes, map, full, x0 + 64, k[0], k[1], k[2], k[3]);
+                    tma_gather4(dst, map, full, x0, k[0], k[1], k[2], k[3], policy);
+                    if (kHalves == 2) tma_gather4(dst + kHalfBytes, map, full, x0 + 64, k[0], k[1], k[2], k[3], policy);
                 }
                 dst += span * 128;
             }
@@ -846,6 +847,7 @@ constexpr int kThreadsJoin = 256;
 // kParts parts are in flight at once.
 template <int D, int kEntries, int kParts>
 __device__ __forceinline__ void join_entries(const TreeArgs &A, const Cut &cut, int first_cta, int n, int d) {
+    static_assert(kEntries == 16 || kEntries == 4, "one store");
     float top = kRefMin, l = 0.f, acc[kEntries] = {};
     for (int k0 = 0; k0 < cut.members; k0 += kParts) {
         float ref[kParts], sum[kParts], o[kParts][kEntries];
@@ -885,10 +887,12 @@ __device__ __forceinline__ void join_entries(const TreeArgs &A, const Cut &cut, 
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t *out = reinterpret_cast<uint32_t *>(
-        A.out + ((int64_t)(cut.row0 + n / A.G) * A.Hq + cut.head0 + n % A.G) * D + d);
+    uint16_t *const out = A.out + ((int64_t)(cut.row0 + n / A.G) * A.Hq + cut.head0 + n % A.G) * D + d;
+    uint32_t y[kEntries / 2];
 #pragma unroll
-    for (int e = 0; e < kEntries; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    for (int e = 0; e < kEntries; e += 2) y[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if constexpr (kEntries == 16) st_global32(out, y, A.wide_out);
+    else *reinterpret_cast<uint2 *>(out) = make_uint2(y[0], y[1]);
 }
 
 // A warp takes 32 columns of a unit, a lane each, and some of their entries: 16 where there are up to three parts,
