@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(PKG, "lib", "libdspark.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "score_budget.cu", "compact.cu", "verify.cu", "verify_small.cu", "sts_fit.cu",
            "tensor_map.cu", "rope_append.cu", "step_attention.cu", "prompt_attention.cu",
-           "step_attention_sinks.cu", "step_attention_tree.cu", "tree_attention.cu",
+           "step_attention_sinks.cu", "tree_attention.cu",
            "prompt_attention_sinks.cu", "verify_tree.cu", "commit_path.cu", "update_pages.cu"]
 
 

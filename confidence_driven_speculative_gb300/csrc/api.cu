@@ -748,7 +748,7 @@ dspark_status step_attention(const dspark_attn *a, const uint64_t *row_seen, boo
         return fail(DSPARK_EINVAL,
                     "%s: page_size=%d is not a multiple of 8, and page_stride or head_stride is not "
                     "a whole number of slots", fn, a->page_size);
-    if (!dspark::step_list_fits(*a) || (tree && !dspark::tree_list_fits(*a)))
+    if (!(tree ? dspark::tree_list_fits(*a) : dspark::step_list_fits(*a)))
         return fail(DSPARK_EINVAL, "%s: B=%d Hkv=%d max_pages=%d is too large a batch", fn, a->B, a->Hkv,
                     a->max_pages);
     if (tree) {

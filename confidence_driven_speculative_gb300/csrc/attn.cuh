@@ -29,8 +29,6 @@ cudaError_t launch_step_attention_tree(const dspark_attn &a, const uint64_t *row
 
 size_t tree_attn_workspace_bytes(int Hq, int Hkv, int D, int q_max);
 bool tree_list_fits(const dspark_attn &a);
-cudaError_t launch_tree_attention(const dspark_attn &a, const uint64_t *row_seen, int sinks, int sms, uint64_t wait_ns,
-                                  cudaStream_t s);
 cudaError_t launch_prompt_attention(const dspark_attn &a, int sms, uint64_t wait_ns, cudaStream_t s);
 cudaError_t launch_prompt_attention_sinks(const dspark_attn &a, int sinks, int sms, uint64_t wait_ns, cudaStream_t s);
 

@@ -25,7 +25,7 @@ bool step_list_fits(const dspark_attn &a) {
 }
 
 cudaError_t launch_step_attention(const dspark_attn &a, int sms, uint64_t wait_ns, cudaStream_t s) {
-    return launch_rows<kChain>(a, nullptr, 0, sms, wait_ns, s);
+    return launch_rows<kChain>(a, 0, sms, wait_ns, s);
 }
 
 }  // namespace dspark

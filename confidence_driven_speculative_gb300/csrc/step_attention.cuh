@@ -84,8 +84,7 @@ constexpr size_t kSmemBytes = 232448;  // shared memory of a CTA
 // What rows see of the keys up to their own.
 enum Seen : int {
     kChain,  // all, or the last `window` of them
-    kSinks,  // those and the first `sinks` keys
-    kTree    // of the cached keys as above; of the rows' own entries the set bits of a word
+    kSinks   // those and the first `sinks` keys
 };
 
 struct StepArgs {
@@ -105,8 +104,6 @@ struct StepArgs {
     int64_t page_stride, slot_stride, head_stride;
     const uint16_t *v_cache;
     const int32_t *row_off, *seq_lens, *block_table;
-    const int32_t *packed_pos;  // kTree with a window
-    const uint64_t *row_seen;   // kTree
     uint16_t *out;
     float *part;               // [2 * CTAs][ncap][D]
     float *stat;               // [2 * CTAs][2][ncap]: reference, sum
@@ -279,54 +276,6 @@ __device__ __forceinline__ void visible_columns(const StepArgs &A, const Unit<kS
         hi = int(min(max(min(j, (long long)u.q.n) * A.G, 0ll), (long long)u.ncols));
     }
     if (bad || (kpos < u.q.kbeg && !sink) || kpos >= u.q.kend) hi = lo;
-}
-
-// A tree's row: what it sees, and where its window ends (its position).
-struct TreeRow {
-    uint64_t seen;
-    int pos;
-    __device__ __forceinline__ TreeRow(const StepArgs &A, const Req &q, int j, bool there) : seen(0), pos(q.pos0) {
-        if (!there) return;
-        // (asked for here, and not where it is used first)
-        asm volatile("ld.global.b64 %0, [%1];" : "=l"(seen) : "l"(A.row_seen + q.row0 + j));
-        if (A.window > 0) pos = max(A.packed_pos[q.row0 + j], q.pos0);
-    }
-    // Which of the 32 keys from k0 on it sees.
-    __device__ __forceinline__ uint32_t word(const StepArgs &A, const Req &q, int k0) const {
-        auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
-        uint32_t cached = below(q.pos0 - k0);
-        if (A.window > 0) cached &= ~below(pos - A.window + 1 - k0) | below(A.sinks - k0);
-        const int at = k0 - q.pos0;  // the own entry that k0 is
-        const uint32_t own = at >= 64 || at <= -32 ? 0u : at >= 0 ? uint32_t(seen >> at) : uint32_t(seen) << -at;
-        return (cached | own) & below(q.kend - k0);
-    }
-};
-
-// Bit i of lane j's word becomes bit j of lane i's.
-__device__ __forceinline__ uint32_t transpose32(uint32_t x, int lane) {
-    uint32_t mask = 0x0000ffffu;
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
-        const uint32_t y = __shfl_xor_sync(0xffffffffu, x, m);
-        x = lane & m ? (x & ~mask) | ((y >> m) & mask) : (x & mask) | ((y & mask) << m);
-        mask ^= mask << (m >> 1);
-    }
-    return x;
-}
-
-// Bits of the columns n .. n + 15 whose rows are in `rows`.
-__device__ __forceinline__ uint32_t rows16(const StepArgs &A, uint64_t rows, int n) {
-    int j = n / A.G, g = n - j * A.G;
-    uint32_t seen = 0;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        seen |= (j < 64 ? uint32_t(rows >> j) & 1u : 0u) << e;
-        if (++g == A.G) {
-            g = 0;
-            ++j;
-        }
-    }
-    return seen;
 }
 
 // 16 columns of a tile, on their way from TMEM: weights 2^((s - ref) * scale2), rounded, to P; returns
@@ -901,19 +850,9 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
         for (int unit = 1; i < tiles; ++unit) {
             const int N = (u.ncols + 15) & ~15, t_first = t;
             const int here = min(u.q.nt - t, tiles - i);
-            // kTree: two rows of the unit to a lane
-            const int nrows = u.ncols / A.G;
-            const uint64_t all_rows = kSeen == kTree ? ~0ull >> (64 - nrows) : 0ull;
-            TreeRow row_a(A, u.q, u.j0 + lane, kSeen == kTree && lane < nrows);
-            TreeRow row_b(A, u.q, u.j0 + 32 + lane, kSeen == kTree && 32 + lane < nrows);
             // tiles that every column sees in full: [whole_lo, whole_hi), and those of sinks
-            int whole_hi = min(u.q.kend, u.q.pos0 + u.j0 + 1) / kTile;
-            int last_pos = u.q.pos0 + u.j0 + nrows - 1;
-            if (kSeen == kTree) {
-                whole_hi = min(u.q.kend, u.q.pos0) / kTile;
-                last_pos = __reduce_max_sync(0xffffffffu, max(row_a.pos, row_b.pos));
-            }
-            const int last_beg = A.window > 0 ? max(last_pos - A.window + 1, u.q.kbeg) : u.q.kbeg;
+            const int whole_hi = min(u.q.kend, u.q.pos0 + u.j0 + 1) / kTile;
+            const int last_beg = A.window > 0 ? max(u.q.pos0 + u.j0 + u.ncols / A.G - A.window, u.q.kbeg) : u.q.kbeg;
             const int whole_lo = (last_beg + kTile - 1) / kTile;
             for (int k = 0; k < here; ++k, ++t, ++i) {
                 const bool first = k == 0;
@@ -930,29 +869,17 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 const bool whole = (bw.x | bw.y | bw.z | bw.w) == 0 && tile < whole_hi &&
                                    (tile >= whole_lo || (kSeen != kChain && (tile + 1) * kTile <= A.sinks));
                 int lo = 0, hi = N;
-                uint64_t rows = 0;  // kTree: the rows that see the key
                 if (!whole) {
                     const int q = warp & 3;
                     const uint32_t word = q == 0 ? bw.x : q == 1 ? bw.y : q == 2 ? bw.z : bw.w;
-                    const bool bad = (word >> lane) & 1;
-                    if (kSeen == kTree) {
-                        const int k0 = tile * kTile + 32 * q;
-                        rows = transpose32(lane < nrows ? row_a.word(A, u.q, k0) : 0u, lane);
-                        if (nrows > 32)
-                            rows |= uint64_t(transpose32(32 + lane < nrows ? row_b.word(A, u.q, k0) : 0u, lane)) << 32;
-                        if (bad) rows = 0;
-                    } else {
-                        visible_columns<kSeen>(A, u, tile * kTile + key, bad, lo, hi);
-                    }
+                    visible_columns<kSeen>(A, u, tile * kTile + key, (word >> lane) & 1, lo, hi);
                 }
-                auto seen = [&](int n) { return kSeen == kTree ? rows16(A, rows, n) : seen16(n, lo, hi); };
-                const bool none = kSeen == kTree ? rows == 0 : lo >= hi;
                 bool move = first;
                 const int pb = A.two_p ? i & 1 : 0;
                 const uint32_t p_row = p_smem + pb * p_bytes + key * 32;
                 if (i > A.two_p)  // P's last reader
                     wait_or_give_up(&C.pv_done[pb], ((A.two_p ? i >> 1 : i) - 1) & 1, A.wait_ns, gave_up);
-                if (__builtin_expect(!whole, 0) && (kSeen == kTree ? rows != all_rows : lo > 0 || hi < u.ncols)) {
+                if (__builtin_expect(!whole, 0) && (lo > 0 || hi < u.ncols)) {
                     // Masked keys must not reach O through 0 * infinity: a
                     // value row that no column sees is cleared, and one that
                     // some see loses its NaN and infinities, which are added
@@ -962,7 +889,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
 #pragma unroll 1
                     for (int ch = grp; ch < 8 * kHalves; ch += kGroups) {
                         const uint32_t at = vb + (ch / 8) * kHalfBytes + (((ch % 8) ^ swz) << 4);
-                        if (none) {
+                        if (lo >= hi) {
                             st_shared16(at, 0, 0, 0, 0);
                             continue;
                         }
@@ -991,13 +918,12 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                         for (int n = 16 * grp; n < N; n += 16 * kGroups) {
                             float s[16];
                             tmem_ld16(s, s_tm + n);
-                            // kTree: a whole tile's bits are not made
-                            const uint32_t bits = kSeen == kTree && whole ? seen16(n, 0, N) : seen(n);
+                            const uint32_t seen = seen16(n, lo, hi);
                             tmem_wait_ld(s);
                             float keep = -INFINITY;
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                float x = ((bits >> e) & 1) ? s[e] : -INFINITY;
+                                float x = ((seen >> e) & 1) ? s[e] : -INFINITY;
                                 asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(x) : "f"(x));
                                 if (lane == e) keep = x;
                             }
@@ -1038,7 +964,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                         tmem_ld16(s, s_tm + n);
                         const uint32_t at = p_row + (n / 16) * kPGroup;
                         top = fmaxf(top, whole ? weigh16<false>(s, C.ref + n, A.scale2, 0, at, p_swz)
-                                               : weigh16<true>(s, C.ref + n, A.scale2, seen(n), at, p_swz));
+                                               : weigh16<true>(s, C.ref + n, A.scale2, seen16(n, lo, hi), at, p_swz));
                     }
                     fence_async_shared();
                     tc_fence_before();
@@ -1112,28 +1038,16 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 for (int x = t_first * kTile; x < t * kTile; ++x) {
                     const int k = tile_at<kSeen>(u.q, x / kTile) * kTile + x % kTile;
                     if (k >= u.q.kend) break;
-                    int vlo = 0, vhi = u.ncols;
-                    if (kSeen == kTree) {
-                        if (k < u.q.pos0 && A.window == 0) continue;
-                    } else {
-                        visible_columns<kSeen>(A, u, k, false, vlo, vhi);
-                        if (vlo >= vhi || (vlo == 0 && vhi == u.ncols)) continue;
-                    }
+                    int vlo, vhi;
+                    visible_columns<kSeen>(A, u, k, false, vlo, vhi);
+                    if (vlo >= vhi || (vlo == 0 && vhi == u.ncols)) continue;
                     const int page = A.block_table[(int64_t)u.b * A.max_pages + k / A.page_size];
                     if (page < 0 || page >= A.num_pages) continue;
                     const float v = bf16_lo(A.v_cache[page * A.page_stride + (k % A.page_size) * A.slot_stride +
                                                       u.h * A.head_stride + d]);
                     if (isfinite(v)) continue;
-                    uint64_t rows = 0;
-                    if (kSeen == kTree) {
-#pragma unroll 1
-                        for (int j = 0; j < nrows; ++j)
-                            rows |= uint64_t(TreeRow(A, u.q, u.j0 + j, true).word(A, u.q, k) & 1u) << j;
-                        if (rows == all_rows) continue;
-                    }
 #pragma unroll 1
                     for (int n = vlo; n < vhi; ++n) {
-                        if (kSeen == kTree && !((rows >> (n / A.G)) & 1)) continue;
                         if (split) {
                             part0[(int64_t)n * D] += v;
                         } else {
@@ -1251,14 +1165,12 @@ inline bool step_gather_rows(const dspark_attn &a, int64_t *row, int64_t *page_r
 
 // The arguments and tensor maps of a call: units of up to `rows_cap` rows, whose columns' parts have room for
 // `ncap`; a copy of queries takes q_rows rows.
-inline cudaError_t step_args(const dspark_attn &a, const uint64_t *row_seen, int sinks, int rows_cap, int ncap, int q_rows,
+inline cudaError_t step_args(const dspark_attn &a, int sinks, int rows_cap, int ncap, int q_rows,
                              uint64_t wait_ns, StepArgs &A, CUtensorMap (&maps)[3]) {
     A.B = a.B; A.rows = a.rows; A.q_max = a.q_max; A.Hq = a.Hq; A.Hkv = a.Hkv; A.G = a.Hq / a.Hkv;
     A.page_size = a.page_size; A.num_pages = a.num_pages; A.max_pages = a.max_pages;
     A.window = a.window;
     A.sinks = sinks;
-    A.row_seen = row_seen;
-    A.packed_pos = a.packed_pos;
     A.page_shift = 31;  // exact below 2^31: page_mul = ceil(2^shift / page_size) < 2^32
     while ((1u << (A.page_shift - 31)) < unsigned(a.page_size)) ++A.page_shift;
     A.page_mul = uint32_t(((1ull << A.page_shift) + a.page_size - 1) / a.page_size);
@@ -1318,10 +1230,10 @@ inline cudaError_t step_args(const dspark_attn &a, const uint64_t *row_seen, int
 }
 
 template <Seen kSeen>
-cudaError_t launch_rows(const dspark_attn &a, const uint64_t *row_seen, int sinks, int sms, uint64_t wait_ns, cudaStream_t s) {
+cudaError_t launch_rows(const dspark_attn &a, int sinks, int sms, uint64_t wait_ns, cudaStream_t s) {
     StepArgs A{};
     CUtensorMap maps[3];
-    const cudaError_t e = step_args(a, row_seen, sinks, step_rows(a.Hq, a.Hkv, a.q_max),
+    const cudaError_t e = step_args(a, sinks, step_rows(a.Hq, a.Hkv, a.q_max),
                                     step_columns(a.Hq, a.Hkv, a.q_max), 1, wait_ns, A, maps);
     if (e != cudaSuccess) return e;
     const int ctas = std::min(sms, kAttnMaxCtas);

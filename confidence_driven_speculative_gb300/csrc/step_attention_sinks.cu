@@ -5,7 +5,7 @@
 namespace dspark {
 
 cudaError_t launch_step_attention_sinks(const dspark_attn &a, int sinks, int sms, uint64_t wait_ns, cudaStream_t s) {
-    return launch_rows<kSinks>(a, nullptr, sinks, sms, wait_ns, s);
+    return launch_rows<kSinks>(a, sinks, sms, wait_ns, s);
 }
 
 }  // namespace dspark

@@ -1,4 +1,5 @@
-// tree_attention.cu -- dspark_step_attention_tree for trees of many rows.
+// tree_attention.cu -- dspark_step_attention_tree: the rows of drafted trees
+// over the paged cache.
 //
 // Mathematics.  As in step_attention.cuh; here the query vectors are the M side
 // of the tensor core.  One request and one cached head give rows * G vectors
@@ -44,10 +45,33 @@ struct Cut {
 };
 
 struct TreeArgs : StepArgs {
+    const int32_t *packed_pos;  // with a window
+    const uint64_t *row_seen;
     int rb;       // rows of a block
     int v_slots;
     int wide_out;  // out is 32-byte aligned
     Cut *cuts;    // [CTAs], by the CTA that the unit begins in
+};
+
+// A tree's row: what it sees, and where its window ends (its position).
+struct TreeRow {
+    uint64_t seen;
+    int pos;
+    __device__ __forceinline__ TreeRow(const TreeArgs &A, const Req &q, int j, bool there) : seen(0), pos(q.pos0) {
+        if (!there) return;
+        // (asked for here, and not where it is used first)
+        asm volatile("ld.global.b64 %0, [%1];" : "=l"(seen) : "l"(A.row_seen + q.row0 + j));
+        if (A.window > 0) pos = max(A.packed_pos[q.row0 + j], q.pos0);
+    }
+    // Which of the 32 keys from k0 on it sees.
+    __device__ __forceinline__ uint32_t word(const TreeArgs &A, const Req &q, int k0) const {
+        auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+        uint32_t cached = below(q.pos0 - k0);
+        if (A.window > 0) cached &= ~below(pos - A.window + 1 - k0) | below(A.sinks - k0);
+        const int at = k0 - q.pos0;  // the own entry that k0 is
+        const uint32_t own = at >= 64 || at <= -32 ? 0u : at >= 0 ? uint32_t(seen >> at) : uint32_t(seen) << -at;
+        return (cached | own) & below(q.kend - k0);
+    }
 };
 
 // What a CTA does of one unit.
@@ -113,9 +137,9 @@ struct Tiles {
     __device__ __forceinline__ Tiles(const TreeArgs &A) : span(kBox ? A.box : 4), boxes(kTile / span), policy(evict_first()) {}
 
     __device__ __forceinline__ void look_up(const TreeArgs &A, int b, const Req &q, int t, int lane, Ids &ids) const {
-        const int key0 = tile_at<kTree>(q, t) * kTile + lane * span;
+        const int key0 = tile_at<kSinks>(q, t) * kTile + lane * span;
         const int32_t *table = A.block_table + (int64_t)b * A.max_pages;
-        const bool wanted = lane < boxes && wants<kTree>(A, q, t, key0, span);
+        const bool wanted = lane < boxes && wants<kSinks>(A, q, t, key0, span);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             ids.page[i] = -1;
@@ -130,8 +154,8 @@ struct Tiles {
                                          const Ids &ids, uint32_t dst, uint64_t *full, uint32_t *bad) const {
         constexpr int kHalves = D / 64;
         constexpr uint32_t kHalfBytes = kTile * 128;
-        const int tile0 = tile_at<kTree>(q, t) * kTile, key0 = tile0 + lane * span;
-        const bool here = lane < boxes && wants<kTree>(A, q, t, key0, span);
+        const int tile0 = tile_at<kSinks>(q, t) * kTile, key0 = tile0 + lane * span;
+        const bool here = lane < boxes && wants<kSinks>(A, q, t, key0, span);
         uint32_t bad_bits = 0;
         int row[4];
 #pragma unroll
@@ -265,7 +289,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
         auto cost_of = [&](const Req &r) { return r.blocks * A.Hkv * (r.nt * places_of(r) + U); };
         int mine = 0;
 #pragma unroll 4
-        for (int b = b_lo; b < b_hi; ++b) mine += cost_of(load_req<kTree>(A, b));
+        for (int b = b_lo; b < b_hi; ++b) mine += cost_of(load_req<kSinks>(A, b));
         int sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -282,7 +306,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
             const int src = __ffs(who) - 1;
             if (lane == src)
                 for (b = b_lo; b < b_hi; ++b) {
-                    const int c = cost_of(load_req<kTree>(A, b));
+                    const int c = cost_of(load_req<kSinks>(A, b));
                     if (start < place + c) break;
                     place += c;
                 }
@@ -295,7 +319,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
         int published = 0, issued = 0, q_use = 0, jobs = 0;
         bool ok = true;
         for (; b < A.B && place < end && ok; ++b) {
-            const Req q = load_req<kTree>(A, b);
+            const Req q = load_req<kSinks>(A, b);
             const int w = places_of(q), each = q.nt * w + U, units = q.blocks * A.Hkv;
             int i = max(start - place, 0) / each;
             for (; i < units && place + i * each < end && ok; ++i) {
@@ -599,7 +623,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
             // Once a wait has given up, the others return at once and the
             // loops run to their ends on whatever there is; the status tells.
             for (int k = k0; k < jobs; k += 2) {
-                const int t = blocks == 2 ? k >> 1 : k, tile = tile_at<kTree>(q, t_beg + t);
+                const int t = blocks == 2 ? k >> 1 : k, tile = tile_at<kSinks>(q, t_beg + t);
                 wait_or_give_up(&C.s_full[a], s_uses & 1, A.wait_ns, gave_up);
                 __syncwarp();
                 ++s_uses;
@@ -789,7 +813,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
                 // what was taken out of the values that this row sees
 #pragma unroll 1
                 for (int t = t_beg; t < t_beg + n; ++t) {
-                    const int tile = tile_at<kTree>(q, t);
+                    const int tile = tile_at<kSinks>(q, t);
                     const bool edge = tile >= whole_hi || !(tile >= whole_lo || (tile + 1) * kTile <= A.sinks);
                     if (!edge && C.spread[part % 8] != part + 1) continue;
 #pragma unroll 1
@@ -976,13 +1000,15 @@ size_t tree_attn_workspace_bytes(int Hq, int Hkv, int D, int q_max) {
     return cuts_at(Hq, Hkv, D, q_max) + sizeof(Cut) * kAttnMaxCtas;
 }
 
-cudaError_t launch_tree_attention(const dspark_attn &a, const uint64_t *row_seen, int sinks, int sms, uint64_t wait_ns,
+cudaError_t launch_step_attention_tree(const dspark_attn &a, const uint64_t *row_seen, int sinks, int sms, uint64_t wait_ns,
                                   cudaStream_t s) {
     TreeArgs A{};
+    A.row_seen = row_seen;
+    A.packed_pos = a.packed_pos;
     CUtensorMap maps[3];
     A.rb = block_rows(a.Hq, a.Hkv, a.q_max);
     const int rows = unit_rows(a.Hq, a.Hkv, a.q_max);
-    const cudaError_t e = step_args(a, row_seen, sinks, rows, rows * (a.Hq / a.Hkv), A.rb, wait_ns, A, maps);
+    const cudaError_t e = step_args(a, sinks, rows, rows * (a.Hq / a.Hkv), A.rb, wait_ns, A, maps);
     if (e != cudaSuccess) return e;
     A.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
     A.cuts = reinterpret_cast<Cut *>(static_cast<char *>(a.workspace) + cuts_at(a.Hq, a.Hkv, a.D, a.q_max));
