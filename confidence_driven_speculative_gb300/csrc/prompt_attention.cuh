@@ -132,7 +132,7 @@ struct Ctrl {
     int poisoned[8];          // by unit number % 8: the last unit + 1 that lost values
     int pairs[kScan + 1];     // exclusive sums of the units (per head) of each thread's prompts
     int warp_sum[kScan / 32];
-    float swap[2][2][2][kTile];  // between the two threads of a row (maxima, sums): by block and half
+    float swap[2][2][kTile];  // between the two threads of a row (maxima, sums): by block and half
     uint32_t tmem;
     int issued[2], q_issued[2];  // copies of K and V tiles, of the blocks' queries
     int gave_up;
@@ -162,12 +162,12 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
     constexpr uint32_t kHalfBytes = kTile * 128;
     constexpr uint32_t kSlotBytes = kHalves * kHalfBytes;
     constexpr uint32_t kColO = 2 * kTile;  // S_0, S_1, O_0, O_1
-    extern __shared__ uint8_t dyn[];
-    __shared__ Ctrl C;
+    extern __shared__ __align__(1024) uint8_t dyn[];
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-    const uint32_t q_smem = (smem_addr(dyn) + 1023) & ~1023u;
-    const uint32_t ring = q_smem + 2 * kSlotBytes;
+    // Queries, ring, control.
+    const uint32_t q_smem = smem_addr(dyn), ring = q_smem + 2 * kSlotBytes;
+    Ctrl &C = *reinterpret_cast<Ctrl *>(dyn + (2 + A.slots) * kSlotBytes);
     const int v_slots = A.slots - A.k_slots;
     const uint32_t v_ring = ring + A.k_slots * kSlotBytes;
     volatile int *gave_up = &C.gave_up;
@@ -522,11 +522,11 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
             return r != 0;
         };
         auto pair_sync = [&] { asm volatile("barrier.cta.sync %0, 64;" ::"r"(pair_bar) : "memory"); };
-        // The other thread's x.  A pair_any lies between two uses of a kind.
-        auto exchange = [&](int kind, float x) {
-            C.swap[kind][a][half][row] = x;
+        // The other thread's x.  A barrier of the two lies between two uses.
+        auto exchange = [&](float x) {
+            C.swap[a][half][row] = x;
             pair_sync();
-            return C.swap[kind][a][half ^ 1][row];
+            return C.swap[a][half ^ 1][row];
         };
         SchedReader sched;
         Ring rv;  // of the block's next tile
@@ -625,7 +625,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                 const float m = max3(m0, m1, fmaxf(s[kKeys - 2], s[kKeys - 1]));
                 const bool first = t == sp.lo;
                 if (__builtin_expect(pair_any(first || m * scale2 > ref), 0)) {
-                    const float top = fmaxf(m, exchange(0, m)), near = top * A.scale2 + kHeadroom;
+                    const float top = fmaxf(m, exchange(m)), near = top * A.scale2 + kHeadroom;
                     const float to_scale = fabsf(near) > kFar ? A.far_scale : A.scale2;
                     const float to = fmaxf(top * to_scale + kHeadroom, kRefMin);
                     if (first) {
@@ -677,7 +677,8 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
                 l2 = add2(sums[0], sums[1]);
             }
             for (int t = sp.hi; t < t_hi; ++t) rv.next(v_slots);
-            const float mine = l2.x + l2.y, l = mine + exchange(1, mine), inv = l == 0.f ? 0.f : 1.f / l;
+            pair_sync();
+            const float mine = l2.x + l2.y, l = mine + exchange(mine), inv = l == 0.f ? 0.f : 1.f / l;
             wait_or_give_up(&C.o_full[a], o_uses & 1, A.wait_ns, gave_up);
             __syncwarp();
             ++o_uses;
@@ -747,11 +748,11 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs A, const __grid_const
 
 template <int D, Seen kSeen>
 cudaError_t launch(PromptArgs A, const CUtensorMap (&maps)[3], int ctas, cudaStream_t s) {
-    const size_t slot = size_t(D) * 2 * kTile;
-    A.slots = int(std::min<size_t>((kSmemBytes - sizeof(Ctrl) - 1024 - 2 * slot) / slot, kSlotsMax));
+    constexpr size_t slot = size_t(D) * 2 * kTile, room = (kSmemBytes - sizeof(Ctrl)) / slot;
+    static_assert(room >= 2 + 5, "queries of two blocks, two tiles of K and three of V");
+    A.slots = int(std::min<size_t>(room - 2, kSlotsMax));
     A.k_slots = A.slots / 2;
-    static_assert((kSmemBytes - sizeof(Ctrl) - 1024) / (D * 2 * kTile) >= 2 + 4, "two slots each of K and V");
-    const size_t smem = 1024 + (2 + A.slots) * slot;
+    const size_t smem = (2 + A.slots) * slot + sizeof(Ctrl);
     const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D, kSeen>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
