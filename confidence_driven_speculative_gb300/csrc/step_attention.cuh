@@ -47,7 +47,9 @@
 // TB/s: 256 requests of 16 to 4095 keys with 1 to 7 rows of 32 heads 311 to
 // 319 us (floor 297); 2 of 131 000 keys with 9 rows of 64 heads 171 (158); 32
 // of 16 to 4095 keys with 17 rows 62.5 (42); one row over 4096 keys 13.3 (2.5);
-// 64 requests with a window of 1024 over single-position pages 84.5 (39).
+// 64 requests with a window of 1024 over single-position pages 84.5 (39); 256 of
+// 16 to 8191 keys with 1 to 17 rows, a window of 1024 and 4 sinks over pages of 16
+// 190 (151).
 // Long caches run at the memory's rate.  Otherwise a unit's end costs what two
 // to three tiles do (the wait for its last product, the outputs, the fences of
 // its parts), and one request alone is a chain of latencies: launch, cut, tile,
@@ -91,6 +93,7 @@ struct StepArgs {
     int B, rows, q_max, Hq, Hkv, G;
     int page_size, num_pages, max_pages, window, sinks;
     uint32_t page_mul, page_shift;  // position / page_size = position * mul >> shift
+    int fold;                  // sinks go in the window's first tile by so many keys (2^k), if they fit; 0: never
     int box;                   // keys of a TMA box (divides the page and the tile); 0: gather
     int ncap;                  // columns of a unit at most, a multiple of 16
     int rows_cap;              // rows of a unit at most
@@ -119,6 +122,7 @@ struct Req {
     int kbeg, kend;  // keys that some row sees
     int t0, nt;      // tiles: those of the window begin at t0
     int ns;          // tiles of sinks in front of them that do not touch the window's
+    int sb, se;      // or the keys of tile t0 in whose place the sinks are read
     int blocks, per; // blocks of rows, rows of one
 };
 
@@ -137,11 +141,22 @@ __device__ __forceinline__ Req load_req(const StepArgs &A, int b) {
     const int cap = A.max_pages * A.page_size;
     r.kend = min(r.pos0 + r.n, cap);
     r.kbeg = A.window > 0 ? min(max(r.pos0 - A.window + 1, 0), r.kend) : 0;
-    r.ns = 0;
+    r.ns = r.sb = r.se = 0;
     if (kSeen != kChain && A.window > 0 && A.sinks > 0) {
         // The sinks' tiles, unless one of them holds keys of the window: then all is one run of tiles.
         r.ns = (min(A.sinks, r.kbeg) + kTile - 1) / kTile;
         if (r.kbeg / kTile < r.ns) r.kbeg = r.ns = 0;
+        // Few sinks take no tile of their own where the window's first one has room for them right in front
+        // of the window (so the boxes to copy stay one run): 256 requests with 4 sinks 197 us -> 190, one
+        // request 11.2 -> 11.4.  The remainder stays a division: with a mask the same call takes 194 us.
+        if (A.fold > 0 && r.ns == 1) {
+            const int se = r.kbeg - r.kbeg % A.fold, sb = se - ((A.sinks + A.fold - 1) & ~(A.fold - 1));
+            if (sb >= (r.kbeg & ~(kTile - 1))) {
+                r.sb = sb;
+                r.se = se;
+                r.ns = 0;
+            }
+        }
     }
     r.t0 = r.kbeg / kTile;
     r.nt = max(r.ns + (r.kend + kTile - 1) / kTile - r.t0, 1);
@@ -161,10 +176,17 @@ __device__ __forceinline__ int tile_at(const Req &q, int t) {
     return kSeen != kChain && t < q.ns ? t : q.t0 + t - (kSeen != kChain ? q.ns : 0);
 }
 
+// The position that the key at `key` of the tiles' run stands for.
+template <Seen kSeen>
+__device__ __forceinline__ int pos_at(const Req &q, int key) {
+    return kSeen != kChain && key >= q.sb && key < q.se ? key - q.sb : key;
+}
+
 // Is some key of [key0, key0 + span) of tile t wanted?
 template <Seen kSeen>
 __device__ __forceinline__ bool wants(const StepArgs &A, const Req &q, int t, int key0, int span) {
     if (kSeen != kChain && t < q.ns) return key0 < A.sinks;
+    if (kSeen != kChain && key0 < q.se) return key0 >= q.sb;
     return key0 < q.kend && key0 + span > q.kbeg;
 }
 
@@ -509,6 +531,8 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 start_req.t0 = __shfl_sync(0xffffffffu, q.t0, src);
                 start_req.nt = __shfl_sync(0xffffffffu, q.nt, src);
                 start_req.ns = kSeen == kChain ? 0 : __shfl_sync(0xffffffffu, q.ns, src);
+                start_req.sb = kSeen == kChain ? 0 : __shfl_sync(0xffffffffu, q.sb, src);
+                start_req.se = kSeen == kChain ? 0 : __shfl_sync(0xffffffffu, q.se, src);
                 start_req.blocks = __shfl_sync(0xffffffffu, q.blocks, src);
                 start_req.per = __shfl_sync(0xffffffffu, q.per, src);
             }
@@ -608,11 +632,12 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
             const int key0 = tile_at<kSeen>(x.q, tile) * kTile + my_box * span;
             const int32_t *table = A.block_table + (int64_t)x.b * A.max_pages;
             const bool wanted = my_turn && wants<kSeen>(A, x.q, tile, key0, span);
+            const int pos0 = pos_at<kSeen>(x.q, key0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 ids.page[i] = -1;
                 if ((i == 0 || !kBox) && wanted) {
-                    const int pi = page_of(A, key0 + i);
+                    const int pi = page_of(A, pos0 + i);
                     if (pi < A.max_pages) ids.page[i] = table[pi];
                 }
             }
@@ -635,6 +660,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
 
             const int tile0 = tile_at<kSeen>(u.q, t) * kTile, key0 = tile0 + my_box * span;
             const bool here = my_turn && wants<kSeen>(A, u.q, t, key0, span);
+            const int pos0 = pos_at<kSeen>(u.q, key0);
             uint32_t bad_bits = 0;  // of the lane's keys (gather) or of the whole box
             int row[4];
 #pragma unroll
@@ -643,8 +669,8 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 if (!good) bad_bits |= 1u << j;
                 const int page = good ? ids.page[j] : 0;  // masked; any memory will do
                 row[j] = kBox ? page
-                               : page * A.page_rows + u.h * A.head_rows + key0 + j -
-                                     page_of(A, key0 + j) * A.page_size;
+                               : page * A.page_rows + u.h * A.head_rows + pos0 + j -
+                                     page_of(A, pos0 + j) * A.page_size;
             }
             const bool lane_bad = here && (kBox ? (bad_bits & 1) : bad_bits != 0);
             uint32_t words[4] = {0, 0, 0, 0};
@@ -690,7 +716,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                     mbar_arrive_expect_tx(full, bytes);
                     uint32_t dst = ring + slot * kSlotBytes + box_lo * span * 128;
                     if (kBox) {
-                        const int first_key = tile0 + box_lo * span;
+                        const int first_key = pos_at<kSeen>(u.q, tile0 + box_lo * span);
                         int in_page = first_key - page_of(A, first_key) * A.page_size;
 #pragma unroll 4
                         for (int j = box_lo; j < box_lo + box_n; ++j) {
@@ -700,6 +726,8 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                             dst += span * 128;
                             in_page += span;
                             if (in_page == A.page_size) in_page = 0;
+                            if (kSeen != kChain && tile0 + (j + 1) * span == u.q.se)
+                                in_page = u.q.se - page_of(A, u.q.se) * A.page_size;
                         }
                     } else {
                         const int x0 = u.h * A.head_x;
@@ -872,7 +900,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 if (!whole) {
                     const int q = warp & 3;
                     const uint32_t word = q == 0 ? bw.x : q == 1 ? bw.y : q == 2 ? bw.z : bw.w;
-                    visible_columns<kSeen>(A, u, tile * kTile + key, (word >> lane) & 1, lo, hi);
+                    visible_columns<kSeen>(A, u, pos_at<kSeen>(u.q, tile * kTile + key), (word >> lane) & 1, lo, hi);
                 }
                 bool move = first;
                 const int pb = A.two_p ? i & 1 : 0;
@@ -1036,7 +1064,7 @@ step_attention_kernel(const __grid_constant__ StepArgs A, const __grid_constant_
                 // tiles that some columns see and others do not.
 #pragma unroll 1
                 for (int x = t_first * kTile; x < t * kTile; ++x) {
-                    const int k = tile_at<kSeen>(u.q, x / kTile) * kTile + x % kTile;
+                    const int k = pos_at<kSeen>(u.q, tile_at<kSeen>(u.q, x / kTile) * kTile + x % kTile);
                     if (k >= u.q.kend) break;
                     int vlo, vhi;
                     visible_columns<kSeen>(A, u, k, false, vlo, vhi);
@@ -1236,6 +1264,7 @@ cudaError_t launch_rows(const dspark_attn &a, int sinks, int sms, uint64_t wait_
     const cudaError_t e = step_args(a, sinks, step_rows(a.Hq, a.Hkv, a.q_max),
                                     step_columns(a.Hq, a.Hkv, a.q_max), 1, wait_ns, A, maps);
     if (e != cudaSuccess) return e;
+    if (kSeen != kChain) A.fold = A.box ? A.box : 4;
     const int ctas = std::min(sms, kAttnMaxCtas);
     if (A.box) return a.D == 128 ? launch<128, true, kSeen>(A, maps, ctas, s) : launch<64, true, kSeen>(A, maps, ctas, s);
     return a.D == 128 ? launch<128, false, kSeen>(A, maps, ctas, s) : launch<64, false, kSeen>(A, maps, ctas, s);

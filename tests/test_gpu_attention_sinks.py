@@ -59,6 +59,14 @@ def test_step_shapes(cuda_lib, shape):
     Step(2, 4, window=150, **shape).check()
 
 
+@pytest.mark.parametrize("page", [1, 8, 24, 64])
+@pytest.mark.parametrize("sinks", [3, 30, 65])
+def test_step_every_place_of_the_window_in_its_first_tile(cuda_lib, sinks, page):
+    # 64 requests whose windows begin at every second key of a tile: the sinks fit in front of some of them
+    Step(12, sinks, ctx=[500 + 131 * i for i in range(64)], n=[1 + i % 5 for i in range(64)], Hq=4, Hkv=2, D=128,
+         page=page, window=200 + sinks).check()
+
+
 def test_step_without_sinks_or_window_is_the_plain_call(cuda_lib):
     kw = dict(ctx=[300, 40, 700], n=[17, 9, 1], Hq=8, Hkv=2, D=128, page=16)
     for window, sinks in ((0, 0), (0, 9), (100, 0)):
