@@ -357,14 +357,15 @@ __global__ void __launch_bounds__(kThreadsCopy) copy_tails_kernel(const CopyArgs
     }
 }
 
-// The workspace: status word, number of copies; copies; ranks; claims; free pages.
-struct PagesLayout { size_t copies, claim, free_list, total; };
+// The workspace: status word, number of copies; claims; free pages; copies.  The claims, which are zero between
+// calls, lie where they do for every B.
+struct PagesLayout { size_t claim, free_list, copies, total; };
 PagesLayout pages_layout(int B, int num_pages) {
     PagesLayout l;
-    l.copies = 256;
-    l.claim = l.copies + align256(sizeof(int4) * size_t(B));
+    l.claim = 256;
     l.free_list = l.claim + align256(sizeof(int32_t) * size_t(num_pages));
-    l.total = l.free_list + align256(sizeof(int32_t) * size_t(num_pages));
+    l.copies = l.free_list + align256(sizeof(int32_t) * size_t(num_pages));
+    l.total = l.copies + align256(sizeof(int4) * size_t(B));
     return l;
 }
 

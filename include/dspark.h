@@ -520,8 +520,8 @@ typedef struct dspark_tree {
     int32_t logit_dtype; /* dspark_dtype of target_logits */
 
     /* ---- inputs (device, read only) -------------------------------------- */
-    const void *target_logits;  /* [rows, V]; rows as in the alignment convention.  -inf
-                                   marks masked ids */
+    const void *target_logits;  /* [rows, V]; rows as in the alignment convention.  Finite, or
+                                   -inf for masked ids */
     const int32_t *row_off;     /* [B+1] request b owns rows row_off[b] .. row_off[b+1] */
     const int32_t *parent;      /* [rows] index of the parent in the request, below the row's
                                    own; another value: no parent, never reached.  Row 0's is
@@ -539,7 +539,7 @@ typedef struct dspark_tree {
 
     /* ---- scratch --------------------------------------------------------- */
     void *workspace;        /* dspark_tree_workspace_size() bytes, under the workspace
-                               convention */
+                               convention: one of the largest size serves every shape */
     size_t workspace_bytes;
 } dspark_tree;
 
@@ -605,7 +605,8 @@ typedef struct dspark_pages {
 
     /* ---- shapes ---------------------------------------------------------- */
     int32_t B_in;        /* rows of table_in, 0..DSPARK_MAX_B */
-    int32_t B;           /* requests of the next step, 0..DSPARK_MAX_B */
+    int32_t B;           /* requests of the next step, 0..DSPARK_MAX_B (0: the call is a no-op,
+                            every page is free, totals are not written) */
     int32_t max_pages;   /* columns of both tables, >= 1 */
     int32_t sinks;       /* positions that first_pos does not drop, >= 0 */
 
@@ -633,7 +634,8 @@ typedef struct dspark_pages {
 
     /* ---- scratch --------------------------------------------------------- */
     void *workspace;        /* dspark_pages_workspace_size() bytes, under the workspace
-                               convention */
+                               convention: one of the largest B serves every B, another
+                               num_pages needs dspark_workspace_init() again */
     size_t workspace_bytes;
 } dspark_pages;
 

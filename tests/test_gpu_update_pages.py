@@ -215,3 +215,15 @@ def test_streams_and_graphs(cuda_lib):
             if want[2][r] >= 0:
                 x[:, want[3][r], :b.keep[r] % 16] = x[:, want[2][r], :b.keep[r] % 16]
         assert np.array_equal(bits5(t), x)
+
+
+def test_one_workspace_for_batches_of_every_size(cuda_lib):
+    # every case has the same number of pages; the claims of one call must not count in the next
+    cases = [Case(seed, [90, 33, 64], B, 8, spare=100, grow=30) for seed, B in enumerate((3, 70, 1, 200, 12, 70))]
+    largest = max((c.handle() for c in cases), key=lambda h: h.ws_bytes)
+    for c in cases:
+        assert c.num_pages == cases[0].num_pages
+        h = c.handle()
+        h.workspace, h.ws_bytes = largest.workspace, largest.ws_bytes
+        h.pages.workspace, h.pages.workspace_bytes = largest.workspace.data_ptr(), largest.ws_bytes
+        c.check(h)

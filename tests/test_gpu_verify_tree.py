@@ -217,3 +217,15 @@ def test_streams_and_graphs(cuda_lib):
     for c, h in ((a, ha), (b, hb)):
         for k, w in c.want().items():
             assert np.array_equal(getattr(h, k).cpu().numpy(), w), k
+
+
+def test_one_workspace_for_every_shape(cuda_lib):
+    cases = [Case(20 + i, n, V) for i, (n, V) in enumerate((([30], 4096), ([3, 5, 9], 32000), ([20] * 60, 1024),
+                                                             ([64, 1], 512), ([7] * 5, 129280)))]
+    handles = [c.handle() for c in cases]
+    largest = max(handles, key=lambda h: h.ws_bytes)
+    for _ in range(2):
+        for c, h in zip(cases, handles):
+            h.tree.workspace, h.tree.workspace_bytes = largest.workspace.data_ptr(), largest.ws_bytes
+            c.commit = h._keep["seq_lens_commit"]
+            c.check(h)
