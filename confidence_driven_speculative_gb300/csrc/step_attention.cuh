@@ -144,13 +144,14 @@ __device__ __forceinline__ Req load_req(const StepArgs &A, int b) {
     r.ns = r.sb = r.se = 0;
     if (kSeen != kChain && A.window > 0 && A.sinks > 0) {
         // The sinks' tiles, unless one of them holds keys of the window: then all is one run of tiles.
-        r.ns = (min(A.sinks, r.kbeg) + kTile - 1) / kTile;
+        const int sinks = min(A.sinks, r.kbeg);
+        r.ns = (sinks + kTile - 1) / kTile;
         if (r.kbeg / kTile < r.ns) r.kbeg = r.ns = 0;
         // Few sinks take no tile of their own where the window's first one has room for them right in front
         // of the window (so the boxes to copy stay one run): 256 requests with 4 sinks 197 us -> 190, one
         // request 11.2 -> 11.4.  The remainder stays a division: with a mask the same call takes 194 us.
         if (A.fold > 0 && r.ns == 1) {
-            const int se = r.kbeg - r.kbeg % A.fold, sb = se - ((A.sinks + A.fold - 1) & ~(A.fold - 1));
+            const int se = r.kbeg - r.kbeg % A.fold, sb = se - ((sinks + A.fold - 1) & ~(A.fold - 1));
             if (sb >= (r.kbeg & ~(kTile - 1))) {
                 r.sb = sb;
                 r.se = se;

@@ -67,6 +67,14 @@ def test_step_every_place_of_the_window_in_its_first_tile(cuda_lib, sinks, page)
          page=page, window=200 + sinks).check()
 
 
+@pytest.mark.parametrize("sinks", [2**31 - 1, 2**31 - 9])
+@pytest.mark.parametrize("page", [1, 16])
+def test_step_sinks_without_end(cuda_lib, sinks, page):
+    # windows that begin around the end of a tile
+    Step(13, sinks, ctx=[99 + w for w in range(24, 34)] + [355], n=[1, 3] * 5 + [2], Hq=4, Hkv=2, D=128, page=page,
+         window=100).check()
+
+
 def test_step_without_sinks_or_window_is_the_plain_call(cuda_lib):
     kw = dict(ctx=[300, 40, 700], n=[17, 9, 1], Hq=8, Hkv=2, D=128, page=16)
     for window, sinks in ((0, 0), (0, 9), (100, 0)):
