@@ -11,12 +11,19 @@
 // present row, each warp hands its key to every CTA of the cluster, and one
 // cluster barrier later all know the next row.  Bound: bytes of the walks'
 // rows while many walk, later the latency of a level (a load, a reduction, a
-// barrier).  Clusters are as large as still lets all requests walk at once.
+// barrier).  Clusters are as large as still lets all requests walk at once.  So
+// late a level takes 1.4 us however short its row, and what a cluster has in
+// flight at once counts: most loads go through shared memory (cp.async), each to
+// a place that only its own thread reads, and leave the registers to more CTAs
+// (seven an SM with 4 + 12 loads a thread; 16 to registers in four 28.0 us against
+// 22.9 for 128 requests of 129280 ids, 77.5 against 57.8 for 400, 17.2 against
+// 18.5 for 64; the walks' own rows take 11.4 at a copy's rate).
 //
 // Few rows are read all at once (verify_tree_all_kernel): every CTA
 // takes a part of a row and merges its key by atomicMax, and the one that
 // finishes a request's last part walks in registers.  Reading more than needed
-// costs less than waiting once per level.
+// costs less than waiting once per level: one tree of 32 rows and 129280 ids
+// takes 4.9 us.
 #include <algorithm>
 
 #include "cache.cuh"
@@ -28,12 +35,13 @@ namespace {
 
 constexpr int kThreadsAll = 256;    // verify_tree_all_kernel
 constexpr int kThreadsWalk = 128;   // verify_tree_kernel
-constexpr int kResident = 4;        // its CTAs of an SM
+constexpr int kResident = 7;        // its CTAs of an SM
 constexpr int kMaxCluster = 16;
 // Bytes of all rows up to which they are read at once.
 constexpr size_t kAllBytes = size_t(24) << 20;
 constexpr int kAllRequests = 1024;  // and requests
-constexpr int kLoadsAll = 8, kLoadsWalk = 16;  // 16-byte loads of a thread in flight
+constexpr int kLoadsAll = 8, kLoadsWalk = 4;  // 16-byte loads of a thread in flight to registers
+constexpr int kLaterWalk = 12;                // and to shared memory
 
 struct TreeArgs {
     int B, rows, q_max, V;
@@ -77,38 +85,68 @@ template <> __device__ __forceinline__ float vector_max<float>(const uint4 &x) {
     return fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)), fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
 }
 
-// The largest key of the 16-byte vectors first, first + stride, .. below end of a row, for this thread.  A
-// vector is taken apart only at the end, the one that holds the maximum.
-template <typename T, int kTreeLoads>
-__device__ __forceinline__ Key best_of(const uint4 *row, int first, int end, int stride) {
-    constexpr int E = Vec<T>::kElems;
+// The vector with the largest element so far, of those that a thread has met.
+template <typename T>
+struct Best {
     float v = -INFINITY;
     int at = -1;
-    uint4 best = make_uint4(0, 0, 0, 0);
-    for (int c0 = first; c0 < end; c0 += kTreeLoads * stride) {
-        uint4 x[kTreeLoads];
+    uint4 x = make_uint4(0, 0, 0, 0);
+    __device__ __forceinline__ void meet(const uint4 &y, int c) {
+        const float m = vector_max<T>(y);
+        if (m > v || at < 0) {  // vectors ascend, so the first of equals stays
+            v = m;
+            at = c;
+            x = y;
+        }
+    }
+    // A vector is taken apart only here, the one that holds the maximum.
+    __device__ __forceinline__ Key key() const {
+        constexpr int E = Vec<T>::kElems;
+        if (at < 0) return 0;
+        float z[E];
+        Vec<T>::unpack(x, z);
+        int e = 0;
 #pragma unroll
-        for (int k = 0; k < kTreeLoads; ++k)
+        for (int k = E - 1; k >= 0; --k)
+            if (z[k] == v) e = k;
+        return make_key(v, at * E + e);
+    }
+};
+
+// The largest key of the 16-byte vectors first, first + stride, .. below end of a row, for this thread: kRegs
+// loads in flight to registers and kShared to its own places of shared memory, kThreads apart.
+template <typename T, int kRegs, int kShared, int kThreads>
+__device__ __forceinline__ Key best_of(const uint4 *row, int first, int end, int stride, uint32_t mine) {
+    Best<T> best;
+    for (int c0 = first; c0 < end; c0 += (kRegs + kShared) * stride) {
+#pragma unroll
+        for (int k = 0; k < kShared; ++k) {
+            const int c = c0 + (kRegs + k) * stride;
+            if (c < end)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                             ::"r"(mine + k * kThreads * 16), "l"(row + c) : "memory");
+        }
+        uint4 x[kRegs];
+#pragma unroll
+        for (int k = 0; k < kRegs; ++k)
             if (c0 + k * stride < end) x[k] = __ldcs(row + c0 + k * stride);
 #pragma unroll
-        for (int k = 0; k < kTreeLoads; ++k) {
+        for (int k = 0; k < kRegs; ++k) {
             if (c0 + k * stride >= end) break;
-            const float m = vector_max<T>(x[k]);
-            if (m > v || at < 0) {  // vectors ascend, so the first of equals stays
-                v = m;
-                at = c0 + k * stride;
-                best = x[k];
+            best.meet(x[k], c0 + k * stride);
+        }
+        if (kShared > 0) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+            for (int k = 0; k < kShared; ++k) {
+                const int c = c0 + (kRegs + k) * stride;
+                if (c >= end) break;
+                // its own copies, which wait_all has seen land; the next round's are issued behind these reads
+                best.meet(ld_shared16(mine + k * kThreads * 16), c);
             }
         }
     }
-    if (at < 0) return 0;
-    float z[E];
-    Vec<T>::unpack(best, z);
-    int e = 0;
-#pragma unroll
-    for (int k = E - 1; k >= 0; --k)
-        if (z[k] == v) e = k;
-    return make_key(v, at * E + e);
+    return best.key();
 }
 
 // The lowest child of row `at` whose token is y; -1: none.  Lane j holds rows j and 32 + j.
@@ -166,6 +204,7 @@ struct Walk {
 template <typename T>
 __global__ void __launch_bounds__(kThreadsWalk, kResident) verify_tree_kernel(const TreeArgs A) {
     constexpr int kWarpsTree = kThreadsWalk / 32;
+    __shared__ uint4 later[kLaterWalk][kThreadsWalk];
     __shared__ Key keys[2][kMaxCluster * kWarpsTree];  // by level % 2: of all warps of the cluster
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int rank, size;
@@ -184,7 +223,8 @@ __global__ void __launch_bounds__(kThreadsWalk, kResident) verify_tree_kernel(co
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     while (at >= 0) {
         const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const T *>(A.logits) + int64_t(r.row0 + at) * A.V);
-        Key k = warp_max(best_of<T, kLoadsWalk>(row, rank * kThreadsWalk + tid, vecs, size * kThreadsWalk));
+        Key k = warp_max(best_of<T, kLoadsWalk, kLaterWalk, kThreadsWalk>(
+            row, rank * kThreadsWalk + tid, vecs, size * kThreadsWalk, smem_addr(&later[0][tid])));
         Key *const mine = &keys[walk.len & 1][rank * kWarpsTree + warp];
         if (lane < size)
             asm volatile(
@@ -222,7 +262,8 @@ __global__ void __launch_bounds__(kThreadsAll) verify_tree_all_kernel(const Tree
     }
     const int vecs = A.V / Vec<T>::kElems, each = (vecs + A.parts - 1) / A.parts;
     const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const T *>(A.logits) + int64_t(r.row0 + j) * A.V);
-    Key k = warp_max(best_of<T, kLoadsAll>(row, part * each + tid, min((part + 1) * each, vecs), kThreadsAll));
+    Key k = warp_max(best_of<T, kLoadsAll, 0, kThreadsAll>(row, part * each + tid, min((part + 1) * each, vecs),
+                                                              kThreadsAll, 0));
     if (lane == 0) keys[warp] = k;
     __syncthreads();
     if (warp > 0) return;
