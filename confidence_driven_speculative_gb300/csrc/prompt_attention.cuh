@@ -29,11 +29,15 @@
 // Units are handed out by a counter, the longest of a prompt first, so the
 // CTAs end together; a unit's result does not depend on who computes it.
 //
-// Measured, D = 128: one prompt of 8192 rows and 32 heads 346 to 350 us in loops
-// of seconds, under the power limit, 1.58 PFLOP/s where a library product keeps up
+// Measured, D = 128: one prompt of 8192 rows and 32 heads 340 to 346 us in loops
+// of seconds, under the power limit, 1.60 PFLOP/s where a library product keeps up
 // 1.72; in a burst of 15 ms at 2070 MHz 316 us, 1.74 against 1.91.  24 prompts of
-// 20 to 2000 rows and 40 heads 233 to 236 us (228 in a burst), 113 at the library's
-// rate.  A step's products are 2048 clocks by the tensor cores' nominal rate and
+// 20 to 2000 rows and 40 heads 219 to 222 us, 113 at the library's rate; with a
+// window of 512 and 4 sinks 294 to 297, where the pairs that are seen take 106: a
+// block walks five tiles for its 512 keys and one for 4 sinks, and a unit of six
+// to seven steps has its border to pay.  One of 8192 rows with a window of 1024 and
+// 64 sinks 130 to 133 (71).  The ring has five slots of 32 KB, the most that
+// fit (with four: packed 226, with sinks 317).  A step's products are 2048 clocks by the tensor cores' nominal rate and
 // 2770 at the library's; a step takes about 2900.  The softmax hides behind that:
 // without the halves' vote (240 clocks of a block's chain) an earlier version took
 // 319 us against 321 in a burst.  A unit's border costs some 4000 clocks more (last

@@ -25,6 +25,13 @@
 // step_attention.cuh's.  A unit that was cut leaves its parts in the workspace; a
 // second kernel adds them, a warp for each column, spread over all SMs: with
 // one request the parts are megabytes, and one SM reads a tenth of one per microsecond.
+//
+// Measured, 32 heads over 8 cached ones of 128: 32 requests of 16 to 4095 keys with
+// trees of 17 to 48 rows over pages of 16 positions 72 us (cache, queries and outputs
+// at a copy's 6.78 TB/s 44); one request of 4095 keys with 60 rows 22.3 (2.7): launch
+// 5, cut and first tiles, then every part's last product, its way through the
+// workspace, and the second kernel's 4.  With keys on the M side, as for the few
+// columns of a chain, the same calls took 142 and 34.
 #include "step_attention.cuh"
 
 namespace dspark {
@@ -920,8 +927,9 @@ __device__ __forceinline__ void join_entries(const TreeArgs &A, const Cut &cut, 
 }
 
 // A warp takes 32 columns of a unit, a lane each, and some of their entries: 16 where there are up to three parts,
-// 4 where there are more, so that some 50 loads are in flight either way.  (For one request's 19 parts of 240 columns
-// 2, 4 and 8 entries: 27.3, 25.1 and 29.1 us for the call; 2 entries are bound by their instructions.)
+// 4 where there are more, so that some 50 loads are in flight either way.  (16 and 4 everywhere: one request's 19 parts
+// of 240 columns 30.7 and 22.3 us for the call, 32 requests' two or three parts 72.5 and 79.2.  2 and 8 entries for the
+// one request, in an earlier version where 4 took 25.1: 27.3 and 29.1; 2 entries are bound by their instructions.)
 constexpr int kFewParts = 3, kEntriesFew = 16, kManyParts = 10, kEntriesMany = 4;
 
 template <int D>
