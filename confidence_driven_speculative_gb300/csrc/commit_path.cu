@@ -9,7 +9,7 @@
 //
 // Bound: bytes, each moved entry read and written once.  256 requests in 16
 // layers of 8 heads of 128, 1.9 moves each, 14.0 us (a copy of as many bytes 9.2:
-// the moves lie in pieces of 256 bytes a head); one request 2.9, a launch
+// the moves are pieces of 2 KB, and three trips come first); one request 2.9, a launch
 // and three trips to memory, path to page to entry.
 #include <algorithm>
 

@@ -28,9 +28,9 @@
 //
 // Measured, 32 heads over 8 cached ones of 128: 32 requests of 16 to 4095 keys with
 // trees of 17 to 48 rows over pages of 16 positions 72 us (cache, queries and outputs
-// at a copy's 6.78 TB/s 44); one request of 4095 keys with 60 rows 22.3 (2.7): launch
-// 5, cut and first tiles, then every part's last product, its way through the
-// workspace, and the second kernel's 4.  With keys on the M side, as for the few
+// at a copy's 6.78 TB/s 44); one request of 4095 keys with 60 rows 22.3 (2.7): a
+// chain of launch, cut, first tiles, a part's last product, its way through the
+// workspace and the second kernel, whose loads are 4 of it.  With keys on the M side, as for the few
 // columns of a chain, the same calls took 142 and 34.
 #include "step_attention.cuh"
 

@@ -17,7 +17,7 @@
 // Measured: 256 requests of 16 to 4095 positions in pages of 16 that grow by 17,
 // 15.7 us (with one CTA in place of the cluster of 16, 19.5), most of it six trips
 // to L2 or through the cluster; 8 requests forked 8 ways with tails of 32 layers,
-// 8 heads of 128, pages of 64, 54.5, where a copy of the tails alone takes 53: 12
+// 8 heads of 128, pages of 64, 54.5, as long as a copy of as many bytes: 12
 // CTAs an SM for the copies (with 4, 6 and 8: 66, 61 and 59, the step 14.3 to 15.0).
 #include "cache.cuh"
 #include "dspark_internal.cuh"
