@@ -17,8 +17,11 @@
 // Measured: 256 requests of 16 to 4095 positions in pages of 16 that grow by 17,
 // 15.7 us (with one CTA in place of the cluster of 16, 19.5), most of it six trips
 // to L2 or through the cluster; 8 requests forked 8 ways with tails of 32 layers,
-// 8 heads of 128, pages of 64, 54.5, as long as a copy of as many bytes: 12
-// CTAs an SM for the copies (with 4, 6 and 8: 66, 61 and 59, the step 14.3 to 15.0).
+// 8 heads of 128, pages of 64, 50 (a copy of as many bytes 54.6; seven requests
+// read each source, which L2 serves, so 31 would be the least): 12 CTAs an SM for the
+// copies (with 3, 4, 6 and 9: 66, 66, 61 and 56 against then 54, the step 14.3 to
+// 15.3), their stores streaming (54 without; units taken off a counter by 3 or 4 CTAs
+// an SM 55 and 52).
 #include "cache.cuh"
 #include "dspark_internal.cuh"
 #include "tcgen05.cuh"
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(kThreadsCopy) copy_tails_kernel(const CopyArgs
                     if (s + k * step < c.z) x[k] = __ldcs(reinterpret_cast<const uint4 *>(from + (s + k * step) * A.slot_stride));
 #pragma unroll
                 for (int k = 0; k < kCopies; ++k)
-                    if (s + k * step < c.z) *reinterpret_cast<uint4 *>(to + (s + k * step) * A.slot_stride) = x[k];
+                    if (s + k * step < c.z) __stcs(reinterpret_cast<uint4 *>(to + (s + k * step) * A.slot_stride), x[k]);
             }
         }
     }
