@@ -8,7 +8,7 @@
 // needs no barrier.
 //
 // Bound: bytes, each moved entry read and written once.  256 requests in 16
-// layers of 8 heads of 128, 1.9 moves each, 14.0 us (a copy of as many bytes 9.2:
+// layers of 8 heads of 128, 1.9 moves each, 12.8 us (a copy of as many bytes 9.2:
 // the moves are pieces of 2 KB, and three trips come first); one request 2.9, a launch
 // and three trips to memory, path to page to entry.
 #include <algorithm>
@@ -72,6 +72,17 @@ __global__ void __launch_bounds__(kThreadsCommit, kLayers == 2 ? 5 : 6) commit_p
         if (tid == 0) moves = n;
     }
     __syncthreads();
+    // Many moves go past L2 (256 requests in 16 layers 12.7 us, without 14.1), a few are not worth it (one request
+    // in 32 layers 3.1, without 2.9).
+    auto load = [](const uint16_t *p) {
+        const uint4 *const x = reinterpret_cast<const uint4 *>(p);
+        return kLayers == 2 ? __ldcs(x) : *x;
+    };
+    auto store = [](uint16_t *p, const uint4 &y) {
+        uint4 *const x = reinterpret_cast<uint4 *>(p);
+        if (kLayers == 2) __stcs(x, y);
+        else *x = y;
+    };
     const int n = moves, per = A.heads * A.chunks;
     const bool both = kLayers == 2 && layer0 + 1 < A.layers;
     for (int x = tid; n > 0 && x < 2 * per; x += kThreadsCommit) {
@@ -83,15 +94,15 @@ __global__ void __launch_bounds__(kThreadsCommit, kLayers == 2 ? 5 : 6) commit_p
             for (int m = 0; m < kMoves; ++m) {
                 if (m0 + m >= n) break;
                 const uint16_t *src = base + from[m0 + m];
-                v[0][m] = *reinterpret_cast<const uint4 *>(src);
-                if (kLayers == 2 && both) v[kLayers - 1][m] = *reinterpret_cast<const uint4 *>(src + A.layer_stride);
+                v[0][m] = load(src);
+                if (kLayers == 2 && both) v[kLayers - 1][m] = load(src + A.layer_stride);
             }
 #pragma unroll
             for (int m = 0; m < kMoves; ++m) {
                 if (m0 + m >= n) break;
                 uint16_t *dst = base + to[m0 + m];
-                *reinterpret_cast<uint4 *>(dst) = v[0][m];
-                if (kLayers == 2 && both) *reinterpret_cast<uint4 *>(dst + A.layer_stride) = v[kLayers - 1][m];
+                store(dst, v[0][m]);
+                if (kLayers == 2 && both) store(dst + A.layer_stride, v[kLayers - 1][m]);
             }
         }
     }
@@ -102,7 +113,8 @@ __global__ void __launch_bounds__(kThreadsCommit, kLayers == 2 ? 5 : 6) commit_p
 cudaError_t launch_commit_path(const dspark_cache &c, int B, int q_max, int max_pages, const int32_t *block_table,
                                const int32_t *seq_lens, const int32_t *path, int sms, cudaStream_t s) {
     // Two layers to a CTA, whose path and pages are looked up once, where there are CTAs enough: 48 requests in 32
-    // layers 6.6 us (one layer to a CTA 6.0), 64 in 32 7.7 (7.9), 256 in 16 13.7 (15.2).
+    // layers 6.6 us (one layer to a CTA 6.0), 64 in 32 7.7 (7.9), 256 in 16 13.7 (15.2), all before loads
+    // and stores were streaming ones.
     const bool two = int64_t(B) * c.layers > 12 * sms;
     const int groups = two ? (c.layers + 1) / 2 : c.layers;
     const CommitArgs A{B, q_max, max_pages, c.layers, groups, c.Hkv, c.D / 8, c.page_size, c.num_pages,
