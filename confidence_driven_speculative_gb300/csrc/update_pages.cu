@@ -15,13 +15,15 @@
 // hardware barriers in between; a second kernel on all SMs copies the tails' entries.
 //
 // Measured: 256 requests of 16 to 4095 positions in pages of 16 that grow by 17,
-// 15.7 us (with one CTA in place of the cluster of 16, 19.5), most of it six trips
-// to L2 or through the cluster; 8 requests forked 8 ways with tails of 32 layers,
+// 14.6 us (with one CTA in place of the cluster of 16, 19.5), most of it six trips
+// to L2 or through the cluster and a second launch; 8 requests forked 8 ways with tails of 32 layers,
 // 8 heads of 128, pages of 64, 50 (a copy of as many bytes 54.6; seven requests
 // read each source, which L2 serves, so 31 would be the least): 12 CTAs an SM for the
 // copies (with 3, 4, 6 and 9: 66, 66, 61 and 56 against then 54, the step 14.3 to
 // 15.3), their stores streaming (54 without; units taken off a counter by 3 or 4 CTAs
 // an SM 55 and 52).
+#include <algorithm>
+
 #include "cache.cuh"
 #include "dspark_internal.cuh"
 #include "tcgen05.cuh"
@@ -402,7 +404,8 @@ cudaError_t launch_update_pages(const dspark_pages &p, int sms, cudaStream_t s) 
     if (e != cudaSuccess || !c.k_cache) return e;
     const CopyArgs C{c.layers, c.Hkv, c.D / 8, c.layer_stride, c.page_stride, c.slot_stride, c.head_stride,
                      static_cast<uint16_t *>(c.k_cache), static_cast<uint16_t *>(c.v_cache), A.copies, A.n_copies};
-    return launch_overlapped(copy_tails_kernel, 12 * sms, kThreadsCopy, 0, s, C);
+    const int ctas = int(std::min<int64_t>(12 * sms, int64_t(2) * c.layers * p.B));  // no more than there may be tails
+    return launch_overlapped(copy_tails_kernel, ctas, kThreadsCopy, 0, s, C);
 }
 
 }  // namespace dspark
