@@ -90,6 +90,13 @@ def test_many_requests(cuda_lib, B):
     assert want["accept_len"].max() > 8
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("levels", [0, 3])
+def test_rows_that_a_cta_reads_in_several_rounds(cuda_lib, levels, dtype):
+    """So many requests that each has one CTA."""
+    Case(6 + levels, [1 + i % 3 for i in range(600)], 17000 if levels else 33000, dtype, levels=levels).check()
+
+
 def test_a_chain_of_64_rows_accepted_in_full(cuda_lib):
     for V in (1024, 32000):
         c = Case(1, [64, 64], V, deep=1.0, go=1.0)
