@@ -28,9 +28,9 @@
 //
 // Measured, 32 heads over 8 cached ones of 128: 32 requests of 16 to 4095 keys with
 // trees of 17 to 48 rows over pages of 16 positions 72 us (cache, queries and outputs
-// at a copy's 6.78 TB/s 44); one request of 4095 keys with 60 rows 22.3 (2.7): a
+// at a copy's 6.78 TB/s 44); one request of 4095 keys with 60 rows 18.5 (2.7): a
 // chain of launch, cut, first tiles, a part's last product, its way through the
-// workspace and the second kernel, whose loads are 4 of it.  With keys on the M side, as for the few
+// workspace and the second kernel.  With keys on the M side, as for the few
 // columns of a chain, the same calls took 142 and 34.
 #include "step_attention.cuh"
 
@@ -45,6 +45,11 @@ constexpr int kPartReaders = 19; // warps that read them
 constexpr int kBad = 8;          // ring of the tiles' bad-key words
 // Places of the list: of a tile of one block, of one of two, and what a unit costs beside its tiles.
 constexpr int kTileOne = 2, kTileTwo = 3, kUnitPlaces = 10;
+// Up to so many tiles a CTA all units have one block: the two blocks of a request then go to different CTAs, which
+// read the same keys but have half as many columns to write out and to add up.  Trees of 60 rows, 8 cached heads,
+// one block and two: 1 request of 4095 keys (1.7 tiles a CTA) 18.5 us and 22.2, 8 of 1000 (3.8) 27.2 and 29.4,
+// 4 of 4095 (6.9) 34.9 and 36.0, 1 of 16 000 (6.6) 31.4 and 29.5, 12 of 2000 (10.4) 49.5 and 44.0.
+constexpr int kFewTiles = 6;
 
 // A unit that was cut, for the second kernel.
 struct Cut {
@@ -80,6 +85,18 @@ struct TreeRow {
         return (cached | own) & below(q.kend - k0);
     }
 };
+
+// The same request in units of up to `rows` rows.
+__device__ __forceinline__ Req in_units_of(Req r, int rows) {
+    if (r.per > rows) {
+        // for up to 64: the quotient lies 1 / (2 b) at least from a whole number
+        auto ceil_div = [](int a, int b) { return int(__fdividef(float(a + b) - 0.5f, float(b))); };
+        r.blocks = ceil_div(r.n, rows);
+        r.per = ceil_div(r.n, r.blocks);
+        r.blocks = ceil_div(r.n, r.per);
+    }
+    return r;
+}
 
 // What a CTA does of one unit.
 struct Part {
@@ -294,9 +311,19 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
         const int me = blockIdx.x, per = (A.B + 31) / 32, b_lo = min(lane * per, A.B), b_hi = min(b_lo + per, A.B);
         auto places_of = [&](const Req &r) { return r.per > A.rb ? kTileTwo : kTileOne; };  // of a tile
         auto cost_of = [&](const Req &r) { return r.blocks * A.Hkv * (r.nt * places_of(r) + U); };
-        int mine = 0;
-#pragma unroll 4
-        for (int b = b_lo; b < b_hi; ++b) mine += cost_of(load_req<kSinks>(A, b));
+        // Units of two blocks or of one: see kFewTiles.
+        int two = 0, tiles_two = 0;
+        uint32_t one = 0;  // (may pass 32 bits where it is not used)
+        // (unrolled, the loop costs its fetch: 0.4 us for few requests, and a lane's requests share a sector)
+#pragma unroll 1
+        for (int b = b_lo; b < b_hi; ++b) {
+            const Req r = load_req<kSinks>(A, b);
+            two += cost_of(r);
+            one += uint32_t(cost_of(in_units_of(r, A.rb)));
+            tiles_two += r.blocks * A.Hkv * r.nt;
+        }
+        const bool few = __reduce_add_sync(0xffffffffu, tiles_two) <= kFewTiles * int(gridDim.x);
+        const int rows_cap = few ? A.rb : A.rows_cap, mine = few ? int(one) : two;
         int sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -313,7 +340,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
             const int src = __ffs(who) - 1;
             if (lane == src)
                 for (b = b_lo; b < b_hi; ++b) {
-                    const int c = cost_of(load_req<kSinks>(A, b));
+                    const int c = cost_of(in_units_of(load_req<kSinks>(A, b), rows_cap));
                     if (start < place + c) break;
                     place += c;
                 }
@@ -326,7 +353,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs A, const __grid_constant_
         int published = 0, issued = 0, q_use = 0, jobs = 0;
         bool ok = true;
         for (; b < A.B && place < end && ok; ++b) {
-            const Req q = load_req<kSinks>(A, b);
+            const Req q = in_units_of(load_req<kSinks>(A, b), rows_cap);
             const int w = places_of(q), each = q.nt * w + U, units = q.blocks * A.Hkv;
             int i = max(start - place, 0) / each;
             for (; i < units && place + i * each < end && ok; ++i) {
@@ -927,9 +954,10 @@ __device__ __forceinline__ void join_entries(const TreeArgs &A, const Cut &cut, 
 }
 
 // A warp takes 32 columns of a unit, a lane each, and some of their entries: 16 where there are up to three parts,
-// 4 where there are more, so that some 50 loads are in flight either way.  (16 and 4 everywhere: one request's 19 parts
-// of 240 columns 30.7 and 22.3 us for the call, 32 requests' two or three parts 72.5 and 79.2.  2 and 8 entries for the
-// one request, in an earlier version where 4 took 25.1: 27.3 and 29.1; 2 entries are bound by their instructions.)
+// 4 where there are more, so that some 50 loads are in flight either way.  (16 and 4 everywhere: 19 parts of 240 columns
+// 30.7 and 22.3 us for the call, 32 requests' two or three parts 72.5 and 79.2.  2 and 8 entries for the 19 parts, in an
+// earlier version where 4 took 25.1: 27.3 and 29.1; 2 entries are bound by their instructions.  A third kind, 8 entries
+// of up to 6 parts: 2 requests of 4095 keys 25.2 to 23.8, but one 18.5 to 18.7 and one of 65 000 62.2 to 64.6.)
 constexpr int kFewParts = 3, kEntriesFew = 16, kManyParts = 10, kEntriesMany = 4;
 
 template <int D>
