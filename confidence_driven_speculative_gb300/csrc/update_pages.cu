@@ -15,9 +15,9 @@
 // hardware barriers in between; a second kernel on all SMs copies the tails' entries.
 //
 // Measured: 256 requests of 16 to 4095 positions in pages of 16 that grow by 17,
-// 12.5 us (with one CTA in place of the cluster of 16, some 5 more), most of it six trips
+// 12.0 us (with one CTA in place of the cluster of 16, some 5 more), most of it six trips
 // to L2 or through the cluster and a second launch; the same in pages of one position
-// 88 (half a million entries on 16 SMs); 8 requests forked 8 ways with tails of 32 layers,
+// 86 (half a million entries on 16 SMs); 8 requests forked 8 ways with tails of 32 layers,
 // 8 heads of 128, pages of 64, 50 (a copy of as many bytes 54.6; seven requests
 // read each source, which L2 serves, so 31 would be the least): 12 CTAs an SM for the
 // copies (with 3, 4, 6 and 9: 66, 66, 61 and 56 against then 54, the step 14.3 to
@@ -36,7 +36,6 @@ constexpr int kThreadsPages = 1024;
 static_assert(kThreadsPages == 32 * 32, "the scan takes a warp's sums from a lane each");
 constexpr int kSeg = 256;               // entries of a table that a warp takes at once
 constexpr int kPages = 8;               // pages in a row that a thread looks at
-constexpr int kFewPages = 4;            // new pages that a thread writes by itself; of more, a warp
 constexpr int kFull = 0x7fffffff;       // claim of a request that only reads
 constexpr int kWriters = 1 << 17;       // kWriters - b: claim of request b that writes
 
@@ -48,8 +47,8 @@ struct PagesArgs {
     int32_t *claim;   // [num_pages], 0 between calls
     int32_t *free_list;  // [num_pages]
     int4 *copies;        // [B] source, destination, entries
-    int32_t *first_rank; // [B] rank of a request's first new page, where it wants many
-    int32_t *n_copies, *many;  // copies; does some request want many?
+    int32_t *first_rank; // [B] rank of a request's first new page
+    int32_t *n_copies;
 };
 
 // A request: whose pages it takes over, and which.
@@ -119,7 +118,7 @@ __global__ void __launch_bounds__(kThreadsPages, 1) update_pages_kernel(const Pa
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // A thread looks after `per` requests; of the first it keeps what it knows.
-    if (g == 0) *A.n_copies = *A.many = 0;
+    if (g == 0) *A.n_copies = 0;
     const int per = (A.B + kAll - 1) / kAll;
     const int b_lo = min(g * per, A.B), b_hi = min(b_lo + per, A.B);
     auto tail_page = [&](const Want &w) {  // that the tail lies in, or -1
@@ -271,12 +270,9 @@ __global__ void __launch_bounds__(kThreadsPages, 1) update_pages_kernel(const Pa
     int start = start0;
     for (int b = b_lo; b < b_hi; ++b) {
         const Want w = b == b_lo ? w0 : load_want(A, b);
-        const int share = b == b_lo ? share0 : shares(b, tail_page(w)), count = Fresh(A, w).count;
-        if (count > kFewPages) {
-            A.first_rank[b] = start + share;
-            *A.many = 1;
-        }
-        start += count + share;
+        const int share = b == b_lo ? share0 : shares(b, tail_page(w));
+        A.first_rank[b] = start + share;
+        start += Fresh(A, w).count + share;
     }
     cluster_sync();
 
@@ -296,30 +292,22 @@ __global__ void __launch_bounds__(kThreadsPages, 1) update_pages_kernel(const Pa
                            : given < share ? w.keep
                                            : max(f.place(w, given - share) * A.page_size, w.keep);
     };
-    // New pages first, first + step, ..; `start` is the rank of the first new one.
-    auto give = [&](int b, const Want &w, const Fresh &f, int start, int first, int step) {
-        const int given = min(max(there - start, 0), f.count);
-        for (int i = first; i < given; i += step)
-            A.table_out[int64_t(b) * A.max_pages + f.place(w, i)] = __ldcg(A.free_list + start + i);
-    };
-    const int many = __ldcg(A.many);
     start = start0;
     for (int b = b_lo; b < b_hi; ++b) {
         const Want w = b == b_lo ? w0 : load_want(A, b);
         const int page = b == b_lo ? tail0 : tail_page(w), share = b == b_lo ? share0 : shares(b, page);
         const Fresh f(A, w);
         finish(b, w, f, start, share, page);
-        if (f.count <= kFewPages) give(b, w, f, start + share, 0, 1);
         start += f.count + share;
     }
-    // The requests lie with neighbouring threads.  Where some want many pages, all warps of the cluster take them:
-    // 192 requests that want up to 47 each 41 -> 12.5 us against a loop over each warp's own.
-    if (many) {
-        for (int b = gw; b < A.B; b += kAllWarps) {
-            const Want w = load_want(A, b);
-            const Fresh f(A, w);
-            if (f.count > kFewPages) give(b, w, f, __ldcg(A.first_rank + b), lane, 32);
-        }
+    // New pages, a request to a warp.  (By the threads that know the requests, which are neighbours, the others of a
+    // warp waiting: 192 requests that want up to 47 each 41 us against 12.5.)
+    for (int b = gw; b < A.B; b += kAllWarps) {
+        const Want w = load_want(A, b);
+        const Fresh f(A, w);
+        const int first = __ldcg(A.first_rank + b), given = min(max(there - first, 0), f.count);
+        for (int i = lane; i < given; i += 32)
+            A.table_out[int64_t(b) * A.max_pages + f.place(w, i)] = __ldcg(A.free_list + first + i);
     }
     if (per > 1) cluster_sync();  // claims are read up to here
     for (int64_t p = int64_t(g) * kPages; p < A.num_pages; p += chunk) {
@@ -374,7 +362,7 @@ __global__ void __launch_bounds__(kThreadsCopy) copy_tails_kernel(const CopyArgs
     }
 }
 
-// The workspace: status word, number of copies, many; claims; free pages; copies; first ranks.  The claims, which are zero between
+// The workspace: status word, number of copies; claims; free pages; copies; first ranks.  The claims, which are zero between
 // calls, lie where they do for every B.
 struct PagesLayout { size_t claim, free_list, copies, first_rank, total; };
 PagesLayout pages_layout(int B, int num_pages) {
@@ -403,7 +391,7 @@ cudaError_t launch_update_pages(const dspark_pages &p, int sms, cudaStream_t s) 
                 p.want_len, p.first_pos, p.held, p.table_out, p.granted_len, p.tail_src, p.tail_dst, p.totals,
                 reinterpret_cast<int32_t *>(ws + l.claim), reinterpret_cast<int32_t *>(ws + l.free_list),
                 reinterpret_cast<int4 *>(ws + l.copies), reinterpret_cast<int32_t *>(ws + l.first_rank),
-                reinterpret_cast<int32_t *>(ws) + 1, reinterpret_cast<int32_t *>(ws) + 2};
+                reinterpret_cast<int32_t *>(ws) + 1};
     constexpr int kCtas = 16;
     cudaError_t e = cudaFuncSetAttribute(update_pages_kernel<kCtas>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
