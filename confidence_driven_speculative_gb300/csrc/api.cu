@@ -947,6 +947,9 @@ dspark_status dspark_update_pages(const dspark_pages *p, dspark_stream_t stream)
     if (st || (st = check_batch(p->B_in, "B_in", fn))) return st;
     if (p->sinks < 0) return fail(DSPARK_EINVAL, "%s: sinks=%d < 0", fn, p->sinks);
     if ((st = check_layers(&p->cache, p->max_pages, p->cache.k_cache || p->cache.v_cache, fn))) return st;
+    // Wanted pages are numbered over the whole batch, and no request wants more than its row of the table holds.
+    if ((long long)p->B * p->max_pages > INT32_MAX)
+        return fail(DSPARK_EINVAL, "%s: B=%d max_pages=%d is too large a batch", fn, p->B, p->max_pages);
     if (p->B == 0) return DSPARK_OK;
     if (p->B_in > 0) REQUIRE(p->table_in);
     REQUIRE(p->keep_len);

@@ -607,7 +607,7 @@ typedef struct dspark_pages {
     int32_t B_in;        /* rows of table_in, 0..DSPARK_MAX_B */
     int32_t B;           /* requests of the next step, 0..DSPARK_MAX_B (0: the call is a no-op,
                             every page is free, totals are not written) */
-    int32_t max_pages;   /* columns of both tables, >= 1 */
+    int32_t max_pages;   /* columns of both tables, >= 1; B * max_pages below 2^31 */
     int32_t sinks;       /* positions that first_pos does not drop, >= 0 */
 
     /* ---- inputs (device, read only) -------------------------------------- */
