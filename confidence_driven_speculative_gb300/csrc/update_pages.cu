@@ -65,7 +65,7 @@ __device__ __forceinline__ Want load_want(const PagesArgs &A, int b) {
     const int cap = A.max_pages * A.page_size;
     w.parent = A.parent ? A.parent[b] : b;
     if (w.parent >= A.B_in) w.parent = -1;
-    w.keep = min(max(A.keep_len[b], 0), cap);
+    w.keep = w.parent < 0 ? 0 : min(max(A.keep_len[b], 0), cap);  // nothing is kept of no parent
     w.want = min(max(A.want_len[b], w.keep), cap);
     w.first = A.first_pos ? page_of(max(A.first_pos[b], 0)) : 0;
     w.keep_pages = page_of(w.keep + A.page_size - 1);

@@ -614,7 +614,8 @@ typedef struct dspark_pages {
     const int32_t *table_in;  /* [B_in, max_pages] pages of the requests so far; an entry
                                  outside [0, num_pages) is none */
     const int32_t *parent;    /* [B] row of table_in that request b continues; outside
-                                 [0, B_in): it starts from nothing.  NULL: b itself */
+                                 [0, B_in): it starts from nothing, as if keep_len were 0.
+                                 NULL: b itself */
     const int32_t *keep_len;  /* [B] positions taken over from the parent */
     const int32_t *want_len;  /* [B] positions that have memory afterwards; those from
                                  keep_len[b] on are about to be written.  Less than keep_len

@@ -49,7 +49,8 @@ def update_pages(table_in, parent, keep, want, page: int, num_pages: int, first=
     """(table_out, granted, tail_src, tail_dst, totals) as the call leaves them."""
     B, width = len(keep), table_in.shape[1]
     cap = width * page
-    keep = [min(max(int(x), 0), cap) for x in keep]
+    parent = [int(p) for p in (range(B) if parent is None else parent)]
+    keep = [min(max(int(x), 0), cap) if 0 <= p < table_in.shape[0] else 0 for x, p in zip(keep, parent)]
     want = [min(max(int(w), k), cap) for w, k in zip(want, keep)]
     first = [0] * B if first is None else [max(int(x), 0) for x in first]
     held = np.zeros(num_pages, bool) if held is None else np.asarray(held) != 0
@@ -57,9 +58,7 @@ def update_pages(table_in, parent, keep, want, page: int, num_pages: int, first=
     out = np.full((B, width), -1, np.int32)
     readers, writers = set(), {}
     for b in range(B):
-        p = b if parent is None else int(parent[b])
-        if not 0 <= p < table_in.shape[0]:
-            continue
+        p = parent[b]
         for i in range(-(-keep[b] // page)):
             x = int(table_in[p, i])
             if drops(b, i) or not 0 <= x < num_pages:

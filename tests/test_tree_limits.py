@@ -2,9 +2,11 @@
 workspaces that serve smaller calls, tables that overlap.  All of it is decided on the host."""
 import ctypes
 
+import numpy as np
 import pytest
 
 from confidence_driven_speculative_gb300 import _build, binding
+from oracle import tree as ot
 from tests.test_tree_abi import EINVAL, EWORKSPACE, pages
 
 
@@ -23,3 +25,12 @@ def test_pages_of_more_entries_than_32_bits_count(lib, B, max_pages, page):
     assert "too large a batch" in binding.last_error()
     kw["workspace_bytes"] = 8  # as many columns as the limit allows: the next check speaks
     assert lib.dspark_update_pages(ctypes.byref(pages(max_pages=(2 ** 31 - 1) // B, **kw)), None) == EWORKSPACE
+
+
+def test_oracle_nothing_is_kept_of_no_parent():
+    """By hand: pages of 16; whatever keep_len says, pages from the first position on."""
+    table = np.array([[2, 4, -1, -1, -1]], np.int32)
+    out, granted, src, dst, totals = ot.update_pages(table, [-1, 0, 1], [40, 20, 16], [70, 21, 9], 16, 12)
+    assert out.tolist() == [[0, 1, 3, 5, 6], [2, 4, -1, -1, -1], [7, -1, -1, -1, -1]]
+    assert granted.tolist() == [70, 21, 9] and totals.tolist() == [4, 0]
+    assert src.tolist() == dst.tolist() == [-1, -1, -1]
