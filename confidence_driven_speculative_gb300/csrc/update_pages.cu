@@ -121,8 +121,9 @@ __global__ void __launch_bounds__(kThreadsPages, 1) update_pages_kernel(const Pa
     if (g == 0) *A.n_copies = 0;
     const int per = (A.B + kAll - 1) / kAll;
     const int b_lo = min(g * per, A.B), b_hi = min(b_lo + per, A.B);
+    auto tail_kept = [&](const Want &w) { return w.tail >= 0 && (w.tail >= w.first || w.tail < A.sink_pages); };
     auto tail_page = [&](const Want &w) {  // that the tail lies in, or -1
-        if (w.tail < 0 || w.parent < 0 || !(w.tail >= w.first || w.tail < A.sink_pages)) return -1;
+        if (w.parent < 0 || !tail_kept(w)) return -1;
         const int page = A.table_in[int64_t(w.parent) * A.max_pages + w.tail];
         return page < A.num_pages ? page : -1;
     };
@@ -288,8 +289,8 @@ __global__ void __launch_bounds__(kThreadsPages, 1) update_pages_kernel(const Pa
         }
         A.tail_src[b] = src;
         A.tail_dst[b] = dst;
-        A.granted_len[b] = given == all ? w.want
-                           : given < share ? w.keep
+        A.granted_len[b] = (tail_kept(w) && page < 0) || given < share ? w.keep  // where keep lies has no memory
+                           : given == all ? w.want
                                            : max(f.place(w, given - share) * A.page_size, w.keep);
     };
     start = start0;

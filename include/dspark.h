@@ -627,8 +627,9 @@ typedef struct dspark_pages {
 
     /* ---- outputs (device, caller-allocated) ------------------------------ */
     int32_t *table_out;   /* [B, max_pages], apart from table_in; -1 where there is no page */
-    int32_t *granted_len; /* [B] want_len, or where pages ran out the first position that
-                             has no memory to be written */
+    int32_t *granted_len; /* [B] want_len, or the first position to be written that has no
+                             memory: where pages ran out, or where the parent's row has none
+                             for the page that keep_len lies inside */
     int32_t *tail_src;    /* [B] page whose first keep_len % page_size entries were copied */
     int32_t *tail_dst;    /* [B] to this one, in all layers; -1 and -1 for none */
     int32_t *totals;      /* [2] pages left free, and pages that were wanted but missing */

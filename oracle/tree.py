@@ -72,6 +72,9 @@ def update_pages(table_in, parent, keep, want, page: int, num_pages: int, first=
     n_free, asked = len(free), 0
     granted, src, dst = list(want), [-1] * B, [-1] * B
     for b in range(B):
+        at = keep[b] // page
+        if want[b] > keep[b] and keep[b] % page and not drops(b, at) and out[b, at] < 0:
+            granted[b] = keep[b]  # the page that keep lies inside is missing
         for i in range(-(-want[b] // page)):
             x = int(out[b, i])
             own = x >= 0 and (i + 1) * page > keep[b] and want[b] > keep[b]

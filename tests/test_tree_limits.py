@@ -34,3 +34,14 @@ def test_oracle_nothing_is_kept_of_no_parent():
     assert out.tolist() == [[0, 1, 3, 5, 6], [2, 4, -1, -1, -1], [7, -1, -1, -1, -1]]
     assert granted.tolist() == [70, 21, 9] and totals.tolist() == [4, 0]
     assert src.tolist() == dst.tolist() == [-1, -1, -1]
+
+
+def test_oracle_a_last_page_that_is_missing_is_told():
+    """By hand: pages of 16.  Nothing can be written at position 20 if its page is none, except where nobody
+    looks at it any more, or writes it."""
+    table = np.array([[2, -1, -1, -1], [5, 12, -1, -1]], np.int32)
+    out, granted, src, dst, totals = ot.update_pages(
+        table, [0, 1, 0, 0, 0], [20, 20, 20, 16, 20], [40, 40, 20, 40, 40], 16, 12, first=[0, 0, 0, 0, 32])
+    assert granted.tolist() == [20, 20, 20, 40, 40]
+    assert out.tolist() == [[2, -1, 0, -1], [5, -1, 1, -1], [2, -1, -1, -1], [2, 3, 4, -1], [-1, -1, 6, -1]]
+    assert totals.tolist() == [5, 0]
