@@ -673,7 +673,8 @@ dspark_status check_in_place(const dspark_attn *a, const void *x, const void *ro
     return DSPARK_OK;
 }
 
-dspark_status check_attn_softmax(const dspark_attn *a, const char *fn) {
+// need: bytes of workspace
+dspark_status check_attn_softmax(const dspark_attn *a, size_t need, const char *fn) {
     if (!(a->scale > 0.0f) || std::isinf(a->scale))
         return fail(DSPARK_EINVAL, "%s: scale must be finite and > 0", fn);
     REQUIRE(a->q_rot);
@@ -681,7 +682,6 @@ dspark_status check_attn_softmax(const dspark_attn *a, const char *fn) {
     REQUIRE(a->out);
     REQUIRE_ALIGNED(a->q_rot, 16);
     REQUIRE_ALIGNED(a->out, 16);
-    const size_t need = dspark::attn_workspace_bytes(a->Hq, a->Hkv, a->D, a->q_max);
     if (!a->workspace) return fail(DSPARK_EWORKSPACE, "%s: workspace is NULL", fn);
     if (!aligned(a->workspace, 256))
         return fail(DSPARK_EWORKSPACE, "%s: workspace is not 256-byte aligned", fn);
@@ -742,7 +742,9 @@ dspark_status step_attention(const dspark_attn *a, const uint64_t *row_seen, boo
         return fail(DSPARK_EINVAL, "%s: %d query heads per cached head, at most %d", fn,
                     a->Hq / a->Hkv, DSPARK_MAX_STEP_GROUP);
     if (a->B == 0 || a->rows == 0) return DSPARK_OK;
-    if ((st = check_attn_softmax(a, fn))) return st;
+    const size_t need = tree ? dspark::tree_attn_workspace_bytes(a->Hq, a->Hkv, a->D, a->q_max)
+                             : dspark::attn_workspace_bytes(a->Hq, a->Hkv, a->D, a->q_max);
+    if ((st = check_attn_softmax(a, need, fn))) return st;
     if ((st = check_cache(a, fn))) return st;
     if (!dspark::step_strides_ok(*a))
         return fail(DSPARK_EINVAL,
@@ -773,7 +775,9 @@ dspark_status prompt_attention(const dspark_attn *a, int32_t sinks, const char *
     if (st) return st;
     if (sinks < 0) return fail(DSPARK_EINVAL, "%s: sinks=%d < 0", fn, sinks);
     if (a->B == 0 || a->rows == 0) return DSPARK_OK;
-    if ((st = check_attn_softmax(a, fn))) return st;
+    // the same for every q_max
+    const size_t need = dspark::attn_workspace_bytes(a->Hq, a->Hkv, a->D, DSPARK_MAX_STEP_ROWS + 1);
+    if ((st = check_attn_softmax(a, need, fn))) return st;
     REQUIRE(a->k_rot);
     REQUIRE(a->v);
     REQUIRE_ALIGNED(a->k_rot, 16);
@@ -839,7 +843,10 @@ size_t dspark_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t D, int32_t q_
     if (Hq < 1 || Hq > DSPARK_MAX_HEADS || Hkv < 1 || Hkv > Hq || Hq % Hkv || (D != 64 && D != 128) ||
         q_max < 1)
         return 0;
-    return dspark::attn_workspace_bytes(Hq, Hkv, D, q_max);
+    const size_t bytes = dspark::attn_workspace_bytes(Hq, Hkv, D, q_max);
+    if (q_max > DSPARK_MAX_STEP_ROWS || Hq / Hkv > DSPARK_MAX_STEP_GROUP) return bytes;
+    // (one more row than a tree has: what serves 65 rows serves fewer, in a tree or not)
+    return std::max(bytes, dspark::tree_attn_workspace_bytes(Hq, Hkv, D, std::min(q_max, DSPARK_MAX_TREE_ROWS)));
 }
 
 dspark_status dspark_rope_append(const dspark_attn *a, dspark_stream_t stream) {

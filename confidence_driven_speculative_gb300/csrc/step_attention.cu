@@ -7,10 +7,8 @@ namespace dspark {
 size_t attn_workspace_bytes(int Hq, int Hkv, int D, int q_max) {
     if (q_max > DSPARK_MAX_STEP_ROWS) return kHeaderBytes;  // dspark_prompt_attention's
     const size_t cols = size_t(step_columns(Hq, Hkv, q_max));
-    const size_t step = kHeaderBytes + align256(2 * kAttnMaxCtas * cols * D * sizeof(float)) +
-                        align256(2 * kAttnMaxCtas * 2 * cols * sizeof(float));
-    if (q_max > DSPARK_MAX_TREE_ROWS || Hq / Hkv > DSPARK_MAX_STEP_GROUP) return step;
-    return std::max(step, tree_attn_workspace_bytes(Hq, Hkv, D, q_max));
+    return kHeaderBytes + align256(2 * kAttnMaxCtas * cols * D * sizeof(float)) +
+           align256(2 * kAttnMaxCtas * 2 * cols * sizeof(float));
 }
 
 bool step_strides_ok(const dspark_attn &a) {

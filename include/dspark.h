@@ -416,7 +416,10 @@ typedef struct dspark_attn {
 } dspark_attn;
 
 /* Bytes of workspace that the attention calls need for these heads and this
- * q_max (any B, any length).  Returns 0 outside the limits above. */
+ * q_max (any B, any length).  Up to DSPARK_MAX_STEP_ROWS one of a larger q_max
+ * serves the calls of a smaller one, trees among them; above that only
+ * dspark_prompt_attention is meant, which needs the same few bytes for every
+ * q_max.  Returns 0 outside the limits above. */
 size_t dspark_attn_workspace_size(int32_t Hq, int32_t Hkv, int32_t D, int32_t q_max);
 
 /*

@@ -1,0 +1,35 @@
+"""One workspace of the largest batch serves the smaller ones: sized as a program sizes it, once."""
+import numpy as np
+import pytest
+import torch
+
+from confidence_driven_speculative_gb300 import binding
+from tests.test_gpu_attention_sinks import Prompt, Step
+from tests.test_gpu_step_attention_tree import Tree
+
+pytestmark = pytest.mark.gpu
+
+
+def workspace(size):
+    ws = torch.empty(size + 256, dtype=torch.uint8, device="cuda")
+    ws[size:] = 0xa5  # nothing is written behind it
+    binding.dspark_workspace_init(ws.data_ptr(), size)
+    return ws
+
+
+def test_attention_calls_on_a_workspace_of_65_rows(cuda_lib):
+    heads = dict(Hq=32, Hkv=8, D=128)
+    size = binding.dspark_attn_workspace_size(32, 8, 128, 65)
+    ws = workspace(size)
+    long = dict(ctx=[3000, 40, 700, 1], page=16, **heads)
+    cases = [Step(1, 4, n=[64, 3, 33, 9], window=900, **long), Tree(2, n=[64, 1, 33, 17], **long),
+             Step(3, 4, n=[40, 3, 2, 9], window=900, **long), Tree(4, n=[9, 1, 2, 3], **long),
+             Prompt(5, 4, [300, 31], window=100, **heads)]
+    want = [c.call() for c in cases]
+    for c in cases:
+        c.h.attn.workspace, c.h.attn.workspace_bytes = ws.data_ptr(), size
+    for _ in range(2):
+        for c, w in zip(cases, want):
+            assert np.array_equal(c.call(), w)
+    assert binding.dspark_read_device_status(ws.data_ptr()) == 0
+    assert (ws[size:] == 0xa5).all()

@@ -7,6 +7,7 @@ import pytest
 
 from confidence_driven_speculative_gb300 import _build, binding
 from oracle import tree as ot
+from tests.test_attn_abi import FAKE, valid
 from tests.test_tree_abi import EINVAL, EWORKSPACE, pages
 
 
@@ -45,3 +46,36 @@ def test_oracle_a_last_page_that_is_missing_is_told():
     assert granted.tolist() == [20, 20, 20, 40, 40]
     assert out.tolist() == [[2, -1, 0, -1], [5, -1, 1, -1], [2, -1, -1, -1], [2, 3, 4, -1], [-1, -1, 6, -1]]
     assert totals.tolist() == [5, 0]
+
+
+HEADS = [(32, 8, 128), (8, 8, 64), (40, 1, 128), (128, 1, 64), (15, 3, 128)]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", HEADS)
+def test_an_attention_workspace_of_more_rows_serves_fewer(lib, Hq, Hkv, D):
+    sizes = [binding.dspark_attn_workspace_size(Hq, Hkv, D, q) for q in range(1, 66)]
+    assert sizes == sorted(sizes)
+    # the checks that come after the workspace's: a missing cache, missing keys
+    a = dict(Hq=Hq, Hkv=Hkv, D=D, k_cache=None, k_rot=None, workspace_bytes=sizes[-1])
+    for q_max in range(1, 66):
+        for f in (lambda x: lib.dspark_step_attention(x, None), lambda x: lib.dspark_prompt_attention(x, None),
+                  lambda x: lib.dspark_step_attention_sinks(x, 4, None),
+                  lambda x: lib.dspark_prompt_attention_sinks(x, 4, None),
+                  lambda x: lib.dspark_step_attention_tree(x, FAKE, 4, None)):
+            assert f(ctypes.byref(valid(q_max=q_max, **a))) == EINVAL, q_max
+            assert "is NULL" in binding.last_error() or "outside [1, 64]" in binding.last_error()
+
+
+def test_chains_and_prompts_do_not_need_what_trees_need(lib):
+    """For 32 heads over 8 of 128 and 65 rows a chain's parts take 26 625 024 bytes; 64 rows of a tree take more."""
+    a = dict(Hq=32, Hkv=8, D=128, k_cache=None, k_rot=None, workspace_bytes=26625024)
+    for q_max in (40, 63, 64, 65):
+        for f in (lib.dspark_step_attention, lib.dspark_prompt_attention):
+            assert f(ctypes.byref(valid(q_max=q_max, **a)), None) == EINVAL
+            assert "is NULL" in binding.last_error()
+    assert lib.dspark_step_attention_tree(ctypes.byref(valid(q_max=64, **a)), FAKE, 0, None) == EWORKSPACE
+    # and prompts of any length need one size
+    small = binding.dspark_attn_workspace_size(32, 8, 128, 8192)
+    for q_max in (1, 30, 65, 66, 8192):
+        assert lib.dspark_prompt_attention(ctypes.byref(valid(**dict(a, q_max=q_max, workspace_bytes=small))), None) == EINVAL
+        assert "is NULL" in binding.last_error()
