@@ -880,7 +880,7 @@ dspark_status dspark_prompt_attention_sinks(const dspark_attn *a, int32_t sinks,
 
 size_t dspark_tree_workspace_size(int32_t B, int32_t rows, int32_t V) {
     if (B < 0 || B > DSPARK_MAX_B || rows < 0 || rows > DSPARK_MAX_ROWS || V < 1 || V > DSPARK_MAX_V) return 0;
-    return dspark::tree_workspace_bytes(B, rows, V);
+    return dspark::tree_workspace_bytes();
 }
 
 dspark_status dspark_verify_tree(const dspark_tree *t, dspark_stream_t stream) {
@@ -910,7 +910,7 @@ dspark_status dspark_verify_tree(const dspark_tree *t, dspark_stream_t stream) {
     REQUIRE_ALIGNED(t->target_logits, 16);
     if (t->V * dtype_size(t->logit_dtype) % 16)
         return fail(DSPARK_EALIGN, "%s: rows of V=%d logits are not a multiple of 16 bytes", fn, t->V);
-    if ((st = check_scratch(t->workspace, t->workspace_bytes, dspark::tree_workspace_bytes(t->B, t->rows, t->V), fn)))
+    if ((st = check_scratch(t->workspace, t->workspace_bytes, dspark::tree_workspace_bytes(), fn)))
         return st;
     DeviceInfo *dev;
     if ((st = device_info(&dev))) return st;

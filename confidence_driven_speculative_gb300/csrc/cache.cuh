@@ -9,7 +9,7 @@
 
 namespace dspark {
 
-size_t tree_workspace_bytes(int B, int rows, int V);
+size_t tree_workspace_bytes();
 cudaError_t launch_verify_tree(const dspark_tree &t, int sms, cudaStream_t s);
 
 cudaError_t launch_commit_path(const dspark_cache &c, int B, int q_max, int max_pages, const int32_t *block_table,

@@ -41,6 +41,7 @@ constexpr int kMaxCluster = 16;
 // seven in a row accepted, 6.0), 2 x 40 rows, 20.7 MB, 6.9 (6.0).
 constexpr size_t kAllBytes = size_t(18) << 20;
 constexpr int kAllRequests = 1024;  // and requests
+constexpr int kAllItems = 1280;     // and rows that they may have: B * q_max, 8 to an SM of 160
 constexpr int kLoadsAll = 8, kLoadsWalk = 4;  // 16-byte loads of a thread in flight to registers
 constexpr int kLaterWalk = 12;                // and to shared memory
 
@@ -49,7 +50,7 @@ struct TreeArgs {
     const void *logits;
     const int32_t *row_off, *parent, *ids;
     int32_t *accept_len, *num_emitted, *path, *out_tokens, *commit;
-    unsigned long long *key;  // [rows]: verify_tree_all_kernel, 0 between calls
+    unsigned long long *key;  // [B, q_max]: verify_tree_all_kernel, 0 between calls
     int32_t *done;            // [B]: parts read, 0 between calls
     int parts;                // of a row
 };
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(kThreadsAll) verify_tree_all_kernel(const Tree
     if (warp > 0) return;
     k = warp_max(lane < kThreadsAll / 32 ? keys[lane] : 0);
     if (lane == 0) {
-        atomicMax(A.key + r.row0 + j, k);
+        atomicMax(A.key + item, k);
         __threadfence();
         last = atomicAdd(A.done + b, 1) == r.n * A.parts - 1;
     }
@@ -282,8 +283,9 @@ __global__ void __launch_bounds__(kThreadsAll) verify_tree_all_kernel(const Tree
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if (32 * h + lane < r.n) {
-            best[h] = id_of(__ldcg(A.key + r.row0 + 32 * h + lane));
-            A.key[r.row0 + 32 * h + lane] = 0;  // as the next call wants it
+            Key *const at = A.key + b * A.q_max + 32 * h + lane;
+            best[h] = id_of(__ldcg(at));
+            *at = 0;  // as the next call wants it
         }
     }
     if (lane == 0) A.done[b] = 0;
@@ -297,16 +299,10 @@ __global__ void __launch_bounds__(kThreadsAll) verify_tree_all_kernel(const Tree
     walk.write(A, b, lane);
 }
 
-// Rows that are read at once, at most: what the workspace has room for.
-size_t all_rows(int B, int rows, int V) {
-    const size_t most = B <= kAllRequests ? kAllBytes / (size_t(V) * 2) : 0;
-    return size_t(rows) <= most ? size_t(rows) : 0;
-}
-
 template <typename T>
-cudaError_t launch(TreeArgs A, size_t together, int sms, cudaStream_t s) {
+cudaError_t launch(TreeArgs A, bool together, int sms, cudaStream_t s) {
     // all in one wave of CTAs
-    if (together && A.B * A.q_max <= 8 * sms) {
+    if (together && A.B * A.q_max <= std::min(8 * sms, kAllItems)) {
         A.parts = std::max(1, std::min(4 * sms / (A.B * A.q_max), A.V / 2048));
         return launch_overlapped(verify_tree_all_kernel<T>, A.B * A.q_max * A.parts, kThreadsAll, 0, s, A);
     }
@@ -323,21 +319,18 @@ cudaError_t launch(TreeArgs A, size_t together, int sms, cudaStream_t s) {
 
 }  // namespace
 
-// The workspace: status; parts done by request; keys by row.
-size_t tree_workspace_bytes(int B, int rows, int V) {
-    const size_t n = all_rows(B, rows, V);
-    return n ? 256 + align256(sizeof(int32_t) * size_t(B)) + align256(sizeof(Key) * n) : 256;
-}
+// The workspace: status; parts done by request; keys by request and row.  As large for every shape, so that one serves all.
+constexpr size_t kDoneAt = 256, kKeysAt = kDoneAt + sizeof(int32_t) * kAllRequests;
+size_t tree_workspace_bytes() { return kKeysAt + sizeof(Key) * kAllItems; }
 
 cudaError_t launch_verify_tree(const dspark_tree &t, int sms, cudaStream_t s) {
     char *ws = static_cast<char *>(t.workspace);
     const bool bf16 = t.logit_dtype == DSPARK_BF16;
-    const size_t n = all_rows(t.B, t.rows, t.V), bytes = size_t(t.rows) * t.V * (bf16 ? 2 : 4);
+    const size_t bytes = size_t(t.rows) * t.V * (bf16 ? 2 : 4);
     const TreeArgs A{t.B, t.rows, t.q_max, t.V, t.target_logits, t.row_off, t.parent, t.packed_ids,
                      t.accept_len, t.num_emitted, t.path, t.out_tokens, t.seq_lens_commit,
-                     reinterpret_cast<Key *>(ws + 256 + align256(sizeof(int32_t) * size_t(t.B))),
-                     reinterpret_cast<int32_t *>(ws + 256), 1};
-    const size_t together = bytes <= kAllBytes ? n : 0;
+                     reinterpret_cast<Key *>(ws + kKeysAt), reinterpret_cast<int32_t *>(ws + kDoneAt), 1};
+    const bool together = t.rows > 0 && t.B <= kAllRequests && bytes <= kAllBytes;
     return bf16 ? launch<uint16_t>(A, together, sms, s) : launch<float>(A, together, sms, s);
 }
 

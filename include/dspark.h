@@ -542,11 +542,12 @@ typedef struct dspark_tree {
 
     /* ---- scratch --------------------------------------------------------- */
     void *workspace;        /* dspark_tree_workspace_size() bytes, under the workspace
-                               convention: one of the largest size serves every shape */
+                               convention: one serves every shape */
     size_t workspace_bytes;
 } dspark_tree;
 
-/* Bytes of workspace that dspark_verify_tree needs.  0 outside the limits. */
+/* Bytes of workspace that dspark_verify_tree needs, the same for every shape.
+ * 0 outside the limits. */
 size_t dspark_tree_workspace_size(int32_t B, int32_t rows, int32_t V);
 
 /*

@@ -6,6 +6,7 @@ import torch
 from confidence_driven_speculative_gb300 import binding
 from tests.test_gpu_attention_sinks import Prompt, Step
 from tests.test_gpu_step_attention_tree import Tree
+from tests import test_gpu_verify_tree as verify
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +34,21 @@ def test_attention_calls_on_a_workspace_of_65_rows(cuda_lib):
             assert np.array_equal(c.call(), w)
     assert binding.dspark_read_device_status(ws.data_ptr()) == 0
     assert (ws[size:] == 0xa5).all()
+
+
+@pytest.mark.parametrize("largest", [(1024, 4096, 1024), (1025, 70000, 1024), (64, 4096, 129280)])
+def test_tree_verifies_on_a_workspace_of_the_largest_batch(cuda_lib, largest):
+    """Few rows read at once and many walked, in turn: keys and counters are back at zero after each."""
+    size = binding.dspark_tree_workspace_size(*largest)
+    ws = workspace(size)
+    cases = [verify.Case(30 + i, n, V, dtype) for i, (n, V, dtype) in enumerate((
+        ([30], 4096, torch.bfloat16), ([3, 5, 0, 64, 9], 1024, torch.float32), ([1] * 1020, 64, torch.bfloat16),
+        ([20] * 60, 1024, torch.bfloat16), ([2] * 600, 64, torch.float32), ([64, 1], 512, torch.bfloat16),
+        ([1] * 1200, 64, torch.bfloat16)))]
+    handles = [c.handle() for c in cases]
+    for _ in range(2):
+        for c, h in zip(cases, handles):
+            h.tree.workspace, h.tree.workspace_bytes = ws.data_ptr(), size
+            c.commit = h._keep["seq_lens_commit"]
+            c.check(h)
+    assert (ws[size:] == 0xa5).all() and (ws[:size] == 0).all()

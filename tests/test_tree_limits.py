@@ -8,7 +8,7 @@ import pytest
 from confidence_driven_speculative_gb300 import _build, binding
 from oracle import tree as ot
 from tests.test_attn_abi import FAKE, valid
-from tests.test_tree_abi import EINVAL, EWORKSPACE, pages
+from tests.test_tree_abi import EINVAL, EWORKSPACE, pages, tree
 
 
 @pytest.fixture(scope="module")
@@ -79,3 +79,18 @@ def test_chains_and_prompts_do_not_need_what_trees_need(lib):
     for q_max in (1, 30, 65, 66, 8192):
         assert lib.dspark_prompt_attention(ctypes.byref(valid(**dict(a, q_max=q_max, workspace_bytes=small))), None) == EINVAL
         assert "is NULL" in binding.last_error()
+
+
+def test_a_tree_workspace_of_the_largest_batch_serves_smaller_ones(lib):
+    """A program sizes its workspace for the most requests, rows and ids that it will see."""
+    shapes = [(1, 1, 8), (1, 64, 129280), (1, 74, 129280), (8, 512, 129280), (1024, 4096, 1024), (1025, 4096, 1024),
+              (65536, 1 << 24, 1024), (64, 4096, 1 << 24)]
+    sizes = {s: binding.dspark_tree_workspace_size(*s) for s in shapes}
+    for big in shapes:
+        for small in shapes:
+            if all(x <= y for x, y in zip(small, big)):
+                assert sizes[small] <= sizes[big], (small, big)
+    for B, rows, V in shapes:  # what the call asks for is what the size says
+        t = tree(B=B, rows=rows, V=V, workspace_bytes=sizes[B, rows, V] - 1)
+        assert lib.dspark_verify_tree(ctypes.byref(t), None) == EWORKSPACE
+        assert f"needs {sizes[B, rows, V]}" in binding.last_error()
