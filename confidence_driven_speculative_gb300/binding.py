@@ -668,13 +668,17 @@ class AttnBuffers:
         return dspark_read_device_status(self.workspace.data_ptr(), stream)
 
 
-def tree_rows(parent, row_off, seq_lens=None):
+def tree_rows(parent, row_off, seq_lens=None, window: int = 0, sinks: int = 0):
     """What the rows of trees see and where they sit, from ``parent`` and ``row_off`` (as in
     :class:`DsparkTree`; int32 tensors of one device, row_off[B] rows at most DSPARK_MAX_TREE_ROWS a
     request): (row_seen int64 [rows], packed_pos int32 [rows], row_req int32 [rows]), the rows past
-    row_off[B] as padding.  Set-up in torch operations without a host round trip: once where the
-    trees' shape is fixed, else once a step."""
+    row_off[B] as padding.  ``window`` and ``sinks``: of the layer that row_seen is for; a row does not
+    see the ancestors that its window has left, but for those at positions below ``sinks`` (with a window
+    of 64 or more, or none, it sees them all).  Set-up in torch operations without a host round trip: once
+    where the trees' shape is fixed, else once a step."""
     import torch
+    if window < 0 or sinks < 0:
+        raise ValueError(f"window={window}, sinks={sinks}: neither is < 0")
     rows, dev = parent.shape[0], parent.device
     off = row_off.long()
     r = torch.arange(rows, device=dev)
@@ -687,12 +691,26 @@ def tree_rows(parent, row_off, seq_lens=None):
     one = torch.ones((), dtype=torch.int64, device=dev)
     seen = torch.where(pad, 0, one << j.clamp(0, 63))
     depth = (p >= 0).long()
-    up = torch.where(p >= 0, off[req] + p, r)
+    up, ups = torch.where(p >= 0, off[req] + p, r), []
     for _ in range(6):  # ancestors by doubling: 64 rows are at most 63 deep
         seen = seen | seen[up]
         depth = depth + torch.where(up != r, depth[up], 0)
+        ups.append(up)
         up = up[up]
-    pos = depth if seq_lens is None else depth + seq_lens.long()[req]
+    start = 0 if seq_lens is None else seq_lens.long()[req]
+    if 0 < window < 64:
+        def above(at, steps):
+            for k in range(6):
+                at = torch.where(steps >> k & 1 > 0, ups[k][at], at)
+            return at
+        left = depth >= window  # the first ancestor that the window has left, and those above it
+        first = above(r, torch.where(left, window, 0))
+        near = seen & ~seen[first]
+        if sinks > 0:  # of which the sinks are seen again
+            last = torch.minimum(depth[first], sinks - 1 - start + torch.zeros_like(depth))
+            near = near | torch.where(last >= 0, seen[above(first, (depth[first] - last).clamp(0, 63))], 0)
+        seen = torch.where(left, near, seen)
+    pos = depth + start
     return (seen, torch.where(pad, 0, pos).to(torch.int32), torch.where(pad, -1, req).to(torch.int32))
 
 

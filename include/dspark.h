@@ -503,7 +503,11 @@ dspark_status dspark_rope_append_tree(const dspark_attn *attn, dspark_stream_t s
  *   - of the rows' own entries seq_lens[b] + i, i < the request's rows: those
  *     whose bit i of row_seen[r] is set, whatever the window.
  * For a tree, row_seen[r] holds the row itself and its ancestors; any other
- * set is as good, and a row that sees nothing gives zeros.
+ * set is as good, and a row that sees nothing gives zeros.  Where a layer's
+ * window is shorter than a tree is deep, the bits of the ancestors that it has
+ * left (at packed_pos[r] - window or in front of that, and at sinks or behind)
+ * are not set: then a chain of drafts has the result of
+ * dspark_step_attention_sinks.
  *
  * row_seen: device uint64 [rows], 8-byte aligned.  packed_pos is read where
  * window > 0 (values below seq_lens[b] count as seq_lens[b]).  q_max:

@@ -4,6 +4,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from confidence_driven_speculative_gb300 import _build, binding
 from oracle import tree as ot
@@ -94,3 +95,44 @@ def test_a_tree_workspace_of_the_largest_batch_serves_smaller_ones(lib):
         t = tree(B=B, rows=rows, V=V, workspace_bytes=sizes[B, rows, V] - 1)
         assert lib.dspark_verify_tree(ctypes.byref(t), None) == EWORKSPACE
         assert f"needs {sizes[B, rows, V]}" in binding.last_error()
+
+
+@pytest.mark.parametrize("window", [1, 2, 3, 8, 31, 32, 63, 64, 100])
+@pytest.mark.parametrize("sinks", [0, 1, 4, 20, 1 << 30])
+@pytest.mark.parametrize("lens", [True, False])
+def test_tree_rows_within_a_window(window, sinks, lens):
+    """A row sees the ancestors that the same tokens in a chain would see: those inside its window, and sinks."""
+    rng = np.random.default_rng(window + sinks)
+    n = [64, 0, 64, 17, 40]
+    off = np.concatenate([[0], np.cumsum(n)])
+    rows = int(off[-1]) + 2
+    parent = np.full(rows, 5, np.int32)
+    for b, deep in enumerate((1.0, 0.0, 0.9, 1.0, 0.3)):
+        for j in range(n[b]):
+            parent[off[b] + j] = j - 1 if rng.random() < deep else rng.integers(-1, max(j, 1))
+    start = rng.integers(0, 12, 5) if lens else np.zeros(5, int)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    args = (i32(parent), i32(off), i32(start) if lens else None)
+    seen, pos, req = binding.tree_rows(*args, window=window, sinks=sinks)
+    full = binding.tree_rows(*args)
+    assert torch.equal(pos, full[1]) and torch.equal(req, full[2])
+    cut = 0
+    for b in range(5):
+        for j in range(n[b]):
+            at, up = j, [j]
+            while at > 0 and 0 <= parent[off[b] + at] < at:
+                at = int(parent[off[b] + at])
+                up.append(at)
+            here = start[b] + len(up) - 1
+            word = sum(1 << a for d, a in enumerate(up) if d < window or here - d < sinks)
+            assert int(seen[off[b] + j]) % (1 << 64) == word, (b, j)
+            cut += word != int(full[0][off[b] + j]) % (1 << 64)
+    assert window < 64 or cut == 0
+    assert cut > 0 or start[0] + 63 - window < sinks  # the last row of the chain of 64 has left what is no sink
+    assert (seen[off[-1]:] == 0).all()
+
+
+def test_tree_rows_refuses_a_negative_window():
+    for kw in (dict(window=-1), dict(window=4, sinks=-1)):
+        with pytest.raises(ValueError, match="neither is < 0"):
+            binding.tree_rows(torch.zeros(3, dtype=torch.int32), torch.tensor([0, 3], dtype=torch.int32), **kw)
