@@ -811,10 +811,15 @@ class PageBuffers:
         p.workspace, p.workspace_bytes = self.workspace.data_ptr(), self.ws_bytes
         self._keep = {"cache": cache}
 
-    def bind(self, table_in, keep_len, want_len, parent=None, first_pos=None, held=None) -> "PageBuffers":
+    def bind(self, table_in, keep_len, want_len, parent=None, first_pos=None, held=None,
+             table_out=None) -> "PageBuffers":
         """Point the struct at device int32 tensors: table_in [B_in, max_pages]; keep_len, want_len,
-        parent, first_pos [B]; held [num_pages]."""
+        parent, first_pos [B]; held [num_pages].  table_out [B, max_pages]: in place of the buffers' own,
+        for two tables in turn; it stays as it is where it is left out."""
         p = self.pages
+        if table_out is not None:
+            _device_array(table_out, "table_out", "int32", p.B * p.max_pages)
+            self.table_out, p.table_out = table_out, _ptr(table_out)
         for name, t, n in (("table_in", table_in, p.B_in * p.max_pages), ("keep_len", keep_len, p.B),
                            ("want_len", want_len, p.B)):
             _device_array(t, name, "int32", n)
