@@ -966,7 +966,11 @@ dspark_status dspark_update_pages(const dspark_pages *p, dspark_stream_t stream)
     REQUIRE(p->tail_src);
     REQUIRE(p->tail_dst);
     REQUIRE(p->totals);
-    if (p->table_in == p->table_out) return fail(DSPARK_EINVAL, "%s: table_out is table_in", fn);
+    // rows of table_out are written while others read theirs of table_in
+    const uintptr_t in = reinterpret_cast<uintptr_t>(p->table_in), out = reinterpret_cast<uintptr_t>(p->table_out);
+    const uint64_t row = sizeof(int32_t) * uint64_t(p->max_pages);
+    if (p->B_in > 0 && in < out + p->B * row && out < in + p->B_in * row)
+        return fail(DSPARK_EINVAL, "%s: table_out overlaps table_in", fn);
     if ((st = check_scratch(p->workspace, p->workspace_bytes,
                             dspark::pages_workspace_bytes(p->B, p->cache.num_pages), fn)))
         return st;

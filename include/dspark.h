@@ -634,7 +634,7 @@ typedef struct dspark_pages {
                                  out and not written, whoever else names them */
 
     /* ---- outputs (device, caller-allocated) ------------------------------ */
-    int32_t *table_out;   /* [B, max_pages], apart from table_in; -1 where there is no page */
+    int32_t *table_out;   /* [B, max_pages], no part of it in table_in; -1 where there is no page */
     int32_t *granted_len; /* [B] want_len, or the first position to be written that has no
                              memory: where pages ran out, or where the parent's row has none
                              for the page that keep_len lies inside */

@@ -22,7 +22,7 @@ def lib():
 def test_pages_of_more_entries_than_32_bits_count(lib, B, max_pages, page):
     """Ranks of wanted pages are 32-bit sums over the table's entries."""
     assert B * max_pages > 2 ** 31 - 1
-    kw = dict(B=B, page_size=page, workspace_bytes=binding.dspark_pages_workspace_size(B, 64))
+    kw = dict(B=B, page_size=page, table_out=1 << 45, workspace_bytes=binding.dspark_pages_workspace_size(B, 64))
     assert lib.dspark_update_pages(ctypes.byref(pages(max_pages=max_pages, **kw)), None) == EINVAL
     assert "too large a batch" in binding.last_error()
     kw["workspace_bytes"] = 8  # as many columns as the limit allows: the next check speaks
@@ -137,3 +137,14 @@ def test_tree_rows_refuses_a_negative_window():
     for kw in (dict(window=-1), dict(window=4, sinks=-1)):
         with pytest.raises(ValueError, match="neither is < 0"):
             binding.tree_rows(torch.zeros(3, dtype=torch.int32), torch.tensor([0, 3], dtype=torch.int32), **kw)
+
+
+def test_tables_that_overlap_are_refused(lib):
+    """Rows of table_out are written while other requests read theirs of table_in; 4 and 6 rows of 8 columns."""
+    f = lambda at: lib.dspark_update_pages(ctypes.byref(pages(  # noqa: E731
+        B=6, table_in=FAKE, table_out=FAKE + at, workspace_bytes=8)), None)
+    for at in (-6 * 32 + 4, -32, 0, 32, 4 * 32 - 4):
+        assert f(at) == EINVAL, at
+        assert "overlaps" in binding.last_error()
+    for at in (-6 * 32, 4 * 32):  # side by side: the next check speaks
+        assert f(at) == EWORKSPACE, at
