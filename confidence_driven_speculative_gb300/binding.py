@@ -328,7 +328,7 @@ def dspark_commit_path(cache: DsparkCache, block_table, seq_lens, path, stream=N
         raise ValueError(f"block_table must be [{B}, n], got {tuple(block_table.shape)}")
     lens = None
     if seq_lens is not None:
-        if seq_lens.dtype is not _INT32 or seq_lens.numel() != B or not seq_lens.is_cuda or not seq_lens.is_contiguous():
+        if getattr(seq_lens, "dtype", None) is not _INT32 or seq_lens.numel() != B or not seq_lens.is_cuda or not seq_lens.is_contiguous():
             _device_array(seq_lens, "seq_lens", "int32", B)
         lens = seq_lens.data_ptr()
     rc = load().dspark_commit_path(ctypes.byref(cache), B, q_max, max_pages, block_table.data_ptr(), lens,

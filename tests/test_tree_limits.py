@@ -8,8 +8,8 @@ import torch
 
 from confidence_driven_speculative_gb300 import _build, binding
 from oracle import tree as ot
-from tests.test_attn_abi import FAKE, valid
-from tests.test_tree_abi import EINVAL, EWORKSPACE, pages, tree
+from tests.test_attn_abi import FAKE, fake, valid
+from tests.test_tree_abi import EINVAL, EWORKSPACE, cache, pages, tree
 
 
 @pytest.fixture(scope="module")
@@ -148,3 +148,12 @@ def test_tables_that_overlap_are_refused(lib):
         assert "overlaps" in binding.last_error()
     for at in (-6 * 32, 4 * 32):  # side by side: the next check speaks
         assert f(at) == EWORKSPACE, at
+
+
+def test_commit_path_says_what_is_wrong_with_lengths(lib):
+    table, path = fake(4, 8, dtype=torch.int32), fake(4, 9, dtype=torch.int32)
+    for bad, what in (([1, 2, 3, 4], "torch tensor"), (np.zeros(4, np.int32), "torch tensor"), (7, "torch tensor"),
+                      (fake(4, dtype=torch.int64), "int32"), (fake(5, dtype=torch.int32), "4 elements"),
+                      (torch.zeros(4, dtype=torch.int32), "CUDA")):
+        with pytest.raises(ValueError, match=what):
+            binding.dspark_commit_path(cache(), table, bad, path)
