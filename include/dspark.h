@@ -561,9 +561,11 @@ size_t dspark_tree_workspace_size(int32_t B, int32_t rows, int32_t V);
  * row; the walk ends where there is none, and emits y of its last row.
  *
  * This is the greedy rule.  For sampling at a temperature Tm, hand in
- * logits / Tm plus independent standard Gumbel noise: y_j is then a draw from
+ * logits / Tm plus independent standard Gumbel noise, added and kept in
+ * float32 (logit_dtype DSPARK_F32): y_j is then a draw from
  * softmax(logits / Tm), and the tokens of the walk are those of sampling one
- * by one.
+ * by one.  In bfloat16 they are not: its steps are coarse next to the noise,
+ * and the ties that they make go to the lowest id.
  *
  * Rows that no walk comes to may be left unread.
  */
