@@ -697,7 +697,7 @@ def tree_rows(parent, row_off, seq_lens=None, window: int = 0, sinks: int = 0):
         depth = depth + torch.where(up != r, depth[up], 0)
         ups.append(up)
         up = up[up]
-    start = 0 if seq_lens is None else seq_lens.long()[req]
+    start = 0 if seq_lens is None or off.shape[0] < 2 else seq_lens.long()[req]
     if 0 < window < 64:
         def above(at, steps):
             for k in range(6):

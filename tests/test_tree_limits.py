@@ -157,3 +157,13 @@ def test_commit_path_says_what_is_wrong_with_lengths(lib):
                       (torch.zeros(4, dtype=torch.int32), "CUDA")):
         with pytest.raises(ValueError, match=what):
             binding.dspark_commit_path(cache(), table, bad, path)
+
+
+@pytest.mark.parametrize("window", [0, 3])
+def test_tree_rows_of_no_requests(window):
+    """A batch of padding: nothing is looked up in the lengths, of which there are none."""
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    for rows in ((), (0, 0, 0)):
+        for off, lens in ((i32(0), i32()), (i32(0, 0), i32(5)), (i32(0), None)):
+            seen, pos, req = binding.tree_rows(i32(*rows), off, lens, window, 2)
+            assert (seen == 0).all() and (pos == 0).all() and (req == -1).all() and len(seen) == len(rows)
