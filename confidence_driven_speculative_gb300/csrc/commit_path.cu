@@ -72,8 +72,7 @@ __global__ void __launch_bounds__(kThreadsCommit, kLayers == 2 ? 5 : 6) commit_p
         if (tid == 0) moves = n;
     }
     __syncthreads();
-    // Many moves go past L2 (256 requests in 16 layers 12.7 us, without 14.1), a few are not worth it (one request
-    // in 32 layers 3.1, without 2.9).
+    // Many moves go past L2, few do not: see launch_commit_path.
     auto load = [](const uint16_t *p) {
         const uint4 *const x = reinterpret_cast<const uint4 *>(p);
         return kLayers == 2 ? __ldcs(x) : *x;
@@ -112,10 +111,12 @@ __global__ void __launch_bounds__(kThreadsCommit, kLayers == 2 ? 5 : 6) commit_p
 
 cudaError_t launch_commit_path(const dspark_cache &c, int B, int q_max, int max_pages, const int32_t *block_table,
                                const int32_t *seq_lens, const int32_t *path, int sms, cudaStream_t s) {
-    // Two layers to a CTA, whose path and pages are looked up once, where there are CTAs enough: 48 requests in 32
-    // layers 6.6 us (one layer to a CTA 6.0), 64 in 32 7.7 (7.9), 256 in 16 13.7 (15.2), all before loads
-    // and stores were streaming ones.
-    const bool two = int64_t(B) * c.layers > 12 * sms;
+    // Where there are CTAs enough, two layers to one, whose path and pages are looked up once, and the moves go past
+    // L2; else a CTA a layer, and moves that stay in L2.  Requests in layers, microseconds of both and (of the two
+    // that this rule never takes) of two layers through L2 and one past it: 4 in 32 3.1 against 2.6 (2.7, 3.0), 64 in
+    // 32 7.0 against 6.2 (6.5, 6.6), 80 in 32 7.3 against 7.0, 128 in 18 8.0 against 8.4, 160 in 16 8.4 against 9.5, 96
+    // in 32 9.4 against 10.6 (10.0, 9.8), 256 in 16 11.4 against 14.7 (13.1, 12.5), 256 in 32 20.5 against 25.8.
+    const bool two = int64_t(B) * c.layers > 16 * sms;
     const int groups = two ? (c.layers + 1) / 2 : c.layers;
     const CommitArgs A{B, q_max, max_pages, c.layers, groups, c.Hkv, c.D / 8, c.page_size, c.num_pages,
                        c.layer_stride, c.page_stride, c.slot_stride, c.head_stride,
