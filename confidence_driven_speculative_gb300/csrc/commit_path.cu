@@ -9,8 +9,9 @@
 //
 // Bound: bytes, each moved entry read and written once.  256 requests in 16
 // layers of 8 heads of 128, 1.9 moves each, 12.8 us (a copy of as many bytes 9.2:
-// the moves are pieces of 2 KB, and three trips come first); one request 2.9, a launch
-// and three trips to memory, path to page to entry.
+// the moves are pieces of 2 KB, and three trips come first); one request 2.9 in a
+// captured graph, a launch and three trips to memory, path to page to entry, and 5.1 to
+// 5.8 by plain calls, which the host's part bounds.
 #include <algorithm>
 
 #include "cache.cuh"

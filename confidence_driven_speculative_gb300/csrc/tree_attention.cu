@@ -48,7 +48,8 @@ constexpr int kTileOne = 2, kTileTwo = 3, kUnitPlaces = 10;
 // Up to so many tiles a CTA all units have one block: the two blocks of a request then go to different CTAs, which
 // read the same keys but have half as many columns to write out and to add up.  Trees of 60 rows, 8 cached heads,
 // one block and two: 1 request of 4095 keys (1.7 tiles a CTA) 18.5 us and 22.2, 8 of 1000 (3.8) 27.2 and 29.4,
-// 4 of 4095 (6.9) 34.9 and 36.0, 1 of 16 000 (6.6) 31.4 and 29.5, 12 of 2000 (10.4) 49.5 and 44.0.
+// 4 of 4095 (6.9) 34.9 and 36.0, 1 of 16 000 (6.6) 31.4 and 29.5, 12 of 2000 (10.4) 49.5 and 44.0.  (Near the border
+// the requests' number decides as well, by a few percent either way.)
 constexpr int kFewTiles = 6;
 
 // A unit that was cut, for the second kernel.
