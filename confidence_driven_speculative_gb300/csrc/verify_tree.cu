@@ -16,7 +16,7 @@
 // flight at once counts: most loads go through shared memory (cp.async), each to
 // a place that only its own thread reads, and leave the registers to more CTAs
 // (seven an SM with 4 + 12 loads a thread; 16 to registers in four 28.0 us against
-// 22.9 to 24.6 for 128 requests of 129280 ids, 77.5 against 57.8 for 400, 17.2 against
+// 22.9 to 24.7 for 128 requests of 129280 ids, 77.5 against 57.8 for 400, 17.2 against
 // 18.5 for 64; the walks' own rows take 11.4 at a copy's rate).
 //
 // Few rows are read all at once (verify_tree_all_kernel): every CTA
