@@ -52,3 +52,15 @@ def test_tree_verifies_on_a_workspace_of_the_largest_batch(cuda_lib, largest):
             c.commit = h._keep["seq_lens_commit"]
             c.check(h)
     assert (ws[size:] == 0xa5).all() and (ws[:size] == 0).all()
+
+
+def test_short_prompts_on_a_workspace_of_long_ones(cuda_lib):
+    size = binding.dspark_attn_workspace_size(8, 2, 128, 8192)
+    ws = workspace(size)
+    for n in ([30, 5, 17], [64], [65, 1], [66, 300]):
+        c = Prompt(6, 4, n, Hq=8, Hkv=2, D=128, window=20)
+        want = c.call()
+        c.h.attn.workspace, c.h.attn.workspace_bytes = ws.data_ptr(), size
+        for _ in range(2):
+            assert np.array_equal(c.call(), want)
+    assert (ws[size:] == 0xa5).all()
